@@ -10,6 +10,15 @@ every call raises.
 
     o, lse = attention_forward(q, k, v, causal=True)
     dq, dk, dv = attention_backward(q, k, v, o, lse, do, causal=True)
+
+Training with rotary positions, and serving from a paged cache (paged.py):
+
+    rotary = Rotary(inv_freq, sections=(16, 24, 24))
+    q, k = rotary_forward(q, k, positions, rotary)
+    cache = PagedCache(k_pages, v_pages)
+    batch = PagedBatch(block_table, q_start, kv_len, max_q_len)
+    q = paged_append(cache, batch, k, v, rotary, positions, q)
+    o, lse = paged_attention(cache, batch, q)
 """
 
 import ctypes
@@ -21,7 +30,9 @@ __all__ = [
     "FaError", "fa_forward", "fa_forward_ex", "fa_forward_fp8", "fa_set_forward_tile_rows", "fa_forward_tile_rows_for",
     "fa_backward", "fa_backward_deterministic", "fa_backward_preprocess", "fa_status_string",
     "fa_last_device_error", "fa_selftest_wait_timeout", "fa_set_backward_events", "attention_forward", "attention_backward",
-    "library",
+    "library", "Rotary", "PagedCache", "PagedBatch", "fa_rotary", "fa_rotary_backward",
+    "fa_paged_append", "fa_forward_paged", "paged_workspace", "rotary_forward", "rotary_backward",
+    "paged_append", "paged_attention",
 ]
 
 FA_OK = 0
@@ -29,6 +40,7 @@ FA_ERR_INVALID_ARGUMENT = 1
 FA_ERR_UNSUPPORTED = 2
 FA_ERR_CUDA = 3
 FA_ERR_DEVICE_TIMEOUT = 4
+FA_ERR_BAD_PAGE = 5
 
 
 # torch is imported on first use; the current-stream handle is read with
@@ -249,3 +261,8 @@ def attention_backward(q, k, v, o, lse, do, causal=False, scale=None, determinis
     run = fa_backward_deterministic if deterministic else fa_backward
     run(q, k, v, o, lse, do, dq, dk, dv, scale, causal, stream)
     return dq, dk, dv
+
+
+from .paged import (PagedBatch, PagedCache, Rotary, fa_forward_paged, fa_paged_append,  # noqa: E402
+                    fa_rotary, fa_rotary_backward, paged_append, paged_attention,
+                    paged_workspace, rotary_backward, rotary_forward)

@@ -16,7 +16,40 @@ _STATUS = {
     2: "unsupported head dimension",
     3: "CUDA runtime error",
     4: "a bounded wait inside a kernel ran out",
+    5: "a length or page index outside the block table or cache",
 }
+
+
+class RotarySpec(ctypes.Structure):
+    """fa_rotary_spec of include/fa.h."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("axes", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("axis", ctypes.c_ubyte * 128)]
+
+
+class RotaryRows(ctypes.Structure):
+    """fa_rotary_rows of include/fa.h."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("in_batch", ctypes.c_longlong), ("in_head", ctypes.c_longlong),
+                ("in_pos", ctypes.c_longlong), ("out_batch", ctypes.c_longlong),
+                ("out_head", ctypes.c_longlong), ("out_pos", ctypes.c_longlong),
+                ("heads", ctypes.c_int)]
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """fa_paged_cache of include/fa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("row_stride", ctypes.c_longlong), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("H_kv", ctypes.c_int), ("d", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("k_descale", ctypes.c_float),
+                ("v_descale", ctypes.c_float)]
+
+
+class PagedBatchStruct(ctypes.Structure):
+    """fa_paged_batch of include/fa.h."""
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong),
+                ("max_pages", ctypes.c_int), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("S", ctypes.c_int), ("max_q_len", ctypes.c_int)]
 
 
 class FaError(RuntimeError):
@@ -51,6 +84,18 @@ def _declare(lib):
     lib.fa_backward_noalloc.argtypes = [p, p, p, p, p, p, p, p, p, i, i, i, i, i, f, i, p]
     lib.fa_backward_preprocess.restype = i
     lib.fa_backward_preprocess.argtypes = [p, p, p, ll, i, p]
+    for name in ("fa_rotary", "fa_rotary_backward"):
+        fn = getattr(lib, name)
+        fn.restype = i
+        fn.argtypes = [p, p, i, i, i, p, ll, ll, p, p]
+    lib.fa_paged_append.restype = i
+    lib.fa_paged_append.argtypes = [p, p, p, ll, ll, p, ll, ll, i, p, ll, ll, p, ll, ll, i, p, p,
+                                    ll, p]
+    lib.fa_forward_paged.restype = i
+    lib.fa_forward_paged.argtypes = [p, p, p, ll, ll, p, ll, ll, p, i, i, f, i, p,
+                                     ctypes.c_size_t, p]
+    lib.fa_forward_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.fa_forward_paged_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_status_string.argtypes = [i]
     lib.fa_last_device_error.restype = i

@@ -190,6 +190,22 @@ bool encode_map_bf16(CUtensorMap* m, const void* ptr, int d, int N, long long pl
   return make_map_bf16(m, ptr, d, N, planes);
 }
 
+bool encode_map_pages(CUtensorMap* m, const fa_paged_cache& c, const void* pages, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t elem = c.dtype == FA_CACHE_BF16 ? 2 : 1;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.d) * elem, static_cast<cuuint64_t>(c.page_size),
+                        static_cast<cuuint64_t>(c.H_kv), static_cast<cuuint64_t>(c.n_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.row_stride) * elem,
+                           static_cast<cuuint64_t>(c.head_stride) * elem,
+                           static_cast<cuuint64_t>(c.page_stride) * elem};
+  cuuint32_t box[4] = {128, static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pages), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_map_f32_acc(CUtensorMap* m, const void* ptr, int d, int N, long long planes) {
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ptr, d, N, planes, 32, 128,
                   CU_TENSOR_MAP_SWIZZLE_128B);
@@ -325,6 +341,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_UNSUPPORTED: return "unsupported head dimension";
     case FA_ERR_CUDA: return "CUDA runtime error";
     case FA_ERR_DEVICE_TIMEOUT: return "a bounded wait inside a kernel ran out";
+    case FA_ERR_BAD_PAGE: return "a length or page index outside the block table or cache";
   }
   return "unknown status";
 }
@@ -342,7 +359,7 @@ fa_status fa_last_device_error(cudaStream_t stream) {
   if (cudaMemsetAsync(err, 0, sizeof(word), stream) != cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess)
     return FA_ERR_CUDA;
-  return FA_ERR_DEVICE_TIMEOUT;
+  return (word & ~fa::kErrBadPage) != 0 ? FA_ERR_DEVICE_TIMEOUT : FA_ERR_BAD_PAGE;
 }
 
 fa_status fa_set_forward_tile_rows(int rows) {

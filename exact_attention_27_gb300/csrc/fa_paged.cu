@@ -1,0 +1,790 @@
+// Attention of new tokens over a paged cache for few rows a sequence (single
+// tokens, short drafts): bound by the bytes of K and V.
+//
+// An item is 16 RW rows (tokens x grouped query heads) of one sequence and
+// key/value head; fa_paged.cuh says how the key tiles of all items are divided
+// among the CTAs.  Per key tile of 64 keys a producer warp copies K and V into
+// a ring of shared memory, one box per page and 128-byte column block, and
+// 4 RW warps take 16 keys of 16 rows each, with their own running maximum, sum
+// and O in registers, so that they meet only at the end of an item:
+//     S = Q K^T;  m' = max(m, max S);  p = 2^(S - m');
+//     l = l 2^(m - m') + sum p;  O = O 2^(m - m') + p V.
+// m moves only when it has grown by more than 8 (log2), which bounds p by 2^8
+// and leaves O / l as it is.  At the end the four key groups join (O, m, l)
+// through shared memory.
+//
+// Why mma.sync here: 16 rows fill an eighth of a tcgen05 tile, and at 7 TB/s an
+// SM gets 23 bytes a cycle, 12 bf16 values, which the 16-row products use up at
+// under a quarter of the rate of the warp-level instruction.  What counts is
+// bytes in flight: two CTAs an SM with 96 KB of ring each.
+//
+// bf16 cache: P is rounded to bf16 (2^-9 relative) for P V, as in fa_forward;
+// l sums the unrounded fp32 values.  e4m3 cache: K and V convert to fp16
+// exactly, P is rounded to fp16 (2^-12), and each row of Q is scaled by a power
+// of two to a largest element in [2^7, 2^8), so that its bf16 values fit fp16
+// (what falls below fp16's range is 2^-33 of the row's largest); the power is
+// taken out of the scale of the row's scores.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "fa_internal.h"
+#include "fa_paged.cuh"
+#include "fa_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr float kRescaleThreshold = 8.0f;
+constexpr int kTK = 64;  // keys per tile
+
+template <int D_, bool E4M3_, int RW_>
+struct RowsCfg {
+  static constexpr int D = D_;
+  static constexpr bool E4M3 = E4M3_;
+  static constexpr int RW = RW_;         // groups of 16 rows
+  static constexpr int ROWS = 16 * RW;
+  static constexpr int WARPS = 4 * RW;   // consumers
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int SUB = (D * (E4M3 ? 1 : 2) + 127) / 128;  // 128-byte column blocks
+  static constexpr int BLOCK = kTK * 128;
+  static constexpr int STAGE = 2 * SUB * BLOCK;                 // K and V
+  static constexpr int MERGE = 2 * ROWS * D * 4;                // two of the four key groups' O
+  static constexpr int OCC = RW == 1 && D <= 128 ? 2 : 1;       // CTAs an SM
+  static constexpr int BUDGET = (OCC == 2 ? 112 : 224) * 1024;
+  // At d = 256 the fragments of Q (64 registers) lie in shared memory.
+  static constexpr bool QS = D == 256;
+  static constexpr int QBYTES = QS ? RW * 16 * D * 2 : 0;
+  static constexpr int FIT = (BUDGET - MERGE - QBYTES - 3072) / STAGE;
+  static constexpr int NS = FIT > 8 ? 8 : FIT;
+  static constexpr int OFF_MERGE = NS * STAGE;
+  static constexpr int OFF_Q = OFF_MERGE + MERGE;               // [RW][D / 16][32 lanes] fragments
+  static constexpr int OFF_ML = OFF_Q + QBYTES;                 // [RW][4][16] (m, l)
+  static constexpr int OFF_SCR = OFF_ML + RW * 4 * 16 * 8;
+  static constexpr int OFF_BAR = OFF_SCR + 40 * 8;
+  static constexpr int OFF_MISC = OFF_BAR + 2 * NS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static_assert(NS >= 2 && SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two e4m3 values (the low half of `v`) as packed fp16, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(v)));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Barrier among the four warps of a row group.
+__device__ __forceinline__ void group_sync(int rw) {
+  asm volatile("bar.sync %0, 128;" ::"r"(rw + 1) : "memory");
+}
+
+template <int D, bool E4M3, int RW>
+__global__ void __launch_bounds__(RowsCfg<D, E4M3, RW>::THREADS, RowsCfg<D, E4M3, RW>::OCC)
+    fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+  using C = RowsCfg<D, E4M3, RW>;
+  using Walk = PagedWalk<C::ROWS, kTK>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto full = [&](int st) -> uint32_t { return sbase + C::OFF_BAR + 8 * st; };
+  auto empty = [&](int st) -> uint32_t { return sbase + C::OFF_BAR + 8 * (C::NS + st); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < C::NS; ++st) {
+      mbar_init(full(st), 1);
+      mbar_init(empty(st), C::WARPS);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == C::WARPS && elect_one()) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const PagedRange range = paged_range<C::ROWS, kTK, C::THREADS>(
+      p, reinterpret_cast<long long*>(smem + C::OFF_SCR));
+  __syncthreads();
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) p.notes[cta].last = -1;
+  if (range.end <= range.first) return;  // block-uniform, no copies in flight
+
+  Walk w;
+  int t = w.start(p, range.seq, range.rem);
+  long long unit = range.first;
+
+  if (warp == C::WARPS) {
+    // ------------------------------------------------------------ producer
+    const int page = 1 << p.page_shift;
+    const int box_rows = min(page, kTK);
+    const int boxes_k = kTK / box_rows * C::SUB;
+    // This lane's box: K or V, which rows of the tile, which column block.
+    const bool mine = lane < 2 * boxes_k;
+    const int is_v = lane >= boxes_k;
+    const int in_k = lane - is_v * boxes_k;
+    const int row0 = in_k / C::SUB * box_rows, sub = in_k % C::SUB;
+    const uint32_t dst0 = sbase + (is_v * C::SUB + sub) * C::BLOCK + row0 * 128;
+    int n = 0;  // tiles issued
+    bool ok = true;
+    while (ok && unit < range.end) {
+      const int keys = w.my_keys(p);
+      const int t_end = static_cast<int>(min(static_cast<long long>(w.my_tiles(p)),
+                                             t + (range.end - unit)));
+      unit += t_end - t;
+      for (; t < t_end; ++t, ++n) {
+        const int st = n % C::NS;
+        const int key0 = t * kTK + row0;
+        bool issue = mine && key0 < keys;
+        int id = 0;
+        if (issue) {
+          id = p.table[w.s * p.table_stride + (key0 >> p.page_shift)];
+          if (id < 0 || id >= p.n_pages) {
+            atomicOr(p.err, kErrBadPage);
+            issue = false;
+          }
+        }
+        if (n >= C::NS)
+          ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((n / C::NS) - 1) & 1, abort_flag,
+                                                 p.err, kErrTimeoutLoad));
+        if (!ok) break;
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
+        if (lane == 0) mbar_arrive_expect_tx(full(st), boxes * box_rows * 128);
+        __syncwarp();
+        if (issue)
+          tma_load_4d(dst0 + st * C::STAGE, is_v ? &tmV : &tmK, full(st), sub * 128,
+                      key0 & (page - 1), w.h, id);
+      }
+      t = 0;
+      if (unit < range.end) w.next(p);
+    }
+    // On the abort path the copies already issued land before the CTA's memory is released.
+    if (*abort_flag)
+      for (int i = max(0, n - C::NS); i < n; ++i)
+        mbar_wait_timed(full(i % C::NS), (i / C::NS) & 1);
+  } else {
+    // ------------------------------------------------------------ consumers
+    const int kg = warp & 3, rw = warp >> 2;
+    const int g = lane >> 2, c = lane & 3;  // row (and row + 8), column quad of the fragments
+    constexpr int NT = D / 8;               // 8-column tiles of O
+    float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE) + rw * 2 * 16 * D;
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML) + rw * 4 * 16;
+    uint4* qs = reinterpret_cast<uint4*>(smem + C::OFF_Q) + rw * (D / 16) * 32;
+    int n = 0;
+    bool ok = true;
+    while (unit < range.end) {
+      const int tiles = w.my_tiles(p);
+      const int keys = w.my_keys(p);
+      const int t_begin = t;
+      const int t_end =
+          static_cast<int>(min(static_cast<long long>(tiles), t + (range.end - unit)));
+      const long long unit0 = unit;
+      unit += t_end - t;
+      const int rows = w.g.qlen * p.G;
+      const int r0 = w.rt * C::ROWS + rw * 16;  // this warp's first row
+      // Rows r0 + g and r0 + g + 8: token, query head, last key seen.
+      int tok[2], head[2], last[2];
+      bool live[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + g + 8 * i;
+        live[i] = r < rows;
+        tok[i] = live[i] ? r / p.G : 0;
+        head[i] = w.h * p.G + (live[i] ? r - tok[i] * p.G : 0);
+        last[i] = p.causal ? w.g.klen - w.g.qlen + tok[i] : w.g.klen - 1;
+      }
+      // Keys up to here are seen by every row of the tile.
+      const int all_see = p.causal ? w.g.klen - w.g.qlen + w.rt * C::ROWS / p.G : w.g.klen - 1;
+      // Q fragments, from global memory (rows past the sequence: zeros).  For
+      // e4m3, K is read 8 bytes a lane, which fixes the order of the columns.
+      uint32_t qf[D / 16][4];
+      float cs[2] = {p.scale_log2, p.scale_log2};
+      {
+        const __nv_bfloat16* src[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          src[i] = p.q + (w.g.q0 + tok[i]) * p.q_token + head[i] * p.q_head;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int i = x & 1;
+            const int col = E4M3 ? kk / 2 * 32 + 8 * c + (kk & 1) * 4 + (x >> 1) * 2
+                                 : kk * 16 + 2 * c + (x >> 1) * 8;
+            qf[kk][x] = live[i] ? *reinterpret_cast<const uint32_t*>(src[i] + col) : 0u;
+          }
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+              for (int x = i; x < 4; x += 2)
+                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(qf[kk][x] << 16)),
+                                     fabsf(__uint_as_float(qf[kk][x] & 0xffff0000u))));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            // 2^e with e = 7 - exponent of the largest, within fp32's range.
+            int e = 134 - static_cast<int>(__float_as_uint(mx) >> 23);
+            if (mx == 0.0f || !(mx < INFINITY)) e = 0;
+            e = min(max(e, -120), 120);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            cs[i] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+              for (int x = i; x < 4; x += 2)
+                qf[kk][x] = pack_f16x2(__uint_as_float(qf[kk][x] << 16) * up,
+                                       __uint_as_float(qf[kk][x] & 0xffff0000u) * up);
+          }
+        }
+      }
+      if constexpr (C::QS) {
+        if (kg == 0) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            qs[kk * 32 + lane] = make_uint4(qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3]);
+        }
+        group_sync(rw);
+      }
+      auto q_frag = [&](int kk, uint32_t (&a)[4]) {
+        if constexpr (C::QS) {
+          const uint4 v = qs[kk * 32 + lane];
+          a[0] = v.x;
+          a[1] = v.y;
+          a[2] = v.z;
+          a[3] = v.w;
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) a[x] = qf[kk][x];
+        }
+      };
+      float o[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[i][x] = 0.0f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+      for (; t < t_end; ++t, ++n) {
+        const int st = n % C::NS;
+        // Warp-uniform.  After a timeout the warp still goes through every
+        // item's barriers, without work.
+        if (ok)
+          ok = __all_sync(0xffffffffu, mbar_wait(full(st), (n / C::NS) & 1, abort_flag, p.err,
+                                                 kErrTimeoutSoftmax));
+        if (!ok) continue;
+        const int key0 = t * kTK + kg * 16;  // this warp's first key
+        if (key0 < keys) {
+          const uint32_t sk = sbase + st * C::STAGE, sv = sk + C::SUB * C::BLOCK;
+          // S: two 8-key tiles.
+          float s[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[i][x] = 0.0f;
+          if constexpr (E4M3) {
+#pragma unroll
+            for (int k2 = 0; k2 < D / 32; ++k2) {
+              const int byte = k2 * 32 + 8 * c;
+              uint32_t a0[4], a1[4];
+              q_frag(2 * k2, a0);
+              q_frag(2 * k2 + 1, a1);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int row = kg * 16 + 8 * i + g;
+                const uint2 v = lds64(sk + (byte >> 7) * C::BLOCK + row * 128 +
+                                      ((((byte >> 4) & 7) ^ (row & 7)) << 4) + (byte & 8));
+                mma16816<true>(s[i], a0, e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16));
+                mma16816<true>(s[i], a1, e4m3x2_f16x2(v.y), e4m3x2_f16x2(v.y >> 16));
+              }
+            }
+          } else {
+            const int row = kg * 16 + (lane >> 4) * 8 + (lane & 7);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const int chunk = kk * 2 + ((lane >> 3) & 1);
+              uint32_t a[4], b[4];
+              q_frag(kk, a);
+              ldsm4(sk + (chunk >> 3) * C::BLOCK + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), b);
+              mma16816<false>(s[0], a, b[0], b[1]);
+              mma16816<false>(s[1], a, b[2], b[3]);
+            }
+          }
+          if (key0 + 15 > all_see) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (key0 + 8 * i + 2 * c + (x & 1) > last[x >> 1]) s[i][x] = -INFINITY;
+          }
+          // Running maximum and sum of rows g (x = 0, 1) and g + 8 (x = 2, 3).
+          float alpha[2];
+          bool upd = false;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]),
+                             fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * cs[i];
+            alpha[i] = 1.0f;
+            if (mx > m[i] + kRescaleThreshold) {
+              alpha[i] = ex2_approx(m[i] - mx);
+              m[i] = mx;
+              upd = true;
+            }
+            const float ref = m[i] == -INFINITY ? 0.0f : m[i];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int x = 2 * i; x < 2 * i + 2; ++x)
+                s[j][x] = ex2_approx(fmaf(s[j][x], cs[i], -ref));
+            l[i] = l[i] * alpha[i] + ((s[0][2 * i] + s[0][2 * i + 1]) +
+                                      (s[1][2 * i] + s[1][2 * i + 1]));
+          }
+          if (__any_sync(0xffffffffu, upd)) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              o[i][0] *= alpha[0];
+              o[i][1] *= alpha[0];
+              o[i][2] *= alpha[1];
+              o[i][3] *= alpha[1];
+            }
+          }
+          uint32_t pf[4];
+          if constexpr (E4M3) {
+            pf[0] = pack_f16x2(s[0][0], s[0][1]);
+            pf[1] = pack_f16x2(s[0][2], s[0][3]);
+            pf[2] = pack_f16x2(s[1][0], s[1][1]);
+            pf[3] = pack_f16x2(s[1][2], s[1][3]);
+          } else {
+            pf[0] = pack_bf16x2(s[0][0], s[0][1]);
+            pf[1] = pack_bf16x2(s[0][2], s[0][3]);
+            pf[2] = pack_bf16x2(s[1][0], s[1][1]);
+            pf[3] = pack_bf16x2(s[1][2], s[1][3]);
+          }
+          // O += P V.  Rows of V at and past `keys` (stale or never copied)
+          // have p = 0 but may hold anything, so they are made 0.
+          const bool tail = key0 + 16 > keys;
+          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+          if (tail) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int k = key0 + 8 * i + 2 * c;
+              keep[i] = (k < keys ? 0xffffu : 0u) | (k + 1 < keys ? 0xffff0000u : 0u);
+            }
+          }
+          if constexpr (E4M3) {
+            // A transposed fragment element is a pair of neighbouring columns
+            // of one key; the even and the odd columns form a tile each.
+            const int row = kg * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+            for (int d2 = 0; d2 < D / 32; ++d2) {
+              const int chunk = d2 * 2 + (lane >> 4);
+              uint32_t v[4];
+              ldsm4_trans(sv + (chunk >> 3) * C::BLOCK + row * 128 +
+                              (((chunk & 7) ^ (row & 7)) << 4), v);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t ev = __byte_perm(v[2 * i], v[2 * i + 1], 0x6420);
+                const uint32_t od = __byte_perm(v[2 * i], v[2 * i + 1], 0x7531);
+                uint32_t e0 = e4m3x2_f16x2(ev), e1 = e4m3x2_f16x2(ev >> 16);
+                uint32_t d0 = e4m3x2_f16x2(od), d1 = e4m3x2_f16x2(od >> 16);
+                if (tail) {
+                  e0 &= keep[0];
+                  e1 &= keep[1];
+                  d0 &= keep[0];
+                  d1 &= keep[1];
+                }
+                mma16816<true>(o[4 * d2 + 2 * i], pf, e0, e1);
+                mma16816<true>(o[4 * d2 + 2 * i + 1], pf, d0, d1);
+              }
+            }
+          } else {
+            const int row = kg * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+            for (int d2 = 0; d2 < D / 16; ++d2) {
+              const int chunk = d2 * 2 + (lane >> 4);
+              uint32_t v[4];
+              ldsm4_trans(sv + (chunk >> 3) * C::BLOCK + row * 128 +
+                              (((chunk & 7) ^ (row & 7)) << 4), v);
+              if (tail) {
+                v[0] &= keep[0];
+                v[1] &= keep[1];
+                v[2] &= keep[0];
+                v[3] &= keep[1];
+              }
+              mma16816<false>(o[2 * d2], pf, v[0], v[1]);
+              mma16816<false>(o[2 * d2 + 1], pf, v[2], v[3]);
+            }
+          }
+        }
+        mbar_arrive_warp(empty(st));
+      }
+      t = 0;
+
+      // ---------------------------------------------------------- end of the item
+      // The four key groups join: common maximum, then O of groups 2 and 3
+      // onto 0 and 1, then of 1 onto 0, in registers' order (lane-contiguous).
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if (c == 0) ml[kg * 16 + g + 8 * i] = make_float2(m[i], l[i]);
+      }
+      group_sync(rw);
+      float M[2], L[2], f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float2 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = ml[k * 16 + g + 8 * i];
+        M[i] = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
+        const float ref = M[i] == -INFINITY ? 0.0f : M[i];
+        L[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) L[i] += x[k].y * ex2_approx(x[k].x - ref);
+        f[i] = ex2_approx(m[i] - ref);
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[i][x] *= f[x >> 1];
+      if (kg >= 2) {
+#pragma unroll
+        for (int i = 0; i < NT * 4; ++i)
+          merge[(kg - 2) * 16 * D + i * 32 + lane] = o[i >> 2][i & 3];
+      }
+      group_sync(rw);
+      if (kg < 2) {
+#pragma unroll
+        for (int i = 0; i < NT * 4; ++i) {
+          o[i >> 2][i & 3] += merge[kg * 16 * D + i * 32 + lane];
+          if (kg == 1) merge[16 * D + i * 32 + lane] = o[i >> 2][i & 3];
+        }
+      }
+      group_sync(rw);
+      if (kg == 0 && ok) {
+        const bool whole = t_begin == 0 && t_end == tiles;
+        const int slot = cta * 2 + (t_begin == 0 ? 1 : 0);
+        float* po = p.part_o + (static_cast<long long>(slot) * C::ROWS + rw * 16) * D;
+        float2* pml = p.part_ml + static_cast<long long>(slot) * C::ROWS + rw * 16;
+#pragma unroll
+        for (int i = 0; i < NT * 4; ++i) o[i >> 2][i & 3] += merge[16 * D + i * 32 + lane];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!live[i]) continue;
+          const long long token = w.g.q0 + tok[i];
+          const float inv = L[i] > 0.0f ? p.v_scale / L[i] : 0.0f;
+          __nv_bfloat16* dst = p.o + token * p.o_token + head[i] * p.o_head;
+          float* pd = po + (g + 8 * i) * D;
+#pragma unroll
+          for (int nt = 0; nt < NT; nt += E4M3 ? 2 : 1) {
+            // The lane's columns: two, or for e4m3 four of an even and odd tile.
+            const float x0 = o[nt][2 * i], x1 = o[nt][2 * i + 1];
+            if constexpr (E4M3) {
+              const float y0 = o[nt + 1][2 * i], y1 = o[nt + 1][2 * i + 1];
+              const int col = nt / 2 * 16 + 4 * c;
+              if (whole)
+                *reinterpret_cast<uint2*>(dst + col) = make_uint2(
+                    pack_bf16x2(x0 * inv, y0 * inv), pack_bf16x2(x1 * inv, y1 * inv));
+              else
+                *reinterpret_cast<float4*>(pd + col) = make_float4(x0, y0, x1, y1);
+            } else {
+              const int col = nt * 8 + 2 * c;
+              if (whole)
+                *reinterpret_cast<uint32_t*>(dst + col) = pack_bf16x2(x0 * inv, x1 * inv);
+              else
+                *reinterpret_cast<float2*>(pd + col) = make_float2(x0, x1);
+            }
+          }
+          if (c == 0) {
+            if (!whole)
+              pml[g + 8 * i] = make_float2(M[i], L[i]);
+            else if (p.lse)
+              p.lse[token * p.Hq + head[i]] =
+                  L[i] > 0.0f ? (M[i] + log2f(L[i])) * kPagedLn2 : -INFINITY;
+          }
+        }
+        if (rw == 0 && lane == 0 && t_begin == 0 && t_end < tiles)
+          p.notes[cta] = paged_note<C::ROWS, kTK>(p, range, w, unit0);
+      }
+      if (unit < range.end) w.next(p);
+    }
+  }
+  __syncthreads();
+}
+
+// Joins the parts of the items that several CTAs share: block (c, y) those of
+// the item that starts in CTA c and is not finished there, rows y, y + gridDim.y,
+// ...  Groups of D / 4 threads take parts in turn, each with a running
+// maximum; the groups join through shared memory, always in the same order.
+constexpr int kJoinThreads = 256;
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const PagedParams p) {
+  constexpr int LANES = D / 4;
+  constexpr int GROUPS = kJoinThreads / LANES;
+  __shared__ float4 acc[GROUPS][LANES];
+  __shared__ float2 state[GROUPS];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int cta = blockIdx.x;
+  const PagedNote note = p.notes[cta];
+  if (note.last < 0) return;
+  const int rows = min(ROWS, note.rows - note.tile0);
+  const int grp = threadIdx.x / LANES, lane = threadIdx.x - grp * LANES;
+  const int parts = note.last - cta + 1;
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    float m = -INFINITY, l = 0.0f;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (grp < GROUPS) {
+#pragma unroll 4
+      for (int k = grp; k < parts; k += GROUPS) {
+        const long long slot = (static_cast<long long>(cta + k) * 2 + (k == 0)) * ROWS + row;
+        const float2 ml = p.part_ml[slot];
+        const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot * D + 4 * lane);
+        const float m_new = fmaxf(m, ml.x);
+        const float ref = m_new == -INFINITY ? 0.0f : m_new;
+        const float f = ex2_approx(m - ref), e = ex2_approx(ml.x - ref);
+        a.x = a.x * f + x.x * e;
+        a.y = a.y * f + x.y * e;
+        a.z = a.z * f + x.z * e;
+        a.w = a.w * f + x.w * e;
+        l = l * f + ml.y * e;
+        m = m_new;
+      }
+      acc[grp][lane] = a;
+      if (lane == 0) state[grp] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll 1
+      for (int k = 1; k < GROUPS; ++k) {
+        const float2 ml = state[k];
+        const float4 x = acc[k][lane];
+        const float m_new = fmaxf(m, ml.x);
+        const float ref = m_new == -INFINITY ? 0.0f : m_new;
+        const float f = ex2_approx(m - ref), e = ex2_approx(ml.x - ref);
+        a.x = a.x * f + x.x * e;
+        a.y = a.y * f + x.y * e;
+        a.z = a.z * f + x.z * e;
+        a.w = a.w * f + x.w * e;
+        l = l * f + ml.y * e;
+        m = m_new;
+      }
+      const int r = note.tile0 + row;
+      const int tok = r / p.G;
+      const long long token = note.q0 + tok;
+      const int head = note.head * p.G + (r - tok * p.G);
+      const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
+      *reinterpret_cast<uint2*>(p.o + token * p.o_token + head * p.o_head + 4 * lane) =
+          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+      if (lane == 0 && p.lse)
+        p.lse[token * p.Hq + head] = l > 0.0f ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
+    }
+    __syncthreads();
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+// CTAs of a launch with `rows` rows an item.
+int rows_ctas(int sms, int rows, int d) { return sms * (rows == 16 && d <= 128 ? 2 : 1); }
+
+// Rows an item: the step's largest row count, rounded up to what the kernel has.
+int rows_for(long long most) { return most <= 16 ? 16 : 32; }
+
+// Workspace: notes, (m, l), O; each part 256-byte aligned.
+struct PartLayout {
+  size_t ml, o, total;
+};
+PartLayout part_layout(int ctas, int rows, int d) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  PartLayout l;
+  l.ml = up(static_cast<size_t>(ctas) * sizeof(PagedNote));
+  l.o = l.ml + up(static_cast<size_t>(ctas) * 2 * rows * sizeof(float2));
+  l.total = l.o + static_cast<size_t>(ctas) * 2 * rows * d * sizeof(float);
+  return l;
+}
+
+template <int D, bool E4M3, int RW>
+cudaError_t launch_rows_t(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+                          int ctas, cudaStream_t stream) {
+  using C = RowsCfg<D, E4M3, RW>;
+  cudaError_t e = set_smem_limit_once<fa_paged_rows_kernel<D, E4M3, RW>>(C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(fa_paged_rows_kernel<D, E4M3, RW>, dim3(ctas), dim3(C::THREADS),
+                       C::SMEM_BYTES, stream, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(fa_paged_join_kernel<D, C::ROWS>, dim3(ctas, 4), dim3(kJoinThreads), 0,
+                          stream, p);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_rows_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+                          int rows, int ctas, cudaStream_t stream) {
+  if (rows == 16) return launch_rows_t<D, E4M3, 1>(tk, tv, p, ctas, stream);
+  return launch_rows_t<D, E4M3, 2>(tk, tv, p, ctas, stream);
+}
+
+template <bool E4M3>
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int d,
+                        int rows, int ctas, cudaStream_t stream) {
+  switch (d) {
+    case 64: return launch_rows_d<64, E4M3>(tk, tv, p, rows, ctas, stream);
+    case 96: return launch_rows_d<96, E4M3>(tk, tv, p, rows, ctas, stream);
+    case 128: return launch_rows_d<128, E4M3>(tk, tv, p, rows, ctas, stream);
+    case 256: return launch_rows_d<256, E4M3>(tk, tv, p, rows, ctas, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+size_t fa_forward_paged_workspace_bytes(int H_q, int H_kv, int d, int T, int max_q_len) {
+  using namespace fa;
+  if (H_q < 1 || H_kv < 1 || H_q % H_kv != 0 || T < 0 || max_q_len < 0) return 0;
+  if (d != 64 && d != 96 && d != 128 && d != 256) return 0;
+  const long long most = static_cast<long long>(std::min(T, max_q_len)) * (H_q / H_kv);
+  const int rows = rows_for(most);
+  return part_layout(rows_ctas(sm_count(), rows, d), rows, d).total;
+}
+
+fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* q,
+                           long long q_token, long long q_head, void* o, long long o_token,
+                           long long o_head, float* lse, int T, int H_q, float scale, int causal,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  using namespace fa;
+  const fa_status st = validate_cache(cache, batch, T);
+  if (st != FA_OK) return st;
+  const int d = cache->d, H = cache->H_kv;
+  if (H_q < 1 || H_q % H != 0) return FA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return FA_ERR_INVALID_ARGUMENT;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARGUMENT;
+  const float s_eff = scale * cache->k_descale;
+  if (!std::isfinite(s_eff) || !(s_eff > 0.0f)) return FA_ERR_INVALID_ARGUMENT;
+  if (static_cast<long long>(T) * H_q >= 0x7fffff00LL) return FA_ERR_INVALID_ARGUMENT;
+  if (T == 0 || batch->S == 0) return FA_OK;
+  if (!q || !o || !aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return FA_ERR_INVALID_ARGUMENT;
+  for (long long s : {q_token, q_head, o_token, o_head})
+    if (s < 0 || s % 8 != 0) return FA_ERR_INVALID_ARGUMENT;
+  if ((o_token == 0 && T > 1) || (o_head == 0 && H_q > 1)) return FA_ERR_INVALID_ARGUMENT;
+  const int sms = sm_count();
+  if (sms < 1) return FA_ERR_CUDA;
+  const int G = H_q / H;
+  const long long most = static_cast<long long>(std::min(T, batch->max_q_len)) * G;
+  const int rows = rows_for(most);
+  const int ctas = rows_ctas(sms, rows, d);
+  const PartLayout lay = part_layout(ctas, rows, d);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < lay.total)
+    return FA_ERR_INVALID_ARGUMENT;
+  PagedParams p{};
+  p.err = device_error_word();
+  if (!p.err) return FA_ERR_CUDA;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_token = q_token;
+  p.q_head = q_head;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.o_token = o_token;
+  p.o_head = o_head;
+  p.lse = lse;
+  p.table = batch->block_table;
+  p.table_stride = batch->table_stride;
+  p.q_start = batch->q_start;
+  p.kv_len = batch->kv_len;
+  p.S = batch->S;
+  p.T = T;
+  p.Hq = H_q;
+  p.Hkv = H;
+  p.G = G;
+  p.page_shift = 31 - __builtin_clz(cache->page_size);
+  p.max_pages = batch->max_pages;
+  p.n_pages = cache->n_pages;
+  p.causal = causal;
+  p.rows_min = 1;
+  p.rows_max = 0x7fffffff;
+  p.min_units = 1;
+  p.scale_log2 = s_eff * kPagedLog2e;
+  p.v_scale = cache->v_descale;
+  char* ws = static_cast<char*>(workspace);
+  p.notes = reinterpret_cast<PagedNote*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
+  p.part_o = reinterpret_cast<float*>(ws + lay.o);
+  CUtensorMap tk, tv;
+  const int box = std::min(cache->page_size, kTK);
+  if (!encode_map_pages(&tk, *cache, cache->k, box) || !encode_map_pages(&tv, *cache, cache->v, box))
+    return FA_ERR_CUDA;
+  const cudaError_t e = cache->dtype == FA_CACHE_E4M3
+                            ? launch_rows<true>(tk, tv, p, d, rows, ctas, stream)
+                            : launch_rows<false>(tk, tv, p, d, rows, ctas, stream);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

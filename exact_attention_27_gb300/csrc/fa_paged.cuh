@@ -1,0 +1,235 @@
+// Shared by the kernels of fa_forward_paged: the step's geometry, the division
+// of its key tiles among the CTAs, and the partial results of what is divided.
+//
+// Work is counted in units of one key tile of one item; an item is a tile of
+// ROWS query rows of one (sequence, key/value head), its rows being the
+// head's tokens x the G query heads that share it (row r: token r / G, head
+// r % G), so that grouped heads read K and V once.  Items stand in order of
+// sequence, head and row tile, and CTA c of C takes the units
+// [c U / C, (c + 1) U / C): every CTA the same number of key tiles, however
+// ragged the lengths, and a long sequence of few rows is spread over many.
+// Lengths live on the device, so every CTA works its own range out at its
+// start (one pass over q_start and kv_len by the whole block).
+//
+// An item inside one CTA is finished there.  The part of an item that a CTA
+// shares with others goes to the workspace as (O, m, l), unnormalised fp32:
+// slot 1 of the CTA where the item starts, slot 0 of each CTA that goes on
+// with it (a range has at most one of each), and a second kernel joins them in
+// CTA order, so results do not depend on timing.  The starting CTA leaves a
+// note of the item and of the last CTA that has a part.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+constexpr float kPagedLog2e = 1.4426950408889634f;
+constexpr float kPagedLn2 = 0.6931471805599453f;
+
+struct PagedNote {
+  int last;   // last CTA with a part of the item that starts here; -1: none
+  int q0;     // first token of the sequence
+  int rows;   // rows of the sequence (tokens x G)
+  int tile0;  // the item's first row
+  int head;   // key/value head
+  int pad[3];
+};
+
+struct PagedParams {
+  const __nv_bfloat16* q;
+  long long q_token, q_head;
+  __nv_bfloat16* o;
+  long long o_token, o_head;
+  float* lse;
+  const int* table;
+  long long table_stride;
+  const int* q_start;
+  const int* kv_len;
+  int S, T, Hq, Hkv, G;
+  int page_shift, max_pages, n_pages;
+  int causal;
+  int rows_min, rows_max;  // sequences whose row count lies outside are another kernel's
+  int min_units;           // units that are worth a CTA
+  float scale_log2;        // scale * log2(e) * k_descale
+  float v_scale;
+  float* part_o;           // [CTA][2][ROWS][D]
+  float2* part_ml;         // [CTA][2][ROWS]
+  PagedNote* notes;        // [CTA]
+  uint32_t* err;
+};
+
+struct PagedSeq {
+  int q0, qlen, klen;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int s) {
+  PagedSeq g;
+  g.q0 = min(max(p.q_start[s], 0), p.T);
+  g.qlen = min(max(p.q_start[s + 1], g.q0), p.T) - g.q0;
+  g.klen = min(max(p.kv_len[s], 0), p.max_pages << p.page_shift);
+  return g;
+}
+
+template <int ROWS, int TK>
+struct PagedWalk {
+  int s, h, rt, n_rt;
+  PagedSeq g;
+
+  static __device__ __forceinline__ int row_tiles(const PagedParams& p, const PagedSeq& g) {
+    const int rows = g.qlen * p.G;
+    return rows < p.rows_min || rows > p.rows_max ? 0 : (rows + ROWS - 1) / ROWS;
+  }
+  // Keys that the last row of row tile rt sees.
+  static __device__ __forceinline__ int keys(const PagedParams& p, const PagedSeq& g, int rt) {
+    if (!p.causal) return g.klen;
+    const int tokens = min(g.qlen, (rt * ROWS + ROWS - 1) / p.G + 1);
+    return max(g.klen - g.qlen + tokens, 0);
+  }
+  // Its key tiles: one at least, so that rows without keys are written too.
+  static __device__ __forceinline__ int tiles(const PagedParams& p, const PagedSeq& g, int rt) {
+    return max((keys(p, g, rt) + TK - 1) / TK, 1);
+  }
+  // Key tiles of one head of the sequence.
+  static __device__ __forceinline__ long long head_units(const PagedParams& p, const PagedSeq& g) {
+    const int n = row_tiles(p, g);
+    if (n == 0) return 0;
+    if (!p.causal) return static_cast<long long>(n) * tiles(p, g, 0);
+    long long u = 0;
+    for (int rt = 0; rt < n; ++rt) u += tiles(p, g, rt);
+    return u;
+  }
+
+  __device__ __forceinline__ int my_keys(const PagedParams& p) const { return keys(p, g, rt); }
+  __device__ __forceinline__ int my_tiles(const PagedParams& p) const { return tiles(p, g, rt); }
+
+  // Starts at unit `rem` of sequence s0; returns the key tile.
+  __device__ __forceinline__ int start(const PagedParams& p, int s0, long long rem) {
+    s = s0;
+    g = paged_seq(p, s);
+    n_rt = row_tiles(p, g);
+    const long long per_head = head_units(p, g);
+    h = static_cast<int>(rem / per_head);
+    rem -= h * per_head;
+    for (rt = 0; rt < n_rt - 1; ++rt) {
+      const int t = my_tiles(p);
+      if (rem < t) break;
+      rem -= t;
+    }
+    return static_cast<int>(rem);
+  }
+  __device__ __forceinline__ void next(const PagedParams& p) {
+    if (++rt < n_rt) return;
+    rt = 0;
+    if (++h < p.Hkv) return;
+    h = 0;
+    do {
+      if (++s >= p.S) return;  // (not reached while units are left)
+      g = paged_seq(p, s);
+      n_rt = row_tiles(p, g);
+    } while (n_rt == 0);
+  }
+};
+
+struct PagedRange {
+  long long units, first, end;  // all units; this CTA's
+  int ctas;                     // CTAs with units
+  int seq;                      // where `first` lies
+  long long rem;
+  // CTA whose range holds unit u.
+  __device__ __forceinline__ int owner(long long u) const {
+    return static_cast<int>(((u + 1) * ctas - 1) / units);
+  }
+};
+
+// Every thread of the block calls this; `scratch`: 40 long longs of shared memory.
+template <int ROWS, int TK, int THREADS>
+__device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long long* scratch) {
+  using Walk = PagedWalk<ROWS, TK>;
+  constexpr int WARPS = THREADS / 32;
+  static_assert(WARPS <= 32, "scratch");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Exclusive prefix of `mine` over the block; `all` gets the sum.
+  auto scan = [&](long long mine, long long& all) -> long long {
+    long long x = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    long long before = 0;
+    all = 0;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += scratch[w];
+      all += scratch[w];
+    }
+    __syncthreads();
+    return before + x - mine;
+  };
+  auto units_of = [&](int s) -> long long {
+    if (s >= p.S) return 0;
+    const PagedSeq g = paged_seq(p, s);
+    if (blockIdx.x == 0 && p.kv_len[s] > g.klen) atomicOr(p.err, kErrBadPage);
+    return Walk::head_units(p, g) * p.Hkv;
+  };
+  PagedRange r;
+  long long mine = units_of(tid), all;
+  long long pre = scan(mine, all);
+  r.units = all;
+  for (int base = THREADS; base < p.S; base += THREADS) {
+    scan(units_of(base + tid), all);
+    r.units += all;
+  }
+  r.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x),
+                                (r.units + p.min_units - 1) / p.min_units));
+  r.seq = 0;
+  r.rem = 0;
+  r.first = r.end = 0;
+  if (static_cast<int>(blockIdx.x) >= r.ctas) return r;  // block-uniform
+  r.first = blockIdx.x * r.units / r.ctas;
+  r.end = (blockIdx.x + 1) * r.units / r.ctas;
+  if (tid == 0) scratch[32] = scratch[33] = 0;
+  __syncthreads();
+  long long done = 0;
+  for (int base = 0; base < p.S; base += THREADS) {
+    if (base > 0) {
+      mine = units_of(base + tid);
+      pre = scan(mine, all);
+    } else if (p.S > THREADS) {
+      pre = scan(mine, all);
+    } else {
+      all = r.units;
+    }
+    if (r.first >= done + pre && r.first < done + pre + mine) {
+      scratch[32] = base + tid;
+      scratch[33] = r.first - done - pre;
+    }
+    __syncthreads();
+    if (r.first < done + all) break;
+    done += all;
+  }
+  r.seq = static_cast<int>(scratch[32]);
+  r.rem = scratch[33];
+  return r;
+}
+
+// What a CTA notes about the item that starts in its range and goes on past it.
+template <int ROWS, int TK>
+__device__ __forceinline__ PagedNote paged_note(const PagedParams& p, const PagedRange& r,
+                                                const PagedWalk<ROWS, TK>& w, long long unit0) {
+  PagedNote n{};
+  n.last = r.owner(unit0 + w.my_tiles(p) - 1);
+  n.q0 = w.g.q0;
+  n.rows = w.g.qlen * p.G;
+  n.tile0 = w.rt * ROWS;
+  n.head = w.h;
+  return n;
+}
+
+}  // namespace fa

@@ -42,6 +42,7 @@
 #define FA_H
 
 #include <cuda_runtime_api.h>
+#include <stddef.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -52,7 +53,8 @@ typedef enum {
   FA_ERR_INVALID_ARGUMENT = 1, /* null/misaligned pointer, bad size, bad scale */
   FA_ERR_UNSUPPORTED = 2,      /* head dimension d not supported by the call */
   FA_ERR_CUDA = 3,             /* a CUDA runtime call or launch failed */
-  FA_ERR_DEVICE_TIMEOUT = 4    /* a bounded wait inside a kernel ran out */
+  FA_ERR_DEVICE_TIMEOUT = 4,   /* a bounded wait inside a kernel ran out */
+  FA_ERR_BAD_PAGE = 5          /* a length or page index outside the table or cache */
 } fa_status;
 
 /*
@@ -256,6 +258,151 @@ fa_status fa_backward_noalloc(const void* q, const void* k, const void* v, const
 fa_status fa_backward_preprocess(const void* o, const void* dO, float* D, long long rows, int d,
                                  cudaStream_t stream);
 
+/* ---------------------------------------------------------------- rotary positions
+ *
+ * Rotary positions turn pairs of a head's values by an angle that grows with
+ * the position, so that q.k depends on the distance of two positions only.
+ * Pair p of a row is (x[p], x[p + rot_dim/2]), or (x[2p], x[2p + 1]) when
+ * `interleaved`; with a = positions[axis[p]] * inv_freq[p],
+ *     y_i = x_i cos a - x_j sin a,   y_j = x_i sin a + x_j cos a,
+ * and values at and past rot_dim are copied.  Text has one axis; images and
+ * video have one each for time, height and width, shared out over the pairs
+ * by `axis`.  The angle is reduced to a fraction of a turn in 64-bit integers,
+ * so far positions lose nothing; products and sums are fp32, and each output
+ * is rounded once.
+ */
+typedef struct {
+  const float* inv_freq;   /* device, [rot_dim / 2] fp32: radians per position */
+  int rot_dim;             /* values turned: a multiple of 16, at most d (and 256) */
+  int axes;                /* position axes, 1..4 */
+  int interleaved;         /* 0: pairs (p, p + rot_dim/2); 1: pairs (2p, 2p + 1) */
+  unsigned char axis[128]; /* axis of each pair, below `axes` */
+} fa_rotary_spec;
+
+/* One tensor to turn, [B][heads][N][d] bf16 through its strides (in elements;
+ * d contiguous; multiples of 8), 16-byte aligned.  Input strides may be 0
+ * (broadcast); out may be `in` with the same strides (in place), and must not
+ * overlap it otherwise.  Strides also describe [B][N][heads][d] and slices of
+ * a fused projection. */
+typedef struct {
+  const void* in;
+  void* out;
+  long long in_batch, in_head, in_pos;
+  long long out_batch, out_head, out_pos;
+  int heads;
+} fa_rotary_rows;
+
+/*
+ * Turns q and k (k may be NULL) by their positions, in one launch.
+ *   positions  device int32, entry (axis, b, n) at
+ *              positions[axis * axis_stride + b * batch_stride + n]; may be
+ *              negative; batch_stride 0 shares one row of positions
+ * d in {64, 96, 128, 256}; B, N, heads >= 1.  Returns as fa_forward.
+ */
+fa_status fa_rotary(const fa_rotary_rows* q, const fa_rotary_rows* k, int B, int N, int d,
+                    const int* positions, long long axis_stride, long long batch_stride,
+                    const fa_rotary_spec* spec, cudaStream_t stream);
+
+/*
+ * Gradient of fa_rotary: in = gradients of its outputs (the dq and dk of
+ * fa_backward), out = gradients of its inputs.  The turn is orthogonal, so
+ * this is the turn by -a:  dx_i = g_i cos a + g_j sin a,
+ * dx_j = -g_i sin a + g_j cos a.  Arguments and returns as fa_rotary.
+ */
+fa_status fa_rotary_backward(const fa_rotary_rows* q, const fa_rotary_rows* k, int B, int N, int d,
+                             const int* positions, long long axis_stride, long long batch_stride,
+                             const fa_rotary_spec* spec, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- paged key/value cache
+ *
+ * The keys and values of many sequences lie in pages of page_size positions,
+ * handed out in any order: position j of sequence s is row j % page_size of
+ * page block_table[s][j / page_size].  A step brings new tokens for some of
+ * the sequences: the rows q_start[s] .. q_start[s + 1] - 1 of the step's
+ * [T][heads][d] tensors belong to sequence s, whose length INCLUDING them is
+ * kv_len[s]; new token i sits at position kv_len - q_len + i.  Lengths, starts
+ * and tables are read on the device when the kernels run.
+ */
+#define FA_CACHE_BF16 0
+#define FA_CACHE_E4M3 1
+
+typedef struct {
+  void* k;                /* [n_pages][H_kv][page_size][d] through the strides below, */
+  void* v;                /* 16-byte aligned; bf16, or e4m3 times one factor a tensor */
+  long long page_stride;  /* in elements, d contiguous; each stride a multiple of 16 bytes */
+  long long head_stride;
+  long long row_stride;
+  int n_pages;
+  int page_size;          /* 16, 32, 64, 128 or 256 */
+  int H_kv;
+  int d;                  /* 64, 96, 128 or 256 */
+  int dtype;              /* FA_CACHE_BF16 or FA_CACHE_E4M3 */
+  float k_descale;        /* a stored e4m3 key stands for k * k_descale; finite, > 0; */
+  float v_descale;        /* 1 for bf16 */
+} fa_paged_cache;
+
+typedef struct {
+  const int* block_table;  /* device int32, row s at block_table + s * table_stride; entries */
+  long long table_stride;  /* past a sequence's length are not read */
+  int max_pages;           /* entries of a row */
+  const int* q_start;      /* device int32 [S + 1], not decreasing */
+  const int* kv_len;       /* device int32 [S] */
+  int S;                   /* sequences, >= 0 */
+  int max_q_len;           /* the most new tokens of one sequence: chooses the kernels, and a */
+                           /* wrong value costs time only */
+} fa_paged_batch;
+
+/*
+ * Appends the step's keys and values to the cache, the keys turned by their
+ * rotary positions on the way, in one launch; turns q as well where it is
+ * given (what fa_forward_paged reads next).
+ *   k, v   [T][H_kv][d] bf16 through token and head strides (elements,
+ *          multiples of 8), 16-byte aligned, read
+ *   q      [T][H_q][d] likewise, read; q_out written; both NULL: none.  q_out
+ *          may be q with the same strides.
+ *   spec   NULL: nothing is turned (q is copied)
+ *   positions  device int32, entry (axis, t) at positions[axis * axis_stride + t];
+ *          NULL: each token's place in its sequence, on every axis
+ * An e4m3 cache stores value / descale rounded once from fp32 (nearest even),
+ * saturated at 448.  Rows of k, v and q past q_start[S] belong to no sequence:
+ * nothing is written for them.  A token whose place lies before position 0, past
+ * the table's row or in a page outside the cache is not stored; the last two
+ * are reported by fa_last_device_error.  T = 0 or S = 0: FA_OK, nothing done.
+ */
+fa_status fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* k,
+                          long long k_token, long long k_head, const void* v, long long v_token,
+                          long long v_head, int T, const void* q, long long q_token,
+                          long long q_head, void* q_out, long long qo_token, long long qo_head,
+                          int H_q, const fa_rotary_spec* spec, const int* positions,
+                          long long axis_stride, cudaStream_t stream);
+
+/*
+ * Attention of the step's new tokens over the cache (which holds them already:
+ * fa_paged_append), from one token a sequence to long chunks, ragged.
+ *   q, o   [T][H_q][d] bf16 through token and head strides (elements,
+ *          multiples of 8), 16-byte aligned; H_q % H_kv == 0, query head h reads
+ *          key/value head h / (H_q / H_kv)
+ *   lse    [T][H_q] fp32 contiguous, as fa_forward's; NULL: not wanted
+ *   causal 1: new token i sees positions <= kv_len - q_len + i; 0: all kv_len.
+ *          A token that sees none gets o = 0 and lse = -infinity.
+ *   workspace  device memory of at least fa_forward_paged_workspace_bytes for
+ *          the same H_q, H_kv, d, T and max_q_len, 16-byte aligned; its
+ *          contents do not matter before or after.  Calls whose work can
+ *          overlap (other streams, other captured graphs) need one each.
+ * Positions past a sequence's length are never used, whatever their bits; the
+ * values at positions below it must be finite.  Rows of q past q_start[S] get
+ * no output.  A length past the table's row is cut to it, and a page outside
+ * the cache gives unspecified values for its sequence; both are reported by
+ * fa_last_device_error.  T = 0 or S = 0: FA_OK, nothing done.
+ */
+fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* q,
+                           long long q_token, long long q_head, void* o, long long o_token,
+                           long long o_head, float* lse, int T, int H_q, float scale, int causal,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace for fa_forward_paged on the current device; 0 for sizes it rejects. */
+size_t fa_forward_paged_workspace_bytes(int H_q, int H_kv, int d, int T, int max_q_len);
+
 /* Static, NUL-terminated description of a status code. */
 const char* fa_status_string(fa_status s);
 
@@ -263,7 +410,8 @@ const char* fa_status_string(fa_status s);
  * Synchronises `stream`, then reports what the kernels left behind: FA_ERR_CUDA
  * for a pending CUDA error, FA_ERR_DEVICE_TIMEOUT if a bounded wait inside a
  * kernel of this library ran out since the last call (the flag is then
- * cleared), FA_OK otherwise.  Every wait inside the kernels gives up after
+ * cleared), FA_ERR_BAD_PAGE if a paged call met a length past its table's row
+ * or a page outside its cache (likewise cleared), FA_OK otherwise.  Every wait inside the kernels gives up after
  * about a second instead of hanging; the kernel then skips its remaining work.
  */
 fa_status fa_last_device_error(cudaStream_t stream);
