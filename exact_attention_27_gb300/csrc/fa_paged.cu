@@ -35,6 +35,7 @@
 
 #include "fa_internal.h"
 #include "fa_paged.cuh"
+#include "fa_paged_launch.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
@@ -649,11 +650,12 @@ int sm_count() {
   return n;
 }
 
-// CTAs of a launch with `rows` rows an item.
-int rows_ctas(int sms, int rows, int d) { return sms * (rows == 16 && d <= 128 ? 2 : 1); }
+// Rows of an item, which says the kernel: sequences of at most 32 rows go 16 or
+// 32 rows an item to the kernel above, anything longer to the tile kernel.
+int rows_for(long long most) { return most <= 16 ? 16 : most <= 32 ? 32 : kPagedTileRows; }
 
-// Rows an item: the step's largest row count, rounded up to what the kernel has.
-int rows_for(long long most) { return most <= 16 ? 16 : 32; }
+// CTAs of a launch with `rows` rows an item.
+int ctas_for(int sms, int rows, int d) { return sms * (rows == 16 && d <= 128 ? 2 : 1); }
 
 // Workspace: notes, (m, l), O; each part 256-byte aligned.
 struct PartLayout {
@@ -674,18 +676,15 @@ cudaError_t launch_rows_t(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
   using C = RowsCfg<D, E4M3, RW>;
   cudaError_t e = set_smem_limit_once<fa_paged_rows_kernel<D, E4M3, RW>>(C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(fa_paged_rows_kernel<D, E4M3, RW>, dim3(ctas), dim3(C::THREADS),
-                       C::SMEM_BYTES, stream, tk, tv, p);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(fa_paged_join_kernel<D, C::ROWS>, dim3(ctas, 4), dim3(kJoinThreads), 0,
-                          stream, p);
+  return launch_dependent(fa_paged_rows_kernel<D, E4M3, RW>, dim3(ctas), dim3(C::THREADS),
+                          C::SMEM_BYTES, stream, tk, tv, p);
 }
 
 template <int D, bool E4M3>
 cudaError_t launch_rows_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
                           int rows, int ctas, cudaStream_t stream) {
-  if (rows == 16) return launch_rows_t<D, E4M3, 1>(tk, tv, p, ctas, stream);
-  return launch_rows_t<D, E4M3, 2>(tk, tv, p, ctas, stream);
+  return rows == 16 ? launch_rows_t<D, E4M3, 1>(tk, tv, p, ctas, stream)
+                    : launch_rows_t<D, E4M3, 2>(tk, tv, p, ctas, stream);
 }
 
 template <bool E4M3>
@@ -698,6 +697,16 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Page
     case 256: return launch_rows_d<256, E4M3>(tk, tv, p, rows, ctas, stream);
   }
   return cudaErrorInvalidValue;
+}
+
+template <int ROWS>
+cudaError_t launch_join(const PagedParams& p, int d, int ctas, cudaStream_t stream) {
+  auto kern = d == 64    ? fa_paged_join_kernel<64, ROWS>
+              : d == 96  ? fa_paged_join_kernel<96, ROWS>
+              : d == 128 ? fa_paged_join_kernel<128, ROWS>
+                         : fa_paged_join_kernel<256, ROWS>;
+  return launch_dependent(kern, dim3(ctas, ROWS / 8 < 4 ? 4 : ROWS / 8), dim3(kJoinThreads), 0,
+                          stream, p);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -713,7 +722,7 @@ size_t fa_forward_paged_workspace_bytes(int H_q, int H_kv, int d, int T, int max
   if (d != 64 && d != 96 && d != 128 && d != 256) return 0;
   const long long most = static_cast<long long>(std::min(T, max_q_len)) * (H_q / H_kv);
   const int rows = rows_for(most);
-  return part_layout(rows_ctas(sm_count(), rows, d), rows, d).total;
+  return part_layout(ctas_for(sm_count(), rows, d), rows, d).total;
 }
 
 fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* q,
@@ -741,7 +750,7 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   const int G = H_q / H;
   const long long most = static_cast<long long>(std::min(T, batch->max_q_len)) * G;
   const int rows = rows_for(most);
-  const int ctas = rows_ctas(sms, rows, d);
+  const int ctas = ctas_for(sms, rows, d);
   const PartLayout lay = part_layout(ctas, rows, d);
   if (!workspace || !aligned16(workspace) || workspace_bytes < lay.total)
     return FA_ERR_INVALID_ARGUMENT;
@@ -778,12 +787,18 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   p.part_o = reinterpret_cast<float*>(ws + lay.o);
   CUtensorMap tk, tv;
-  const int box = std::min(cache->page_size, kTK);
+  const bool tile = rows == kPagedTileRows;
+  const bool e4m3 = cache->dtype == FA_CACHE_E4M3;
+  const int box = std::min(cache->page_size, tile ? paged_tile_keys(d) : kTK);
   if (!encode_map_pages(&tk, *cache, cache->k, box) || !encode_map_pages(&tv, *cache, cache->v, box))
     return FA_ERR_CUDA;
-  const cudaError_t e = cache->dtype == FA_CACHE_E4M3
-                            ? launch_rows<true>(tk, tv, p, d, rows, ctas, stream)
-                            : launch_rows<false>(tk, tv, p, d, rows, ctas, stream);
+  cudaError_t e = tile   ? launch_paged_tile(tk, tv, p, d, e4m3, ctas, stream)
+                  : e4m3 ? launch_rows<true>(tk, tv, p, d, rows, ctas, stream)
+                         : launch_rows<false>(tk, tv, p, d, rows, ctas, stream);
+  if (e == cudaSuccess)
+    e = tile         ? launch_join<kPagedTileRows>(p, d, ctas, stream)
+        : rows == 32 ? launch_join<32>(p, d, ctas, stream)
+                     : launch_join<16>(p, d, ctas, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
