@@ -10,6 +10,7 @@
 
 #include "fa.h"
 #include "fa_internal.h"
+#include "fa_paged_host.h"
 #include "fa_ptx.cuh"
 
 namespace {

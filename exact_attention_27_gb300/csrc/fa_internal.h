@@ -106,10 +106,6 @@ fa_status validate_backward(const void* q, const void* k, const void* v, const v
                             const void* dv, int B, int H_q, int H_kv, int N, int d, float scale,
                             int causal);
 
-// Checks a paged cache, a step's batch and its number of tokens (fa_rotary.cu);
-// T = 0 or S = 0 needs no pointers.
-fa_status validate_cache(const fa_paged_cache* c, const fa_paged_batch* b, int T);
-
 // Whether the backward of head dimension d runs as two kernels (dK/dV, then
 // dQ walking the key tiles in order; no dQ accumulator): always when
 // `deterministic`, and at d = 256, whose only backward this is.
@@ -214,9 +210,6 @@ cudaError_t launch_backward_dq(const BwdMaps& m, const float* lse, const float* 
 uint32_t* device_error_word();
 bool encode_map_bf16(CUtensorMap* m, const void* ptr, int d, int N, long long planes);
 bool encode_map_f32_acc(CUtensorMap* m, const void* ptr, int d, int N, long long planes);
-// The pages (k or v) of a paged cache as bytes (d, row, head, page), boxes of
-// 128 bytes x box_rows rows, 128-byte swizzle.
-bool encode_map_pages(CUtensorMap* m, const fa_paged_cache& c, const void* pages, int box_rows);
 bool encode_map_f32_acc32(CUtensorMap* m, const void* ptr, int d, int N, long long planes);
 
 cudaError_t launch_dq_finalize(const float* dq_acc, void* dq, long long n, float scale,

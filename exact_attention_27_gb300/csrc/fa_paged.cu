@@ -35,7 +35,7 @@
 
 #include "fa_internal.h"
 #include "fa_paged.cuh"
-#include "fa_paged_launch.h"
+#include "fa_paged_host.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
@@ -108,19 +108,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Two e4m3 values (the low half of `v`) as packed fp16, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(v)));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // Barrier among the four warps of a row group.
@@ -570,14 +557,18 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, RW>::THREADS, RowsCfg<D, E4M3
   __syncthreads();
 }
 
-// Joins the parts of the items that several CTAs share: block (c, y) those of
-// the item that starts in CTA c and is not finished there, rows y, y + gridDim.y,
-// ...  Groups of D / 4 threads take parts in turn, each with a running
-// maximum; the groups join through shared memory, always in the same order.
+// Joins the parts of the items that several CTAs share: blocks (c, y) those of
+// the item that starts in CTA c and is not finished there.  A group of D / 4
+// threads runs over parts with a running maximum, four loads in flight.  Few
+// parts: each group has a row of its own.  Many (a long history and few rows):
+// the block's groups share a row's parts and join through shared memory.  Either
+// way the order is that of the CTAs.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinFew = 12;
 
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const PagedParams p) {
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    fa_paged_join_kernel(const PagedParams p, int tile_rows) {
   constexpr int LANES = D / 4;
   constexpr int GROUPS = kJoinThreads / LANES;
   __shared__ float4 acc[GROUPS][LANES];
@@ -587,56 +578,74 @@ __global__ void __launch_bounds__(kJoinThreads) fa_paged_join_kernel(const Paged
   const int cta = blockIdx.x;
   const PagedNote note = p.notes[cta];
   if (note.last < 0) return;
-  const int rows = min(ROWS, note.rows - note.tile0);
+  const int rows = min(tile_rows, note.rows - note.tile0);
   const int grp = threadIdx.x / LANES, lane = threadIdx.x - grp * LANES;
   const int parts = note.last - cta + 1;
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-    float m = -INFINITY, l = 0.0f;
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (grp < GROUPS) {
-#pragma unroll 4
-      for (int k = grp; k < parts; k += GROUPS) {
-        const long long slot = (static_cast<long long>(cta + k) * 2 + (k == 0)) * ROWS + row;
-        const float2 ml = p.part_ml[slot];
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot * D + 4 * lane);
-        const float m_new = fmaxf(m, ml.x);
-        const float ref = m_new == -INFINITY ? 0.0f : m_new;
-        const float f = ex2_approx(m - ref), e = ex2_approx(ml.x - ref);
-        a.x = a.x * f + x.x * e;
-        a.y = a.y * f + x.y * e;
-        a.z = a.z * f + x.z * e;
-        a.w = a.w * f + x.w * e;
-        l = l * f + ml.y * e;
-        m = m_new;
+  float m = -INFINITY, l = 0.0f;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](const float2& ml, const float4& x) {
+    const float m_new = fmaxf(m, ml.x);
+    const float ref = m_new == -INFINITY ? 0.0f : m_new;
+    const float f = ex2_approx(m - ref), e = ex2_approx(ml.x - ref);
+    a.x = a.x * f + x.x * e;
+    a.y = a.y * f + x.y * e;
+    a.z = a.z * f + x.z * e;
+    a.w = a.w * f + x.w * e;
+    l = l * f + ml.y * e;
+    m = m_new;
+  };
+  auto run = [&](int row, int k0, int step) {
+    m = -INFINITY;
+    l = 0.0f;
+    a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    constexpr int N = 4;
+    for (int k = k0; k < parts; k += N * step) {
+      float2 ml[N];
+      float4 x[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int part = k + i * step;
+        if (part < parts) {
+          const long long at =
+              (static_cast<long long>(cta + part) * 2 + (part == 0)) * tile_rows + row;
+          ml[i] = p.part_ml[at];
+          x[i] = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (k + i * step < parts) add(ml[i], x[i]);
+    }
+  };
+  auto store = [&](int row) {
+    const int r = note.tile0 + row;
+    const int tok = r / p.G;
+    const long long token = note.q0 + tok;
+    const int head = note.head * p.G + (r - tok * p.G);
+    const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
+    *reinterpret_cast<uint2*>(p.o + token * p.o_token + head * p.o_head + 4 * lane) =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    if (lane == 0 && p.lse)
+      p.lse[token * p.Hq + head] = l > 0.0f ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
+  };
+  if (parts <= kJoinFew) {
+    if (grp < GROUPS)
+      for (int row = blockIdx.y * GROUPS + grp; row < rows; row += gridDim.y * GROUPS) {
+        run(row, 0, 1);
+        store(row);
+      }
+    return;
+  }
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    if (grp < GROUPS) {
+      run(row, grp, GROUPS);
       acc[grp][lane] = a;
       if (lane == 0) state[grp] = make_float2(m, l);
     }
     __syncthreads();
     if (grp == 0) {
-#pragma unroll 1
-      for (int k = 1; k < GROUPS; ++k) {
-        const float2 ml = state[k];
-        const float4 x = acc[k][lane];
-        const float m_new = fmaxf(m, ml.x);
-        const float ref = m_new == -INFINITY ? 0.0f : m_new;
-        const float f = ex2_approx(m - ref), e = ex2_approx(ml.x - ref);
-        a.x = a.x * f + x.x * e;
-        a.y = a.y * f + x.y * e;
-        a.z = a.z * f + x.z * e;
-        a.w = a.w * f + x.w * e;
-        l = l * f + ml.y * e;
-        m = m_new;
-      }
-      const int r = note.tile0 + row;
-      const int tok = r / p.G;
-      const long long token = note.q0 + tok;
-      const int head = note.head * p.G + (r - tok * p.G);
-      const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
-      *reinterpret_cast<uint2*>(p.o + token * p.o_token + head * p.o_head + 4 * lane) =
-          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-      if (lane == 0 && p.lse)
-        p.lse[token * p.Hq + head] = l > 0.0f ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
+      for (int k = 1; k < GROUPS; ++k) add(state[k], acc[k][lane]);
+      store(row);
     }
     __syncthreads();
   }
@@ -651,8 +660,10 @@ int sm_count() {
 }
 
 // Rows of an item, which says the kernel: sequences of at most 32 rows go 16 or
-// 32 rows an item to the kernel above, anything longer to the tile kernel.
-int rows_for(long long most) { return most <= 16 ? 16 : most <= 32 ? 32 : kPagedTileRows; }
+// 32 rows an item to the kernel above, anything longer to the tcgen05 kernels.
+int rows_for(long long most, int d) {
+  return most <= 16 ? 16 : most <= 32 ? 32 : paged_tile_rows(d);
+}
 
 // CTAs of a launch with `rows` rows an item.
 int ctas_for(int sms, int rows, int d) { return sms * (rows == 16 && d <= 128 ? 2 : 1); }
@@ -699,14 +710,13 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Page
   return cudaErrorInvalidValue;
 }
 
-template <int ROWS>
-cudaError_t launch_join(const PagedParams& p, int d, int ctas, cudaStream_t stream) {
-  auto kern = d == 64    ? fa_paged_join_kernel<64, ROWS>
-              : d == 96  ? fa_paged_join_kernel<96, ROWS>
-              : d == 128 ? fa_paged_join_kernel<128, ROWS>
-                         : fa_paged_join_kernel<256, ROWS>;
-  return launch_dependent(kern, dim3(ctas, ROWS / 8 < 4 ? 4 : ROWS / 8), dim3(kJoinThreads), 0,
-                          stream, p);
+cudaError_t launch_join(const PagedParams& p, int rows, int d, int ctas, cudaStream_t stream) {
+  auto kern = d == 64    ? fa_paged_join_kernel<64>
+              : d == 96  ? fa_paged_join_kernel<96>
+              : d == 128 ? fa_paged_join_kernel<128>
+                         : fa_paged_join_kernel<256>;
+  return launch_dependent(kern, dim3(ctas, rows <= 32 ? 4 : 16), dim3(kJoinThreads), 0, stream, p,
+                          rows);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -721,7 +731,7 @@ size_t fa_forward_paged_workspace_bytes(int H_q, int H_kv, int d, int T, int max
   if (H_q < 1 || H_kv < 1 || H_q % H_kv != 0 || T < 0 || max_q_len < 0) return 0;
   if (d != 64 && d != 96 && d != 128 && d != 256) return 0;
   const long long most = static_cast<long long>(std::min(T, max_q_len)) * (H_q / H_kv);
-  const int rows = rows_for(most);
+  const int rows = rows_for(most, d);
   return part_layout(ctas_for(sm_count(), rows, d), rows, d).total;
 }
 
@@ -749,7 +759,7 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   if (sms < 1) return FA_ERR_CUDA;
   const int G = H_q / H;
   const long long most = static_cast<long long>(std::min(T, batch->max_q_len)) * G;
-  const int rows = rows_for(most);
+  const int rows = rows_for(most, d);
   const int ctas = ctas_for(sms, rows, d);
   const PartLayout lay = part_layout(ctas, rows, d);
   if (!workspace || !aligned16(workspace) || workspace_bytes < lay.total)
@@ -787,18 +797,16 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   p.part_o = reinterpret_cast<float*>(ws + lay.o);
   CUtensorMap tk, tv;
-  const bool tile = rows == kPagedTileRows;
+  const bool tile = rows > 32;
   const bool e4m3 = cache->dtype == FA_CACHE_E4M3;
   const int box = std::min(cache->page_size, tile ? paged_tile_keys(d) : kTK);
   if (!encode_map_pages(&tk, *cache, cache->k, box) || !encode_map_pages(&tv, *cache, cache->v, box))
     return FA_ERR_CUDA;
-  cudaError_t e = tile   ? launch_paged_tile(tk, tv, p, d, e4m3, ctas, stream)
+  cudaError_t e = tile   ? d == 256 ? launch_paged_tile(tk, tv, p, e4m3, ctas, stream)
+                                    : launch_paged_tile2(tk, tv, p, d, e4m3, ctas, stream)
                   : e4m3 ? launch_rows<true>(tk, tv, p, d, rows, ctas, stream)
                          : launch_rows<false>(tk, tv, p, d, rows, ctas, stream);
-  if (e == cudaSuccess)
-    e = tile         ? launch_join<kPagedTileRows>(p, d, ctas, stream)
-        : rows == 32 ? launch_join<32>(p, d, ctas, stream)
-                     : launch_join<16>(p, d, ctas, stream);
+  if (e == cudaSuccess) e = launch_join(p, rows, d, ctas, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

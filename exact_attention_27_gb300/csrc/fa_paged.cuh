@@ -24,9 +24,34 @@
 
 #include <cstdint>
 
+#include "fa_paged_host.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
+
+// 4-D tiled copy global -> shared of a page's rows: x in bytes (a multiple of
+// 128 here), row in the page, head, page.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int x,
+                                            int row, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(row), "r"(head), "r"(page)
+      : "memory");
+}
+
+// Two e4m3 values (the low half of `v`) as packed fp16, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(v)));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 constexpr float kPagedLog2e = 1.4426950408889634f;
 constexpr float kPagedLn2 = 0.6931471805599453f;

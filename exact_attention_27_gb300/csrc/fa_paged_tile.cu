@@ -1,10 +1,12 @@
 // Attention of new tokens over a paged cache where sequences bring more than a
-// few rows: tiles of 128 rows (tokens x grouped query heads) on the tcgen05
-// tensor cores.
+// few rows, at head dimension 256: tiles of 128 rows (tokens x grouped query
+// heads) on the tcgen05 tensor cores.  (At d = 64, 96 and 128 two such tiles
+// share the keys: fa_paged_tile2.cu.  Here a 128 x 256 Q tile is 64 KB and its
+// fp32 O takes 256 of the 512 TMEM columns.)
 //
 // Same mathematics as fa_paged.cu (online softmax in base 2, lazy rescale of
-// O), the division of work and the parts of fa_paged.cuh, with key tiles of 128
-// (64 at d = 256).  A CTA lives for the whole call: its items' key tiles form
+// O), the division of work and the parts of fa_paged.cuh, with key tiles of 64.
+// A CTA lives for the whole call: its items' key tiles form
 // one sequence n = 0, 1, ..., and S_{n+1} and S_{n+2} are computed, across the
 // end of an item too, while the softmax works on S_n.
 //
@@ -43,13 +45,12 @@
 
 #include "fa_internal.h"
 #include "fa_paged.cuh"
-#include "fa_paged_launch.h"
+#include "fa_paged_host.h"
+#include "fa_paged_tile.cuh"
 #include "fa_ptx.cuh"
 
 namespace fa {
 namespace {
-
-constexpr float kRescaleThreshold = 8.0f;
 
 template <int D_, bool E4M3_>
 struct TileCfg {
@@ -57,18 +58,18 @@ struct TileCfg {
   static constexpr bool E4M3 = E4M3_;
   static constexpr int DP = (D + 63) / 64 * 64;    // whole 128-byte blocks of 16-bit values
   static constexpr int BM = 128;                   // rows of an item
-  static constexpr int BN = D == 256 ? 64 : 128;   // keys of a tile
+  static constexpr int BN = 64;                    // keys of a tile
   static constexpr int SUB = DP / 64;
   static constexpr int Q_BLOCK = BM * 128;
   static constexpr int KV_BLOCK = BN * 128;
   static constexpr int Q_TILE = SUB * Q_BLOCK;
   static constexpr int KV_TILE = SUB * KV_BLOCK;
-  static constexpr int NQ = D == 256 || (E4M3 && D != 64) ? 1 : 2;  // Q tiles
-  static constexpr int NS = D == 64 ? 4 : 2;                        // K and V stages each
+  static constexpr int NQ = 1;                     // Q tiles
+  static constexpr int NS = 2;                     // K and V stages each
   // e4m3 bytes as they come: K and V tiles in turn.
   static constexpr int RSUB = (D + 127) / 128;
   static constexpr int RAW_TILE = E4M3 ? RSUB * KV_BLOCK : 0;
-  static constexpr int NR = !E4M3 ? 0 : D == 256 ? 2 : D == 64 ? 3 : 4;
+  static constexpr int NR = E4M3 ? 2 : 0;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + NQ * Q_TILE;
   static constexpr int OFF_V = OFF_K + NS * KV_TILE;
@@ -99,68 +100,6 @@ struct TileCfg {
   static constexpr uint32_t COL_O = 512 - DP;
   static_assert(NB * BN <= 512 - DP, "tensor memory");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-};
-
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(v)));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Instruction descriptor for kind::f16 with fp16 A and B (format code 0) and
-// an fp32 accumulator.
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((static_cast<uint32_t>(N) >> 3) << 17) |
-         ((static_cast<uint32_t>(M) >> 4) << 24);
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
-// A CTA's segments: the items of its range one after the other, each with the
-// key tiles [t0, t1) that lie in the range.  Every role walks them on its own.
-template <int BN>
-struct Segments {
-  PagedWalk<128, BN> w;
-  long long unit, end;
-  int t0, t1, tiles, keys;
-  __device__ __forceinline__ void load(const PagedParams& p, int t) {
-    tiles = w.my_tiles(p);
-    keys = w.my_keys(p);
-    t0 = t;
-    t1 = static_cast<int>(min(static_cast<long long>(tiles), t + (end - unit)));
-  }
-  __device__ __forceinline__ void start(const PagedParams& p, const PagedRange& r) {
-    unit = r.first;
-    end = r.end;
-    load(p, w.start(p, r.seq, r.rem));
-  }
-  // False when the range is done.
-  __device__ __forceinline__ bool next(const PagedParams& p) {
-    unit += t1 - t0;
-    if (unit >= end) return false;
-    w.next(p);
-    load(p, 0);
-    return true;
-  }
 };
 
 template <int D, bool E4M3>
@@ -230,7 +169,7 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t sR = sbase + C::OFF_RAW;
   float* q_scale = reinterpret_cast<float*>(smem + C::OFF_SCALE);
 
-  Segments<BN> seg;
+  PagedSegments<128, BN> seg;
 
   if (warp >= 8) {
     reg_decrease<104>();
@@ -319,7 +258,7 @@ __global__ void __launch_bounds__(384, 1)
           return mbar_wait(bar(b), parity, abort_flag, p.err, kErrTimeoutMma);
         };
         // The S products run two tiles ahead of the P V products.
-        Segments<BN> ahead;
+        PagedSegments<128, BN> ahead;
         ahead.start(p, range);
         bool more = true;  // S products are left
         int ta = ahead.t0, na = 0, ia = 0;  // its tile, running number, item
@@ -389,82 +328,19 @@ __global__ void __launch_bounds__(384, 1)
                         mbar_wait(bar(b), parity, abort_flag, p.err, kErrTimeoutLoad)) != 0;
     };
     // Q of item `i` (segment s): row `row`, zeros past the sequence's rows.
-    auto load_q = [&](const Segments<BN>& s, int i) -> bool {
+    auto load_q = [&](const PagedSegments<128, BN>& s, int i) -> bool {
       const int qs = i % C::NQ;
       if (i >= C::NQ && !wait(C::B_QEMPTY + qs, ((i / C::NQ) - 1) & 1)) return false;
-      const int r = s.w.rt * C::BM + row;
-      const bool live = r < s.w.g.qlen * p.G;
-      const int tok = live ? r / p.G : 0;
-      const __nv_bfloat16* src = p.q + (s.w.g.q0 + tok) * p.q_token +
-                                 (s.w.h * p.G + (live ? r - tok * p.G : 0)) * p.q_head;
-      const uint32_t dst = sQ + qs * C::Q_TILE + row * 128;
-      auto at = [&](int c) -> uint32_t {  // 16-byte chunk c of the row
-        return dst + (c >> 3) * C::Q_BLOCK + (((c & 7) ^ (row & 7)) << 4);
-      };
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      if constexpr (E4M3) {
-        // Scaled by 2^e to a largest element in [2^7, 2^8), as fp16.
-        float mx = 0.0f;
-        if (live) {
-#pragma unroll 8
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = reinterpret_cast<const uint4*>(src)[c];
-            for (uint32_t x : {v.x, v.y, v.z, v.w})
-              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x << 16)),
-                                   fabsf(__uint_as_float(x & 0xffff0000u))));
-          }
-        }
-        int e = 134 - static_cast<int>(__float_as_uint(mx) >> 23);
-        if (mx == 0.0f || !(mx < INFINITY)) e = 0;
-        e = min(max(e, -120), 120);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        q_scale[qs * C::BM + row] =
-            p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        auto half = [&](uint32_t x) {
-          return pack_half2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
-        };
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = live ? reinterpret_cast<const uint4*>(src)[c] : zero;
-          sts128(at(c), make_uint4(half(v.x), half(v.y), half(v.z), half(v.w)));
-        }
-      } else {
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c)
-          sts128(at(c), live ? reinterpret_cast<const uint4*>(src)[c] : zero);
-      }
+      q_scale[qs * C::BM + row] =
+          paged_load_q<D, E4M3>(p, paged_row(p, s, row), sQ + qs * C::Q_TILE, row);
       fence_proxy_async_smem();
       mbar_arrive_warp(bar(C::B_QFULL + qs));
       return true;
     };
-    // e4m3 tile in raw slot `raw` to the fp16 tile at `dst`, rows from `keep` on as zeros.
-    auto convert = [&](uint32_t raw, uint32_t dst, int keep) {
-      constexpr int PER = 128 / BN;  // threads a row
-      const int r = row % BN;
-#pragma unroll 4
-      for (int c = row / BN; c < D / 16; c += PER) {
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-        if (r < keep) {
-          const uint4 v = lds128(raw + (c >> 3) * C::KV_BLOCK + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-          lo = make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
-                          e4m3x2_to_f16x2(v.y >> 16));
-          hi = make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
-                          e4m3x2_to_f16x2(v.w >> 16));
-        }
-        const uint32_t blk = dst + (c >> 2) * C::KV_BLOCK + r * 128;
-        sts128(blk + ((((c & 3) * 2) ^ (r & 7)) << 4), lo);
-        sts128(blk + ((((c & 3) * 2 + 1) ^ (r & 7)) << 4), hi);
-      }
-    };
     seg.start(p, range);
-    Segments<BN> ahead = seg;  // the next item's Q (two Q tiles: one item ahead)
     int n = 0, i = 0;
-    bool ok = load_q(ahead, 0), more = true;
+    bool ok = load_q(seg, 0), more = true;
     do {
-      if (C::NQ == 2 && ok) {
-        more = ahead.next(p);
-        if (more) ok = load_q(ahead, i + 1);
-      }
       for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
         const int st = n % C::NS;
         const uint32_t ph = ((n / C::NS) - 1) & 1;
@@ -475,7 +351,7 @@ __global__ void __launch_bounds__(384, 1)
             ok = (n < C::NS || wait((kv ? C::B_VEMPTY : C::B_KEMPTY) + st, ph)) &&
                  wait(C::B_RFULL + rs, (x / C::NR) & 1);
             if (!ok) break;
-            convert(sR + rs * C::RAW_TILE, (kv ? sV : sK) + st * C::KV_TILE, keep);
+            paged_convert<D, BN>(sR + rs * C::RAW_TILE, (kv ? sV : sK) + st * C::KV_TILE, keep, row);
             fence_proxy_async_smem();
             mbar_arrive_warp(bar(C::B_REMPTY + rs));
             mbar_arrive_warp(bar((kv ? C::B_VFIX : C::B_KFULL) + st));
@@ -484,13 +360,7 @@ __global__ void __launch_bounds__(384, 1)
           if (n >= C::NS && !(ok = wait(C::B_VEMPTY + st, ph))) break;
           if (keep < BN) {
             if (!(ok = wait(C::B_VFULL + st, (n / C::NS) & 1))) break;
-            constexpr int CHUNKS = C::SUB * 8;  // 16-byte chunks of a row
-            const int first = max(keep, 0);
-            for (int x = first * CHUNKS + row; x < BN * CHUNKS; x += 128) {
-              const int r = x / CHUNKS, c = x % CHUNKS;
-              sts128(sV + st * C::KV_TILE + (c >> 3) * C::KV_BLOCK + r * 128 + ((c & 7) << 4),
-                     make_uint4(0, 0, 0, 0));
-            }
+            paged_zero_rows<C::SUB, BN, 128>(sV + st * C::KV_TILE, max(keep, 0), row);
             fence_proxy_async_smem();
           }
           mbar_arrive_warp(bar(C::B_VFIX + st));
@@ -499,7 +369,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) break;
       ++i;
       more = seg.next(p);
-      if (C::NQ == 1 && more) ok = load_q(seg, i);
+      if (more) ok = load_q(seg, i);
     } while (ok && more);
   } else {
     // ------------------------------------------------------------ softmax (rows)
@@ -515,17 +385,10 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     seg.start(p, range);
     do {
-      const int rows = seg.w.g.qlen * p.G;
-      const int r = seg.w.rt * C::BM + row;
-      const bool live = r < rows;
-      const int tok = live ? r / p.G : 0;
-      const int head = seg.w.h * p.G + (live ? r - tok * p.G : 0);
-      const int base = seg.w.g.klen - seg.w.g.qlen;
-      const int last = p.causal ? base + tok : seg.w.g.klen - 1;  // last key this row sees
-      const int all_see = p.causal ? base + seg.w.rt * C::BM / p.G : seg.w.g.klen - 1;
+      const PagedRow x = paged_row(p, seg, row);
       const int qs = i % C::NQ;
       if (!(ok = wait(C::B_QFULL + qs, (i / C::NQ) & 1, kErrTimeoutSoftmax))) break;
-      const float c = E4M3 ? q_scale[qs * C::BM + row] : p.scale_log2;
+      const float c = q_scale[qs * C::BM + row];
       mbar_arrive_warp(bar(C::B_QEMPTY + qs));
       float m_used = -INFINITY;  // reference maximum, log2 domain
       float l = 0.0f;
@@ -534,79 +397,16 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t col_s = bf * BN;
         if (!(ok = wait(C::B_SFULL + bf, (n / C::NB) & 1, kErrTimeoutSoftmax))) break;
         tc_fence_after();
-        float s[BN];
-        {
-          uint32_t x[BN];
-#pragma unroll
-          for (int q4 = 0; q4 < BN / 32; ++q4)
-            tmem_ld32(tmem + lane_off + col_s + q4 * 32,
-                      *reinterpret_cast<uint32_t(*)[32]>(&x[q4 * 32]));
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < BN; ++k) s[k] = __uint_as_float(x[k]);
-        }
-        if (t * BN + BN - 1 > all_see) {
-          const int see = last - t * BN;
-#pragma unroll
-          for (int k = 0; k < BN; ++k)
-            if (k > see) s[k] = -INFINITY;
-        }
-        // Row maximum over 8 partial maxima, two new values each time.
-        float pm[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) pm[u] = fmaxf(s[u], s[u + 8]);
-#pragma unroll
-        for (int k = 16; k < BN; k += 16)
-#pragma unroll
-          for (int u = 0; u < 8; ++u) pm[u] = fmax3(pm[u], s[k + u], s[k + u + 8]);
-        const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]),
-                               fmaxf(fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-        const float m_new = fmaxf(m_used, mx * c);
-        float alpha = 1.0f;
-        const bool upd = m_new > m_used + kRescaleThreshold;
-        if (upd) {
-          alpha = ex2_approx(m_used - m_new);
-          m_used = m_new;
-        }
-        const float m_ref = (m_used == -INFINITY) ? 0.0f : m_used;
-        const uint64_t c2 = f2_pack(c, c);
-        const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
-        uint64_t ps2[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) ps2[u] = 0ull;
-        {
-          uint32_t pk[BN / 2];
-#pragma unroll
-          for (int k = 0; k < BN / 2; ++k) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(s[2 * k], s[2 * k + 1]), c2, nm2), x0, x1);
-            const float p0 = ex2_approx(x0);
-            const float p1 = ex2_approx(x1);
-            ps2[k & 3] = f2_add(ps2[k & 3], f2_pack(p0, p1));
-            pk[k] = E4M3 ? pack_half2(p0, p1) : pack_bf16x2(p0, p1);
-          }
-#pragma unroll
-          for (int q4 = 0; q4 < BN / 64; ++q4)
-            tmem_st32(tmem + lane_off + col_s + q4 * 32,
-                      *reinterpret_cast<uint32_t(*)[32]>(&pk[q4 * 32]));
-        }
-        float sum, sum_hi;
-        f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), sum, sum_hi);
-        l = l * alpha + (sum + sum_hi);
+        bool upd;
+        const float alpha =
+            paged_softmax<BN, E4M3>(tmem + lane_off + col_s, t * BN + BN - 1 > x.all_see,
+                                    x.last - t * BN, c, m_used, l, upd);
         if (t > seg.t0 && __any_sync(0xffffffffu, upd)) {
           // O is final before it is rescaled: S_n implies O += P_{n-2} V_{n-2},
           // so the barrier is at most one phase behind.
           if (!(ok = wait(C::B_ODONE, (n - 1) & 1, kErrTimeoutSoftmax))) break;
           tc_fence_after();
-#pragma unroll 1
-          for (int q4 = 0; q4 < D / 32; ++q4) {
-            uint32_t x[32];
-            tmem_ld32(tmem + lane_off + C::COL_O + q4 * 32, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
-            tmem_st32(tmem + lane_off + C::COL_O + q4 * 32, x);
-          }
+          paged_rescale<D>(tmem + lane_off + C::COL_O, alpha);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -615,41 +415,9 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok || !(ok = wait(C::B_FINAL, i & 1, kErrTimeoutEpilogue))) break;
       // ---------------------------------------------------------- end of the item
       tc_fence_after();
-      const bool whole = seg.t0 == 0 && seg.t1 == seg.tiles;
       const int slot = cta * 2 + (seg.t0 == 0 ? 1 : 0);
-      const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
-      const long long token = seg.w.g.q0 + tok;
-      __nv_bfloat16* dst = p.o + token * p.o_token + head * p.o_head;
-      float* part = p.part_o + (static_cast<long long>(slot) * C::BM + row) * D;
-#pragma unroll 1
-      for (int q4 = 0; q4 < D / 32; ++q4) {
-        uint32_t x[32];
-        tmem_ld32(tmem + lane_off + C::COL_O + q4 * 32, x);
-        tmem_wait_ld();
-        if (!live) continue;
-        if (whole) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t y[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              y[u] = pack_bf16x2(__uint_as_float(x[8 * k + 2 * u]) * inv,
-                                 __uint_as_float(x[8 * k + 2 * u + 1]) * inv);
-            reinterpret_cast<uint4*>(dst + q4 * 32)[k] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            reinterpret_cast<uint4*>(part + q4 * 32)[k] =
-                make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-        }
-      }
-      if (live) {
-        if (!whole)
-          p.part_ml[static_cast<long long>(slot) * C::BM + row] = make_float2(m_used, l);
-        else if (p.lse)
-          p.lse[token * p.Hq + head] = l > 0.0f ? (m_used + log2f(l)) * kPagedLn2 : -INFINITY;
-      }
+      paged_store_row<D>(p, x, tmem + lane_off + C::COL_O, seg.t0 == 0 && seg.t1 == seg.tiles,
+                         static_cast<long long>(slot) * C::BM + row, m_used, l);
       if (row == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
         p.notes[cta] = paged_note<C::BM, BN>(p, range, seg.w, seg.unit);
       // (The next item's first O product follows this thread's next P, after a fence.)
@@ -677,24 +445,12 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const PagedPa
                           C::SMEM_BYTES, stream, tk, tv, p);
 }
 
-template <bool E4M3>
-cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int d,
-                     int ctas, cudaStream_t stream) {
-  switch (d) {
-    case 64: return launch_t<64, E4M3>(tk, tv, p, ctas, stream);
-    case 96: return launch_t<96, E4M3>(tk, tv, p, ctas, stream);
-    case 128: return launch_t<128, E4M3>(tk, tv, p, ctas, stream);
-    case 256: return launch_t<256, E4M3>(tk, tv, p, ctas, stream);
-  }
-  return cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 cudaError_t launch_paged_tile(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
-                              int d, bool e4m3, int ctas, cudaStream_t stream) {
-  return e4m3 ? launch_d<true>(tk, tv, p, d, ctas, stream)
-              : launch_d<false>(tk, tv, p, d, ctas, stream);
+                              bool e4m3, int ctas, cudaStream_t stream) {
+  return e4m3 ? launch_t<256, true>(tk, tv, p, ctas, stream)
+              : launch_t<256, false>(tk, tv, p, ctas, stream);
 }
 
 }  // namespace fa

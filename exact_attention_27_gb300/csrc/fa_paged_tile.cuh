@@ -1,0 +1,283 @@
+// Pieces of the two tcgen05 kernels of fa_forward_paged (fa_paged_tile.cu,
+// fa_paged_tile2.cu): a CTA's walk over its items, the rows of Q into shared
+// memory, e4m3 tiles to fp16, the softmax of a row and what becomes of its O.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "fa_paged.cuh"
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+constexpr float kPagedRescale = 8.0f;  // log2 growth of the maximum that moves it
+
+// Instruction descriptor for kind::f16 with fp16 A and B (format code 0) and
+// an fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((static_cast<uint32_t>(N) >> 3) << 17) |
+         ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// A CTA's segments: the items of its range one after the other, each with the
+// key tiles [t0, t1) that lie in the range.  Every role walks them on its own.
+template <int ROWS, int BN>
+struct PagedSegments {
+  PagedWalk<ROWS, BN> w;
+  long long unit, end;
+  int t0, t1, tiles, keys;
+  __device__ __forceinline__ void load(const PagedParams& p, int t) {
+    tiles = w.my_tiles(p);
+    keys = w.my_keys(p);
+    t0 = t;
+    t1 = static_cast<int>(min(static_cast<long long>(tiles), t + (end - unit)));
+  }
+  __device__ __forceinline__ void start(const PagedParams& p, const PagedRange& r) {
+    unit = r.first;
+    end = r.end;
+    load(p, w.start(p, r.seq, r.rem));
+  }
+  // False when the range is done.
+  __device__ __forceinline__ bool next(const PagedParams& p) {
+    unit += t1 - t0;
+    if (unit >= end) return false;
+    w.next(p);
+    load(p, 0);
+    return true;
+  }
+};
+
+// One row of an item, as its thread sees it.
+struct PagedRow {
+  bool live;       // a row of the sequence
+  int head;        // query head
+  int last;        // last key it sees
+  int all_see;     // last key that every row of the item sees
+  long long token;
+};
+
+template <int ROWS, int BN>
+__device__ __forceinline__ PagedRow paged_row(const PagedParams& p,
+                                              const PagedSegments<ROWS, BN>& s, int row) {
+  PagedRow x;
+  const int r = s.w.rt * ROWS + row;
+  x.live = r < s.w.g.qlen * p.G;
+  const int tok = x.live ? r / p.G : 0;
+  x.head = s.w.h * p.G + (x.live ? r - tok * p.G : 0);
+  const int base = s.w.g.klen - s.w.g.qlen;
+  x.last = p.causal ? base + tok : s.w.g.klen - 1;
+  x.all_see = p.causal ? base + s.w.rt * ROWS / p.G : s.w.g.klen - 1;
+  x.token = s.w.g.q0 + tok;
+  return x;
+}
+
+// Row `row` of a Q tile at `q` (128-byte swizzle, blocks of 128 rows x 64
+// values) from global memory, zeros for a row that is none.  Returns the scale
+// of the row's scores: e4m3 pages want Q as fp16, scaled by 2^e to a largest
+// element in [2^7, 2^8).
+template <int D, bool E4M3>
+__device__ __forceinline__ float paged_load_q(const PagedParams& p, const PagedRow& x, uint32_t q,
+                                              int row) {
+  const uint4* src =
+      reinterpret_cast<const uint4*>(p.q + x.token * p.q_token + x.head * p.q_head);
+  auto at = [&](int c) -> uint32_t {  // 16-byte chunk c of the row
+    return q + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+  };
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if constexpr (!E4M3) {
+#pragma unroll 8
+    for (int c = 0; c < D / 8; ++c) sts128(at(c), x.live ? src[c] : zero);
+    return p.scale_log2;
+  } else {
+    float mx = 0.0f;
+#pragma unroll 8
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 v = x.live ? src[c] : zero;
+      for (uint32_t y : {v.x, v.y, v.z, v.w})
+        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(y << 16)),
+                             fabsf(__uint_as_float(y & 0xffff0000u))));
+    }
+    int e = 134 - static_cast<int>(__float_as_uint(mx) >> 23);
+    if (mx == 0.0f || !(mx < INFINITY)) e = 0;
+    e = min(max(e, -120), 120);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    auto half = [&](uint32_t y) {
+      return pack_f16x2(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
+    };
+#pragma unroll 8
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 v = x.live ? src[c] : zero;
+      sts128(at(c), make_uint4(half(v.x), half(v.y), half(v.z), half(v.w)));
+    }
+    return p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  }
+}
+
+// A tile of BN keys from e4m3 bytes (at `raw`, as the copies leave them) to the
+// fp16 tile at `dst`, rows from `keep` on as zeros; 128 threads.
+template <int D, int BN>
+__device__ __forceinline__ void paged_convert(uint32_t raw, uint32_t dst, int keep, int tid) {
+  constexpr int PER = 128 / BN;  // threads a row
+  const int r = tid % BN;
+#pragma unroll 4
+  for (int c = tid / BN; c < D / 16; c += PER) {
+    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    if (r < keep) {
+      const uint4 v = lds128(raw + (c >> 3) * (BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+      lo = make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y),
+                      e4m3x2_f16x2(v.y >> 16));
+      hi = make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w),
+                      e4m3x2_f16x2(v.w >> 16));
+    }
+    const uint32_t blk = dst + (c >> 2) * (BN * 128) + r * 128;
+    sts128(blk + ((((c & 3) * 2) ^ (r & 7)) << 4), lo);
+    sts128(blk + ((((c & 3) * 2 + 1) ^ (r & 7)) << 4), hi);
+  }
+}
+
+// Rows `first`.. of the bf16 tile of BN keys at `v` as zeros; THREADS threads.
+template <int SUB, int BN, int THREADS>
+__device__ __forceinline__ void paged_zero_rows(uint32_t v, int first, int tid) {
+  constexpr int CHUNKS = SUB * 8;  // 16-byte chunks of a row
+  for (int x = first * CHUNKS + tid; x < BN * CHUNKS; x += THREADS) {
+    const int r = x / CHUNKS, c = x % CHUNKS;
+    sts128(v + (c >> 3) * (BN * 128) + r * 128 + ((c & 7) << 4), make_uint4(0, 0, 0, 0));
+  }
+}
+
+// The scores of a row's key tile at TMEM address `s` to P over them, with the
+// running maximum m and sum l (base 2, scores times c).  `see`: the last key of
+// the tile that the row sees, if `mask`.  Returns the factor that O and the old
+// l are due (1 while the maximum has not grown by more than kPagedRescale).
+template <int BN, bool F16>
+__device__ __forceinline__ float paged_softmax(uint32_t s_addr, bool mask, int see, float c,
+                                               float& m, float& l, bool& moved) {
+  float s[BN];
+  {
+    uint32_t x[BN];
+#pragma unroll
+    for (int q4 = 0; q4 < BN / 32; ++q4)
+      tmem_ld32(s_addr + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[q4 * 32]));
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < BN; ++k) s[k] = __uint_as_float(x[k]);
+  }
+  if (mask) {
+#pragma unroll
+    for (int k = 0; k < BN; ++k)
+      if (k > see) s[k] = -INFINITY;
+  }
+  // Row maximum over 8 partial maxima, two new values each time.
+  float pm[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) pm[u] = fmaxf(s[u], s[u + 8]);
+#pragma unroll
+  for (int k = 16; k < BN; k += 16)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) pm[u] = fmax3(pm[u], s[k + u], s[k + u + 8]);
+  const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]),
+                         fmaxf(fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+  const float m_new = fmaxf(m, mx * c);
+  float alpha = 1.0f;
+  moved = m_new > m + kPagedRescale;
+  if (moved) {
+    alpha = ex2_approx(m - m_new);
+    m = m_new;
+  }
+  const float m_ref = m == -INFINITY ? 0.0f : m;
+  const uint64_t c2 = f2_pack(c, c);
+  const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
+  uint64_t ps2[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) ps2[u] = 0ull;
+  uint32_t pk[BN / 2];
+#pragma unroll
+  for (int k = 0; k < BN / 2; ++k) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(s[2 * k], s[2 * k + 1]), c2, nm2), x0, x1);
+    const float p0 = ex2_approx(x0);
+    const float p1 = ex2_approx(x1);
+    ps2[k & 3] = f2_add(ps2[k & 3], f2_pack(p0, p1));
+    pk[k] = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+  }
+#pragma unroll
+  for (int q4 = 0; q4 < BN / 64; ++q4)
+    tmem_st32(s_addr + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[q4 * 32]));
+  float sum, sum_hi;
+  f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), sum, sum_hi);
+  l = l * alpha + (sum + sum_hi);
+  return alpha;
+}
+
+// O of a row (D fp32 columns at TMEM address `o`) times alpha.
+template <int D>
+__device__ __forceinline__ void paged_rescale(uint32_t o_addr, float alpha) {
+#pragma unroll 1
+  for (int q4 = 0; q4 < D / 32; ++q4) {
+    uint32_t x[32];
+    tmem_ld32(o_addr + q4 * 32, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * alpha);
+    tmem_st32(o_addr + q4 * 32, x);
+  }
+}
+
+// A row's O out of TMEM: the result if its item lies whole in this CTA, else
+// its part, at row `part_row` of the parts.
+template <int D>
+__device__ __forceinline__ void paged_store_row(const PagedParams& p, const PagedRow& x,
+                                                uint32_t o_addr, bool whole, long long part_row,
+                                                float m, float l) {
+  const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
+  __nv_bfloat16* dst = p.o + x.token * p.o_token + x.head * p.o_head;
+  float* part = p.part_o + part_row * D;
+#pragma unroll 1
+  for (int q4 = 0; q4 < D / 32; ++q4) {
+    uint32_t v[32];
+    tmem_ld32(o_addr + q4 * 32, v);
+    tmem_wait_ld();
+    if (!x.live) continue;
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          y[u] = pack_bf16x2(__uint_as_float(v[8 * k + 2 * u]) * inv,
+                             __uint_as_float(v[8 * k + 2 * u + 1]) * inv);
+        reinterpret_cast<uint4*>(dst + q4 * 32)[k] = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        reinterpret_cast<uint4*>(part + q4 * 32)[k] =
+            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+  }
+  if (x.live) {
+    if (!whole)
+      p.part_ml[part_row] = make_float2(m, l);
+    else if (p.lse)
+      p.lse[x.token * p.Hq + x.head] = l > 0.0f ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
+  }
+}
+
+}  // namespace fa

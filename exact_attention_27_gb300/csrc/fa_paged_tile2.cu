@@ -1,0 +1,476 @@
+// Attention of new tokens over a paged cache where sequences bring more than a
+// few rows, at head dimensions 64, 96 and 128: items of 256 rows (tokens x
+// grouped query heads), two tiles A and B of 128 that share each K and V tile,
+// on the tcgen05 tensor cores.
+//
+// Same mathematics as fa_paged.cu (online softmax in base 2, lazy rescale of
+// O), the division of work and the parts of fa_paged.cuh.  Bound by the tensor
+// and exponential units: a 128 x 128 tile pair costs 1024 tensor cycles at d =
+// 128 and 512 of the exponential unit; sharing keys between two tiles halves
+// what is read from L2 (64 KB per 2 x 128 x 128 scores), and one tile's softmax
+// runs while the tensor core works on the other's products.
+//
+// A CTA lives for the whole call: its items' key tiles form one sequence, and
+// the first scores of an item are computed while the softmax warps still store
+// the last one's O.
+//
+// Warp roles:
+//   warps 0-3   softmax of tile A, warps 4-7 of tile B: thread t owns row t.
+//               It also puts its row of Q into shared memory (a row's token and
+//               head need not be a regular box): the next item's once its last
+//               scores of this one are there, so before the epilogue.
+//   warp 8      TMA producer: one box per page and 128-byte column block.
+//   warp 9      MMA issuer and TMEM owner, per key tile:
+//               O_A += P_A V, S_A of the next tile, O_B += P_B V, next S_B.
+//   the helpers (bf16 pages: warps 10 and 11; e4m3: warps 12-15, 10 and 11
+//               being idle): V's rows past the last key made 0 (their p is 0,
+//               but the page may hold anything there); e4m3 pages: K and V from
+//               bytes to fp16 tiles, which both tiles then use.
+// An item of at most 128 rows has no tile B; its warps and products skip it.
+// Registers: bf16 384 threads at 168: 224 / 224 / 56; e4m3 512 at 128: 200 /
+// 200 / 56 / 56 (the sums are the launch totals 504 and 512).
+//
+// Tensor memory: S of tile x at columns 128 x (P, packed in pairs, over its
+// first half), O at 256 + DP x.  A tile's next S follows its own O += P V, and
+// its O is first written for an item by a product that waits for a P made
+// after the epilogue of the item before.
+//
+// Every wait is bounded (about a second); on expiry the kernel sets an error
+// bit, every role skips its remaining work and the CTA exits.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "fa_internal.h"
+#include "fa_paged.cuh"
+#include "fa_paged_host.h"
+#include "fa_paged_tile.cuh"
+#include "fa_ptx.cuh"
+
+namespace fa {
+namespace {
+
+template <int D_, bool E4M3_>
+struct Tile2Cfg {
+  static constexpr int D = D_;
+  static constexpr bool E4M3 = E4M3_;
+  static constexpr int DP = (D + 63) / 64 * 64;  // whole 128-byte blocks of 16-bit values
+  static constexpr int BM = 256;                 // rows of an item
+  static constexpr int BN = 128;                 // keys of a tile
+  static constexpr int SUB = DP / 64;
+  static constexpr int BLOCK = 128 * 128;        // 128 rows x 128 bytes
+  static constexpr int TILE = SUB * BLOCK;       // of Q (each of A and B), K or V
+  static constexpr int NS = D == 64 ? 4 : 2;     // K and V stages each
+  static constexpr int NR = !E4M3 ? 0 : D == 64 ? 4 : 2;  // e4m3 tiles as they come, K and V in turn
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_V = OFF_K + NS * TILE;
+  static constexpr int OFF_RAW = OFF_V + NS * TILE;
+  static constexpr int OFF_SCR = OFF_RAW + NR * BLOCK;
+  static constexpr int OFF_BAR = OFF_SCR + 40 * 8;
+  static constexpr int HELPERS = E4M3 ? 4 : 2;   // warps
+  static constexpr int B_QFULL = 0;              // [2] 4 warps
+  static constexpr int B_KFULL = B_QFULL + 2;    // [NS] bytes (e4m3: the helpers)
+  static constexpr int B_KEMPTY = B_KFULL + NS;
+  static constexpr int B_VFULL = B_KEMPTY + NS;  // [NS] bytes (e4m3: not used)
+  static constexpr int B_VEMPTY = B_VFULL + NS;
+  static constexpr int B_VFIX = B_VEMPTY + NS;   // [NS] the helpers: V is whole and finite
+  static constexpr int B_RFULL = B_VFIX + NS;    // [NR] bytes
+  static constexpr int B_REMPTY = B_RFULL + NR;  // [NR] the helpers
+  static constexpr int B_SFULL = B_REMPTY + NR;  // [2] S of tile x
+  static constexpr int B_PFULL = B_SFULL + 2;    // [2] 4 warps
+  static constexpr int B_ODONE = B_PFULL + 2;    // [2] O_x += P_x V
+  static constexpr int B_DRAIN = B_ODONE + 2;
+  static constexpr int NBAR = B_DRAIN + 1;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static constexpr int THREADS = E4M3 ? 512 : 384;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t COL_O = 256;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
+    fa_paged_tile2_kernel(const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+  using C = Tile2Cfg<D, E4M3>;
+  constexpr int BN = C::BN;
+  using Seg = PagedSegments<C::BM, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(C::B_QFULL + x), 4);
+      mbar_init(bar(C::B_SFULL + x), 1);
+      mbar_init(bar(C::B_PFULL + x), 4);
+      mbar_init(bar(C::B_ODONE + x), 1);
+    }
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(bar(C::B_KFULL + s), E4M3 ? C::HELPERS : 1);
+      mbar_init(bar(C::B_KEMPTY + s), 1);
+      mbar_init(bar(C::B_VFULL + s), 1);
+      mbar_init(bar(C::B_VEMPTY + s), 1);
+      mbar_init(bar(C::B_VFIX + s), C::HELPERS);
+    }
+    for (int s = 0; s < C::NR; ++s) {
+      mbar_init(bar(C::B_RFULL + s), 1);
+      mbar_init(bar(C::B_REMPTY + s), C::HELPERS);
+    }
+    mbar_init(bar(C::B_DRAIN), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8 && elect_one()) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const PagedRange range =
+      paged_range<C::BM, BN, C::THREADS>(p, reinterpret_cast<long long*>(smem + C::OFF_SCR));
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) p.notes[cta].last = -1;
+  if (range.end <= range.first) return;  // block-uniform, nothing in flight
+
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sQ = sbase + C::OFF_Q;
+  const uint32_t sK = sbase + C::OFF_K;
+  const uint32_t sV = sbase + C::OFF_V;
+  const uint32_t sR = sbase + C::OFF_RAW;
+
+  Seg seg;
+  // Whether the item has rows in tile B.
+  auto has_b = [&](const Seg& s) -> bool { return s.w.g.qlen * p.G - s.w.rt * C::BM > 128; };
+
+  if (warp >= 8) {
+    reg_decrease<56>();
+    if (warp == 8) {
+      // ---------------------------------------------------------- TMA producer
+      const int page = 1 << p.page_shift;
+      const int box_rows = min(page, BN);
+      constexpr int BLOCKS = E4M3 ? 1 : C::SUB;
+      const bool mine = lane < BN / box_rows * BLOCKS;
+      const int row0 = lane / BLOCKS * box_rows, sub = lane % BLOCKS;
+      const uint32_t dst0 = sub * C::BLOCK + row0 * 128;
+      // Copies the lanes' boxes of one tile; `full` counts their bytes.
+      auto copy = [&](const CUtensorMap* tm, uint32_t dst, uint32_t full, bool issue, int key0,
+                      int head, int id) {
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
+        if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * 128);
+        __syncwarp();
+        if (issue) tma_load_4d(dst + dst0, tm, full, sub * 128, key0 & (page - 1), head, id);
+      };
+      auto wait = [&](uint32_t b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err, kErrTimeoutLoad)) !=
+               0;
+      };
+      int nk = 0, nv = 0;  // K and V tiles issued
+      bool ok = true;
+      seg.start(p, range);
+      do {
+        for (int t = seg.t0; ok && t < seg.t1; ++t) {
+          const int key0 = t * BN + row0;
+          bool issue = mine && key0 < seg.keys;
+          int id = 0;
+          if (issue) {
+            id = p.table[seg.w.s * p.table_stride + (key0 >> p.page_shift)];
+            if (id < 0 || id >= p.n_pages) {
+              atomicOr(p.err, kErrBadPage);
+              issue = false;
+            }
+          }
+          if constexpr (E4M3) {
+            const int i = 2 * nk, j = i + 1;  // as they come: K, then V
+            if (i >= C::NR && !(ok = wait(bar(C::B_REMPTY + i % C::NR), ((i / C::NR) - 1) & 1)))
+              break;
+            copy(&tmK, sR + i % C::NR * C::BLOCK, bar(C::B_RFULL + i % C::NR), issue, key0,
+                 seg.w.h, id);
+            ++nk;
+            if (j >= C::NR && !(ok = wait(bar(C::B_REMPTY + j % C::NR), ((j / C::NR) - 1) & 1)))
+              break;
+            copy(&tmV, sR + j % C::NR * C::BLOCK, bar(C::B_RFULL + j % C::NR), issue, key0,
+                 seg.w.h, id);
+            ++nv;
+          } else {
+            const int st = nk % C::NS;
+            const uint32_t ph = ((nk / C::NS) - 1) & 1;
+            if (nk >= C::NS && !(ok = wait(bar(C::B_KEMPTY + st), ph))) break;
+            copy(&tmK, sK + st * C::TILE, bar(C::B_KFULL + st), issue, key0, seg.w.h, id);
+            ++nk;
+            if (nv >= C::NS && !(ok = wait(bar(C::B_VEMPTY + st), ph))) break;
+            copy(&tmV, sV + st * C::TILE, bar(C::B_VFULL + st), issue, key0, seg.w.h, id);
+            ++nv;
+          }
+        }
+      } while (ok && seg.next(p));
+      if (*abort_flag) {
+        // Let the copies already issued land before the CTA's memory is released.
+        if constexpr (E4M3) {
+          for (int i = max(0, nk + nv - C::NR); i < nk + nv; ++i)
+            mbar_wait_timed(bar(C::B_RFULL + i % C::NR), (i / C::NR) & 1);
+        } else {
+          for (int i = max(0, nk - C::NS); i < nk; ++i)
+            mbar_wait_timed(bar(C::B_KFULL + i % C::NS), (i / C::NS) & 1);
+          for (int i = max(0, nv - C::NS); i < nv; ++i)
+            mbar_wait_timed(bar(C::B_VFULL + i % C::NS), (i / C::NS) & 1);
+        }
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------- MMA issuer
+      if (elect_one()) {
+        constexpr uint32_t ID_S = E4M3 ? idesc_f16_f32(128, BN, false)
+                                       : idesc_bf16_f32(128, BN, false, false);
+        constexpr uint32_t ID_O = E4M3 ? idesc_f16_f32(128, D, true)
+                                       : idesc_bf16_f32(128, D, false, true);
+        const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024);
+        const uint64_t k_desc = smem_desc_sw128(sK, 16, 1024);
+        const uint64_t v_desc = smem_desc_sw128(sV, C::BLOCK, 1024);  // MN-major, N = D
+        auto wait = [&](int b, uint32_t parity) {
+          return mbar_wait(bar(b), parity, abort_flag, p.err, kErrTimeoutMma);
+        };
+        uint32_t items[2] = {0, 0};  // items whose Q tile x was waited for
+        uint32_t done[2] = {0, 0};   // products P_x V issued
+        // S_x = Q_x K^T of key tile n; `first`: the item's first.
+        auto issue_s = [&](int x, int n, bool first) -> bool {
+          if (first && !wait(C::B_QFULL + x, items[x]++ & 1)) return false;
+          tc_fence_after();
+          const uint32_t d_tmem = tmem + x * 128;
+          const uint64_t qd = desc_add(q_desc, x * C::TILE);
+          const uint64_t kd = desc_add(k_desc, (n % C::NS) * C::TILE);
+          mma_ss_k<ID_S, 0>(d_tmem, qd, kd);
+#pragma unroll
+          for (int kk = 1; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::BLOCK + (kk & 3) * 32;
+            mma_ss_k<ID_S, 1>(d_tmem, desc_add(qd, off), desc_add(kd, off));
+          }
+          mma_commit(bar(C::B_SFULL + x));
+          return true;
+        };
+        seg.start(p, range);
+        bool b = has_b(seg), first = true;
+        bool ok = wait(C::B_KFULL, 0) && issue_s(0, 0, true) && (!b || issue_s(1, 0, true));
+        if (ok) mma_commit(bar(C::B_KEMPTY));
+        int t = seg.t0;
+        for (int n = 0; ok; ++n) {
+          const int st = n % C::NS, sn = (n + 1) % C::NS;
+          // The next key tile, of this item or the next.
+          bool more = true, next_b = b, next_first = false;
+          if (++t == seg.t1) {
+            more = seg.next(p);
+            t = 0;
+            next_first = true;
+            next_b = more && has_b(seg);
+          }
+          ok = (E4M3 || wait(C::B_VFULL + st, (n / C::NS) & 1)) &&
+               wait(C::B_VFIX + st, (n / C::NS) & 1);
+          bool k_ready = false;
+#pragma unroll 1
+          for (int x = 0; ok && x < 2; ++x) {
+            if (x == 0 || b) {
+              if (!(ok = wait(C::B_PFULL + x, done[x]++ & 1))) break;
+              tc_fence_after();
+              const uint64_t vd = desc_add(v_desc, st * C::TILE);
+              const uint32_t pa = tmem + x * 128;
+              const uint32_t od = tmem + C::COL_O + x * C::DP;
+              if (first)
+                mma_ts_k<ID_O, 0>(od, pa, vd);
+              else
+                mma_ts_k<ID_O, 1>(od, pa, vd);
+#pragma unroll
+              for (int kk = 1; kk < BN / 16; ++kk)
+                mma_ts_k<ID_O, 1>(od, pa + kk * 8, desc_add(vd, kk * 2048));
+              mma_commit(bar(C::B_ODONE + x));
+            }
+            if (more && (x == 0 || next_b)) {
+              if (!k_ready && !(ok = wait(C::B_KFULL + sn, ((n + 1) / C::NS) & 1))) break;
+              k_ready = true;
+              if (!(ok = issue_s(x, n + 1, next_first))) break;
+            }
+          }
+          if (!ok) break;
+          mma_commit(bar(C::B_VEMPTY + st));
+          if (!more) break;
+          mma_commit(bar(C::B_KEMPTY + sn));
+          b = next_b;
+          first = next_first;
+        }
+        if (*abort_flag) {
+          // Let the MMAs already issued finish before tensor memory is released.
+          mma_commit(bar(C::B_DRAIN));
+          mbar_wait_timed(bar(C::B_DRAIN), 0);
+        }
+      }
+    } else if (warp >= (E4M3 ? 12 : 10)) {
+      // ---------------------------------------------------------- helpers
+      const int tid = threadIdx.x - 32 * (E4M3 ? 12 : 10);
+      auto wait = [&](int b, uint32_t parity) {
+        return __all_sync(0xffffffffu,
+                          mbar_wait(bar(b), parity, abort_flag, p.err, kErrTimeoutLoad)) != 0;
+      };
+      int n = 0;
+      bool ok = true;
+      seg.start(p, range);
+      do {
+        for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
+          const int st = n % C::NS;
+          const uint32_t ph = ((n / C::NS) - 1) & 1;
+          const int keep = min(seg.keys - t * BN, BN);  // rows that are keys
+          if constexpr (E4M3) {
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+              const int i = 2 * n + kv, rs = i % C::NR;
+              ok = (n < C::NS || wait((kv ? C::B_VEMPTY : C::B_KEMPTY) + st, ph)) &&
+                   wait(C::B_RFULL + rs, (i / C::NR) & 1);
+              if (!ok) break;
+              paged_convert<D, BN>(sR + rs * C::BLOCK, (kv ? sV : sK) + st * C::TILE, keep, tid);
+              fence_proxy_async_smem();
+              mbar_arrive_warp(bar(C::B_REMPTY + rs));
+              mbar_arrive_warp(bar((kv ? C::B_VFIX : C::B_KFULL) + st));
+            }
+          } else {
+            if (n >= C::NS && !(ok = wait(C::B_VEMPTY + st, ph))) break;
+            if (keep < BN) {
+              if (!(ok = wait(C::B_VFULL + st, (n / C::NS) & 1))) break;
+              paged_zero_rows<C::SUB, BN, 64>(sV + st * C::TILE, max(keep, 0), tid);
+              fence_proxy_async_smem();
+            }
+            mbar_arrive_warp(bar(C::B_VFIX + st));
+          }
+        }
+      } while (ok && seg.next(p));
+    }
+  } else {
+    // ------------------------------------------------------------ softmax (rows)
+    if constexpr (E4M3)
+      reg_increase<200>();
+    else
+      reg_increase<224>();
+    const int x = warp >> 2;            // tile of this warpgroup
+    const int row = threadIdx.x & 127;  // row within the tile
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_off + x * 128;
+    const uint32_t o_addr = tmem + lane_off + C::COL_O + x * C::DP;
+    // Waits are made warp-uniform: the TMEM loads and stores are
+    // warp-collective, so either every lane goes on or every lane stops.
+    auto wait = [&](int b, uint32_t parity, uint32_t code) {
+      return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, p.err, code)) != 0;
+    };
+    // The next item with rows in this tile (the one at hand if it has).
+    auto settle = [&](bool have) {
+      while (have && x == 1 && !has_b(seg)) have = seg.next(p);
+      return have;
+    };
+    auto load_q = [&](const PagedRow& r) -> float {
+      const float c = paged_load_q<D, E4M3>(p, r, sQ + x * C::TILE, row);
+      fence_proxy_async_smem();
+      mbar_arrive_warp(bar(C::B_QFULL + x));
+      return c;
+    };
+    seg.start(p, range);
+    bool have = settle(true), ok = true;
+    PagedRow r{};
+    float c = 0.0f;
+    if (have) {
+      r = paged_row(p, seg, x * 128 + row);
+      c = load_q(r);
+    }
+    uint32_t n = 0;  // tiles of this warpgroup
+    while (have) {
+      float m = -INFINITY;  // reference maximum, log2 domain
+      float l = 0.0f;
+      for (int t = seg.t0; t < seg.t1; ++t, ++n) {
+        if (!(ok = wait(C::B_SFULL + x, n & 1, kErrTimeoutSoftmax))) break;
+        tc_fence_after();
+        bool moved;
+        const float alpha = paged_softmax<BN, E4M3>(s_addr, t * BN + BN - 1 > r.all_see,
+                                                    r.last - t * BN, c, m, l, moved);
+        if (t > seg.t0 && __any_sync(0xffffffffu, moved)) {
+          // O is final before it is rescaled (S of this tile was issued after
+          // O += P V of the one before, so this does not wait long).
+          if (!(ok = wait(C::B_ODONE + x, (n - 1) & 1, kErrTimeoutSoftmax))) break;
+          tc_fence_after();
+          paged_rescale<D>(o_addr, alpha);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive_warp(bar(C::B_PFULL + x));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- end of the item
+      // Its last scores have been read, so Q's tile is free.
+      const PagedRow now = r;
+      const bool whole = seg.t0 == 0 && seg.t1 == seg.tiles;
+      const int slot = cta * 2 + (seg.t0 == 0 ? 1 : 0);
+      if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
+        p.notes[cta] = paged_note<C::BM, BN>(p, range, seg.w, seg.unit);
+      have = settle(seg.next(p));
+      if (have) {
+        r = paged_row(p, seg, x * 128 + row);
+        c = load_q(r);
+      }
+      if (!(ok = wait(C::B_ODONE + x, (n - 1) & 1, kErrTimeoutEpilogue))) break;
+      tc_fence_after();
+      paged_store_row<D>(p, now, o_addr, whole,
+                         static_cast<long long>(slot) * C::BM + x * 128 + row, m, l);
+      tc_fence_before();
+      // (The next item's first O product waits for this thread's next P.)
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int ctas,
+                     cudaStream_t stream) {
+  using C = Tile2Cfg<D, E4M3>;
+  const cudaError_t e = set_smem_limit_once<fa_paged_tile2_kernel<D, E4M3>>(C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(fa_paged_tile2_kernel<D, E4M3>, dim3(ctas), dim3(C::THREADS),
+                          C::SMEM_BYTES, stream, tk, tv, p);
+}
+
+template <bool E4M3>
+cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int d,
+                     int ctas, cudaStream_t stream) {
+  switch (d) {
+    case 64: return launch_t<64, E4M3>(tk, tv, p, ctas, stream);
+    case 96: return launch_t<96, E4M3>(tk, tv, p, ctas, stream);
+    case 128: return launch_t<128, E4M3>(tk, tv, p, ctas, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tile2(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+                               int d, bool e4m3, int ctas, cudaStream_t stream) {
+  return e4m3 ? launch_d<true>(tk, tv, p, d, ctas, stream)
+              : launch_d<false>(tk, tv, p, d, ctas, stream);
+}
+
+}  // namespace fa

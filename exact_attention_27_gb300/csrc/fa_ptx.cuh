@@ -17,9 +17,6 @@ enum : uint32_t {
   kErrTimeoutSoftmax = 1u << 2,
   kErrTimeoutEpilogue = 1u << 3,
   kErrTimeoutOther = 1u << 4,
-  // Not a wait: a paged call met a length past its block table's row or a
-  // page outside its cache.
-  kErrBadPage = 1u << 5,
 };
 
 // A wait gives up after this many nanoseconds (about a second).
@@ -170,18 +167,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 
-// 4-D tiled copy global -> shared of a page's rows: x in bytes (a multiple of
-// 128 here), row in the page, head, page.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int x,
-                                            int row, int head, int page) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(row), "r"(head), "r"(page)
-      : "memory");
-}
-
-// Same as tma_load_3d, with an L2 cache-policy hint (createpolicy result).
+// Same, with an L2 cache-policy hint (createpolicy result).
 __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void* tmap, uint32_t bar,
                                                  int x, int y, int z, uint64_t policy) {
   asm volatile(

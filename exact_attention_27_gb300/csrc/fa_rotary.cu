@@ -28,6 +28,7 @@
 #include <cstring>
 
 #include "fa_internal.h"
+#include "fa_paged_host.h"
 #include "fa_ptx.cuh"
 
 namespace fa {

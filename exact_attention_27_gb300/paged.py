@@ -10,7 +10,6 @@ The fa_* functions write into the caller's tensors; rotary_forward,
 rotary_backward, paged_append and paged_attention allocate what they return.
 """
 
-import contextlib
 import ctypes
 import math
 
@@ -19,40 +18,39 @@ from ._lib import FaError, library
 
 _byref = ctypes.byref
 
-
-def _torch():
-    import torch
-    return torch
-
-
-def _stream(stream):
-    from . import _stream as current
-    return current(stream)
+# torch is imported on first use, by the first handle; what every call asks for is then at hand
+# (a server's step makes two calls a layer, and each microsecond of host time counts there).
+_torch = _BF16 = _F32 = _I32 = None
+_device = _raw_stream = None
 
 
-def _check(status, what):
-    if status:
-        raise FaError(status, what)
+def _load_torch():
+    global _torch, _BF16, _F32, _I32, _device, _raw_stream
+    if _torch is None:
+        import torch
+        _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda _: torch.cuda.current_stream().cuda_stream)
+        _torch = torch
+    return _torch
 
 
-def _current_device():
-    return _torch().cuda.current_device()
+def _stream(stream, device):
+    if stream is None:
+        return _raw_stream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _on(stream):
-    """Allocations on `stream` (None: the current one), whose later use on it the allocator
-    then orders."""
-    torch = _torch()
-    if stream is None:
-        return contextlib.nullcontext()
+    """Allocations on `stream`, whose later use on it the allocator then orders."""
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
+        stream = _torch.cuda.ExternalStream(stream)
+    return _torch.cuda.stream(stream)
 
 
 def _int32(name, t, dims, device=None):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_cuda:
+    if not isinstance(t, _torch.Tensor) or t.dtype is not _I32 or not t.is_cuda:
         raise ValueError(f"{name} must be an int32 CUDA tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimension(s), has {t.dim()}")
@@ -62,28 +60,42 @@ def _int32(name, t, dims, device=None):
         raise ValueError(f"{name} is on cuda:{t.get_device()}, not cuda:{device}")
 
 
-def _rows(name, t, dims, device):
-    """A bf16 CUDA tensor of `dims` dimensions on `device`, its last one contiguous, addressed
-    in 16-byte vectors."""
-    if t.dtype is not _torch().bfloat16 or not t.is_cuda:
+def _rows3(name, t, device):
+    """Token and head strides of a bf16 [T, heads, d] on `device`, its last dimension
+    contiguous; the library checks the address."""
+    s = t.stride()
+    if t.dtype is _BF16 and t.get_device() == device and len(s) == 3 and s[2] == 1 and \
+            not (s[0] | s[1]) & 7:
+        return s
+    return _strides(name, t, 3, device)
+
+
+def _strides(name, t, dims, device):
+    """The strides of a bf16 CUDA tensor of `dims` dimensions addressed in 16-byte vectors (those
+    of dimensions of one element, which may be anything, rounded to what the library takes)."""
+    if t.dtype is not _BF16 or not t.is_cuda:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, has {t.dim()}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, not cuda:{device}")
     strides = t.stride()
-    if strides[-1] != 1 or t.data_ptr() & 15:
-        raise ValueError(f"{name} must be contiguous along d and start on 16 bytes")
+    if strides[-1] != 1:
+        raise ValueError(f"{name} must be contiguous along d")
     for n, s in zip(t.shape, strides[:-1]):
         if s & 7 and n > 1:
             raise ValueError(f"{name} has strides {strides}: multiples of 8 are needed")
-    return strides
+    return tuple((s + 7) & ~7 for s in strides)
 
 
-def _even(stride):
-    """The stride of a dimension of one element may be anything; the library wants multiples
-    of 8."""
-    return stride if not stride & 7 else (stride + 7) & ~7
+def _same_device(device, *handles):
+    for h in handles:
+        if h is not None and h.device != device:
+            raise ValueError(f"{type(h).__name__} is on cuda:{h.device}, the tensors on "
+                             f"cuda:{device}")
+    if device != _device():
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is "
+                         f"cuda:{_device()}")
 
 
 class Rotary:
@@ -93,7 +105,7 @@ class Rotary:
     (p, p + rot_dim / 2)."""
 
     def __init__(self, inv_freq, sections=None, interleaved=False, axis_of_pair=None):
-        torch = _torch()
+        torch = _load_torch()
         if inv_freq.dtype is not torch.float32 or not inv_freq.is_cuda or inv_freq.dim() != 1 or \
                 not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous fp32 CUDA vector")
@@ -119,6 +131,7 @@ class Rotary:
         self.rot_dim = 2 * half
         self._c = _lib.RotarySpec(inv_freq.data_ptr(), 2 * half, axes, int(bool(interleaved)),
                                   (ctypes.c_ubyte * 128)(*axis_of_pair))
+        self._ref = _byref(self._c)
 
 
 class PagedCache:
@@ -127,7 +140,7 @@ class PagedCache:
     view of [n_pages, page_size, H_kv, d], or slices of one tensor, will do)."""
 
     def __init__(self, k_pages, v_pages, k_descale=1.0, v_descale=1.0):
-        torch = _torch()
+        torch = _load_torch()
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
             raise ValueError("k_pages and v_pages must both be [n_pages, H_kv, page_size, d]")
         kinds = {torch.bfloat16: (0, 2), torch.float8_e4m3fn: (1, 1)}
@@ -163,6 +176,7 @@ class PagedCache:
         self.device = k_pages.get_device()
         self._c = _lib.PagedCacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1],
                                         ks[2], n, page, H, d, dtype, k_descale, v_descale)
+        self._ref = _byref(self._c)
 
 
 class PagedBatch:
@@ -171,6 +185,7 @@ class PagedBatch:
     sequence brings, chooses kernels; a wrong value costs time only."""
 
     def __init__(self, block_table, q_start, kv_len, max_q_len=1):
+        _load_torch()
         _int32("block_table", block_table, 2)
         device = block_table.get_device()
         _int32("q_start", q_start, 1, device)
@@ -189,53 +204,51 @@ class PagedBatch:
             block_table.data_ptr(), block_table.stride(0) if S > 1 else block_table.shape[1],
             block_table.shape[1], q_start.data_ptr(), kv_len.data_ptr(), S,
             min(self.max_q_len, 2**31 - 1))
-
-
-def _same_device(device, *handles):
-    for h in handles:
-        if h is not None and h.device != device:
-            raise ValueError(f"{type(h).__name__} is on cuda:{h.device}, the tensors on "
-                             f"cuda:{device}")
-    if device != _current_device():
-        raise ValueError(f"the tensors are on cuda:{device}, the current device is "
-                         f"cuda:{_current_device()}")
+        self._ref = _byref(self._c)
 
 
 def _rotary_rows(x, out, device, name):
-    a = _rows(name, x, 4, device)
-    b = _rows(name + "_out", out, 4, device)
-    if out.shape != x.shape:
-        raise ValueError(f"{name}_out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
-    for n, s in zip(out.shape, b):
-        if n > 1 and s == 0:
+    a, b = x.stride(), out.stride()
+    shape = x.shape
+    if out.shape != shape:
+        raise ValueError(f"{name}_out has shape {tuple(out.shape)}, expected {tuple(shape)}")
+    if x.dtype is not _BF16 or out.dtype is not _BF16 or x.get_device() != device or \
+            out.get_device() != device or len(a) != 4 or a[3] != 1 or b[3] != 1 or \
+            (a[0] | a[1] | a[2] | b[0] | b[1] | b[2]) & 7 or not (b[0] and b[1] and b[2]):
+        a = _strides(name, x, 4, device)
+        b = _strides(name + "_out", out, 4, device)
+        if any(n > 1 and s == 0 for n, s in zip(shape, b)):
             raise ValueError(f"{name}_out is a broadcast view")
-    B, H, N, _ = x.shape
-    dense = x.shape[3]
-    return _lib.RotaryRows(x.data_ptr(), out.data_ptr(), *(
-        s if n > 1 else dense for s, n in ((a[0], B), (a[1], H), (a[2], N),
-                                           (b[0], B), (b[1], H), (b[2], N))), H)
+    return _lib.RotaryRows(x.data_ptr(), out.data_ptr(), a[0], a[1], a[2], b[0], b[1], b[2],
+                           shape[1])
 
 
 def _turn(fn, q, q_out, k, k_out, positions, rotary, stream):
-    device = q.get_device() if q.is_cuda else -1
+    device = rotary.device
     rows_q = _rotary_rows(q, q_out, device, "q")
-    rows_k = None
     B, _, N, d = q.shape
+    rows_k = None
     if k is not None:
         rows_k = _rotary_rows(k, k_out, device, "k")
-        if (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
+        Bk, _, Nk, dk = k.shape
+        if Bk != B or Nk != N or dk != d:
             raise ValueError("k must be [B, H_kv, N, d] with q's B, N and d")
-    _same_device(device, rotary)
+        rows_k = _byref(rows_k)
+    if device != _device():
+        _same_device(device)
     if positions.dim() == 2:
         positions = positions[None]
-    _int32("positions", positions, 3, device)
-    if tuple(positions.shape) != (rotary.axes, B, N):
+    s = positions.stride()
+    if positions.dtype is not _I32 or positions.get_device() != device or len(s) != 3 or \
+            s[2] != 1:
+        _int32("positions", positions, 3, device)
+    if positions.shape != (rotary.axes, B, N):
         raise ValueError(f"positions have shape {tuple(positions.shape)}, expected "
                          f"{(rotary.axes, B, N)}")
-    _check(getattr(library(), fn)(
-        _byref(rows_q), None if rows_k is None else _byref(rows_k), B, N, d,
-        positions.data_ptr(), positions.stride(0), positions.stride(1), _byref(rotary._c),
-        _stream(stream)), fn)
+    status = getattr(library(), fn)(_byref(rows_q), rows_k, B, N, d, positions.data_ptr(), s[0],
+                                    s[1], rotary._ref, _stream(stream, device))
+    if status:
+        raise FaError(status, fn)
 
 
 def fa_rotary(q, q_out, k, k_out, positions, rotary, stream=None):
@@ -264,13 +277,17 @@ def rotary_backward(dq, dk, positions, rotary, stream=None):
 
 def _empty_rows(x):
     # (an expanded view's layout would keep its zero strides)
-    torch = _torch()
-    return torch.empty_like(x, memory_format=torch.contiguous_format if 0 in x.stride() else
-                            torch.preserve_format)
+    if 0 in x.stride():
+        return _torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return _torch.empty_like(x)
 
 
 def _new_turn(fn, q, k, positions, rotary, stream):
-    with _on(stream):
+    if stream is not None:
+        with _on(stream):
+            q_out = _empty_rows(q)
+            k_out = None if k is None else _empty_rows(k)
+    else:
         q_out = _empty_rows(q)
         k_out = None if k is None else _empty_rows(k)
     _turn(fn, q, q_out, k, k_out, positions, rotary, stream)
@@ -283,45 +300,50 @@ def fa_paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, q_o
     the cache, k turned by `rotary` at `positions` ([axes, T] int32, or [T] for one axis; None:
     each token's place in its sequence), and writes q [T, H_q, d] turned likewise to q_out."""
     device = cache.device
-    ks = _rows("k", k, 3, device)
-    vs = _rows("v", v, 3, device)
-    T, H, d = k.shape
-    if v.shape != k.shape or H != cache.H_kv or d != cache.d:
+    ks = _rows3("k", k, device)
+    vs = _rows3("v", v, device)
+    T, H, d = shape = k.shape
+    if v.shape != shape or H != cache.H_kv or d != cache.d:
         raise ValueError(f"k and v must be [T, {cache.H_kv}, {cache.d}]")
-    _same_device(device, batch, rotary)
-    if (q is None) != (q_out is None):
-        raise ValueError("give q and q_out, or neither")
+    if batch.device != device or device != _device() or \
+            (rotary is not None and rotary.device != device):
+        _same_device(device, batch, rotary)
     qp = op = None
-    qs, os, Hq = (0, 0), (0, 0), 0
-    if q is not None:
-        qs = _rows("q", q, 3, device)
-        os = _rows("q_out", q_out, 3, device)
-        Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != d or q_out.shape != q.shape:
+    q_token = q_head = o_token = o_head = Hq = 0
+    if q is not None and q_out is not None:
+        q_token, q_head, _ = _rows3("q", q, device)
+        o_token, o_head, _ = _rows3("q_out", q_out, device)
+        Tq, Hq, dq = q_shape = q.shape
+        if Tq != T or dq != d or q_out.shape != q_shape:
             raise ValueError(f"q and q_out must be [{T}, H_q, {d}]")
-        if Hq > 1 and os[1] == 0 or T > 1 and os[0] == 0:
-            raise ValueError("q_out is a broadcast view")
         qp, op = q.data_ptr(), q_out.data_ptr()
-    pp, axis_stride = None, 0
+    elif q is not None or q_out is not None:
+        raise ValueError("give q and q_out, or neither")
+    pp, axis_stride, ref = None, 0, None
+    if rotary is not None:
+        ref = rotary._ref
+        if rotary.rot_dim > d:
+            raise ValueError(f"rotary turns {rotary.rot_dim} values of {d}")
     if positions is not None:
         if rotary is None:
             raise ValueError("positions without rotary")
         if positions.dim() == 1:
             positions = positions[None]
-        _int32("positions", positions, 2, device)
-        if tuple(positions.shape) != (rotary.axes, T):
+        s = positions.stride()
+        if positions.dtype is not _I32 or positions.get_device() != device or len(s) != 2 or \
+                s[1] != 1:
+            _int32("positions", positions, 2, device)
+        if positions.shape != (rotary.axes, T):
             raise ValueError(f"positions have shape {tuple(positions.shape)}, expected "
                              f"{(rotary.axes, T)}")
-        pp, axis_stride = positions.data_ptr(), positions.stride(0)
-    if rotary is not None and rotary.rot_dim > d:
-        raise ValueError(f"rotary turns {rotary.rot_dim} values of {d}")
+        pp, axis_stride = positions.data_ptr(), s[0]
     if T == 0 or batch.S == 0:
         return
-    _check(library().fa_paged_append(
-        _byref(cache._c), _byref(batch._c), k.data_ptr(), _even(ks[0]), _even(ks[1]), v.data_ptr(),
-        _even(vs[0]), _even(vs[1]), T, qp, _even(qs[0]), _even(qs[1]), op, _even(os[0]) or d,
-        _even(os[1]) or d, Hq, None if rotary is None else _byref(rotary._c), pp, axis_stride,
-        _stream(stream)), "fa_paged_append")
+    status = library().fa_paged_append(
+        cache._ref, batch._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], T, qp,
+        q_token, q_head, op, o_token, o_head, Hq, ref, pp, axis_stride, _stream(stream, device))
+    if status:
+        raise FaError(status, "fa_paged_append")
 
 
 def paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, stream=None):
@@ -329,67 +351,70 @@ def paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, stream
     the last sequence are left as the allocation has them."""
     q_out = None
     if q is not None:
-        with _on(stream):
-            q_out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
+        if stream is not None:
+            with _on(stream):
+                q_out = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            q_out = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
     fa_paged_append(cache, batch, k, v, rotary, positions, q, q_out, stream)
     return q_out
-
-
-def _workspace_bytes(cache, batch, T, Hq):
-    return library().fa_forward_paged_workspace_bytes(Hq, cache.H_kv, cache.d, T,
-                                                      batch._c.max_q_len)
 
 
 def paged_workspace(cache, batch, q):
     """A workspace for fa_forward_paged calls of this shape.  Its contents do not matter, and
     calls on one stream may share it; calls that can overlap, such as two captured graphs,
     may not."""
-    torch = _torch()
     if q.dim() != 3 or q.shape[1] % cache.H_kv or q.shape[1] < 1:
         raise ValueError(f"q must be [T, H_q, {cache.d}] with H_q a multiple of {cache.H_kv}")
-    return torch.empty(_workspace_bytes(cache, batch, q.shape[0], q.shape[1]), dtype=torch.uint8,
-                       device=q.device)
+    n = library().fa_forward_paged_workspace_bytes(q.shape[1], cache.H_kv, cache.d, q.shape[0],
+                                                   batch._c.max_q_len)
+    return _torch.empty(n, dtype=_torch.uint8, device=q.device)
 
 
 def fa_forward_paged(cache, batch, q, o, lse, scale, causal, workspace, stream=None):
     """fa_forward_paged of include/fa.h: the step's q [T, H_q, d] (a bf16 view) against the
     cache; writes o (like q) and lse [T, H_q] fp32 (None: not wanted)."""
     device = cache.device
-    qs = _rows("q", q, 3, device)
-    os = _rows("o", o, 3, device)
-    T, Hq, d = q.shape
-    if d != cache.d or Hq < 1 or Hq % cache.H_kv or o.shape != q.shape:
+    q_token, q_head, _ = _rows3("q", q, device)
+    o_token, o_head, _ = _rows3("o", o, device)
+    T, Hq, d = shape = q.shape
+    if d != cache.d or o.shape != shape or Hq < 1 or Hq % cache.H_kv:
         raise ValueError(f"q and o must be [T, H_q, {cache.d}] with H_q a multiple of "
                          f"{cache.H_kv}")
-    _same_device(device, batch)
+    if batch.device != device or device != _device():
+        _same_device(device, batch)
     lp = None
     if lse is not None:
-        if lse.dtype is not _torch().float32 or lse.get_device() != device or \
-                not lse.is_contiguous() or tuple(lse.shape) != (T, Hq):
+        if lse.dtype is not _F32 or lse.get_device() != device or lse.shape != shape[:2] or \
+                not lse.is_contiguous():
             raise ValueError(f"lse must be a contiguous fp32 CUDA tensor [{T}, {Hq}]")
         lp = lse.data_ptr()
-    if Hq > 1 and os[1] == 0 or T > 1 and os[0] == 0:
-        raise ValueError("o is a broadcast view")
     if workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor of the cache's device")
     if T == 0 or batch.S == 0:
         return
-    _check(library().fa_forward_paged(
-        _byref(cache._c), _byref(batch._c), q.data_ptr(), _even(qs[0]), _even(qs[1]), o.data_ptr(),
-        _even(os[0]) or d, _even(os[1]) or d, lp, T, Hq, scale, int(bool(causal)),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
-        "fa_forward_paged")
+    status = library().fa_forward_paged(
+        cache._ref, batch._ref, q.data_ptr(), q_token, q_head, o.data_ptr(), o_token, o_head, lp,
+        T, Hq, scale, 1 if causal else 0, workspace.data_ptr(), workspace.nbytes,
+        _stream(stream, device))
+    if status:
+        raise FaError(status, "fa_forward_paged")
 
 
 def paged_attention(cache, batch, q, causal=True, scale=None, stream=None):
     """Allocates o, lse and the workspace and runs fa_forward_paged; returns (o, lse).  Rows
     past the last sequence are left as the allocations have them."""
-    torch = _torch()
+    if stream is not None:
+        with _on(stream):
+            return _paged_attention(cache, batch, q, causal, scale, stream)
+    return _paged_attention(cache, batch, q, causal, scale, stream)
+
+
+def _paged_attention(cache, batch, q, causal, scale, stream):
     if scale is None:
         scale = 1.0 / math.sqrt(cache.d)
-    with _on(stream):
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        workspace = paged_workspace(cache, batch, q)
-        fa_forward_paged(cache, batch, q, o, lse, scale, causal, workspace, stream)
+    o = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = _torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+    fa_forward_paged(cache, batch, q, o, lse, scale, causal, paged_workspace(cache, batch, q),
+                     stream)
     return o, lse
