@@ -88,6 +88,14 @@ struct PagedParams {
   uint32_t* err;
 };
 
+// a / b for a >= 0, b > 0; in 32 bits where they fit (a 64-bit division takes
+// some hundred cycles, and several lie in the way of a short call).
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 struct PagedSeq {
   int q0, qlen, klen;
 };
@@ -138,7 +146,7 @@ struct PagedWalk {
     g = paged_seq(p, s);
     n_rt = row_tiles(p, g);
     const long long per_head = head_units(p, g);
-    h = static_cast<int>(rem / per_head);
+    h = static_cast<int>(paged_div(rem, per_head));
     rem -= h * per_head;
     for (rt = 0; rt < n_rt - 1; ++rt) {
       const int t = my_tiles(p);
@@ -167,7 +175,7 @@ struct PagedRange {
   long long rem;
   // CTA whose range holds unit u.
   __device__ __forceinline__ int owner(long long u) const {
-    return static_cast<int>(((u + 1) * ctas - 1) / units);
+    return static_cast<int>(paged_div((u + 1) * ctas - 1, units));
   }
 };
 
@@ -212,13 +220,13 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
     r.units += all;
   }
   r.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x),
-                                (r.units + p.min_units - 1) / p.min_units));
+                                paged_div(r.units + p.min_units - 1, p.min_units)));
   r.seq = 0;
   r.rem = 0;
   r.first = r.end = 0;
   if (static_cast<int>(blockIdx.x) >= r.ctas) return r;  // block-uniform
-  r.first = blockIdx.x * r.units / r.ctas;
-  r.end = (blockIdx.x + 1) * r.units / r.ctas;
+  r.first = paged_div(blockIdx.x * r.units, r.ctas);
+  r.end = paged_div((blockIdx.x + 1) * r.units, r.ctas);
   if (tid == 0) scratch[32] = scratch[33] = 0;
   __syncthreads();
   long long done = 0;

@@ -135,20 +135,31 @@ __device__ __forceinline__ float paged_load_q(const PagedParams& p, const PagedR
 template <int D, int BN>
 __device__ __forceinline__ void paged_convert(uint32_t raw, uint32_t dst, int keep, int tid) {
   constexpr int PER = 128 / BN;  // threads a row
+  constexpr int N = 4;           // chunks of 16 values in flight
   const int r = tid % BN;
-#pragma unroll 4
-  for (int c = tid / BN; c < D / 16; c += PER) {
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (r < keep) {
-      const uint4 v = lds128(raw + (c >> 3) * (BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-      lo = make_uint4(e4m3x2_f16x2(v.x), e4m3x2_f16x2(v.x >> 16), e4m3x2_f16x2(v.y),
-                      e4m3x2_f16x2(v.y >> 16));
-      hi = make_uint4(e4m3x2_f16x2(v.z), e4m3x2_f16x2(v.z >> 16), e4m3x2_f16x2(v.w),
-                      e4m3x2_f16x2(v.w >> 16));
+  const bool key = r < keep;
+#pragma unroll
+  for (int c0 = 0; c0 < D / 16; c0 += N * PER) {
+    uint4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = c0 + i * PER + (PER == 1 ? 0 : tid / BN);
+      if (c < D / 16)
+        v[i] = lds128(raw + (c >> 3) * (BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
     }
-    const uint32_t blk = dst + (c >> 2) * (BN * 128) + r * 128;
-    sts128(blk + ((((c & 3) * 2) ^ (r & 7)) << 4), lo);
-    sts128(blk + ((((c & 3) * 2 + 1) ^ (r & 7)) << 4), hi);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = c0 + i * PER + (PER == 1 ? 0 : tid / BN);
+      if (c >= D / 16) continue;
+      if (!key) v[i] = make_uint4(0, 0, 0, 0);  // (+0 in both formats)
+      const uint32_t blk = dst + (c >> 2) * (BN * 128) + r * 128;
+      sts128(blk + ((((c & 3) * 2) ^ (r & 7)) << 4),
+             make_uint4(e4m3x2_f16x2(v[i].x), e4m3x2_f16x2(v[i].x >> 16), e4m3x2_f16x2(v[i].y),
+                        e4m3x2_f16x2(v[i].y >> 16)));
+      sts128(blk + ((((c & 3) * 2 + 1) ^ (r & 7)) << 4),
+             make_uint4(e4m3x2_f16x2(v[i].z), e4m3x2_f16x2(v[i].z >> 16), e4m3x2_f16x2(v[i].w),
+                        e4m3x2_f16x2(v[i].w >> 16)));
+    }
   }
 }
 
@@ -240,12 +251,14 @@ __device__ __forceinline__ void paged_rescale(uint32_t o_addr, float alpha) {
   }
 }
 
-// A row's O out of TMEM: the result if its item lies whole in this CTA, else
-// its part, at row `part_row` of the parts.
-template <int D>
+// A row's O out of TMEM (TWO: fa times the one at o_addr plus fb times the one
+// at o_addr2): the result if its item lies whole in this CTA, else its part, at
+// row `part_row` of the parts.
+template <int D, bool TWO>
 __device__ __forceinline__ void paged_store_row(const PagedParams& p, const PagedRow& x,
-                                                uint32_t o_addr, bool whole, long long part_row,
-                                                float m, float l) {
+                                                uint32_t o_addr, uint32_t o_addr2, float fa,
+                                                float fb, bool whole, long long part_row, float m,
+                                                float l) {
   const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
   __nv_bfloat16* dst = p.o + x.token * p.o_token + x.head * p.o_head;
   float* part = p.part_o + part_row * D;
@@ -253,7 +266,16 @@ __device__ __forceinline__ void paged_store_row(const PagedParams& p, const Page
   for (int q4 = 0; q4 < D / 32; ++q4) {
     uint32_t v[32];
     tmem_ld32(o_addr + q4 * 32, v);
-    tmem_wait_ld();
+    if constexpr (TWO) {
+      uint32_t w[32];
+      tmem_ld32(o_addr2 + q4 * 32, w);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        v[k] = __float_as_uint(__uint_as_float(v[k]) * fa + __uint_as_float(w[k]) * fb);
+    } else {
+      tmem_wait_ld();
+    }
     if (!x.live) continue;
     if (whole) {
 #pragma unroll

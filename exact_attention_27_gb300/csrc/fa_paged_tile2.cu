@@ -21,12 +21,15 @@
 //               scores of this one are there, so before the epilogue.
 //   warp 8      TMA producer: one box per page and 128-byte column block.
 //   warp 9      MMA issuer and TMEM owner, per key tile:
-//               O_A += P_A V, S_A of the next tile, O_B += P_B V, next S_B.
+//               O_A += P_A V, S_A of the next tile, O_B += P_B V, next S_B:
+//               each S as soon as its tile's last one is used up.
 //   the helpers (bf16 pages: warps 10 and 11; e4m3: warps 12-15, 10 and 11
 //               being idle): V's rows past the last key made 0 (their p is 0,
 //               but the page may hold anything there); e4m3 pages: K and V from
 //               bytes to fp16 tiles, which both tiles then use.
-// An item of at most 128 rows has no tile B; its warps and products skip it.
+// An item of at most 128 rows (single tokens, among chunks) has its rows in both
+// tiles: A takes its even and B its odd key tiles, so that softmax and products
+// still overlap, and A's warps join (O, m, l) of both, out of tensor memory.
 // Registers: bf16 384 threads at 168: 224 / 224 / 56; e4m3 512 at 128: 200 /
 // 200 / 56 / 56 (the sums are the launch totals 504 and 512).
 //
@@ -70,7 +73,8 @@ struct Tile2Cfg {
   static constexpr int OFF_V = OFF_K + NS * TILE;
   static constexpr int OFF_RAW = OFF_V + NS * TILE;
   static constexpr int OFF_SCR = OFF_RAW + NR * BLOCK;
-  static constexpr int OFF_BAR = OFF_SCR + 40 * 8;
+  static constexpr int OFF_ML = OFF_SCR + 40 * 8;  // [128] (m, l) of B's half of a split item
+  static constexpr int OFF_BAR = OFF_ML + 128 * 8;
   static constexpr int HELPERS = E4M3 ? 4 : 2;   // warps
   static constexpr int B_QFULL = 0;              // [2] 4 warps
   static constexpr int B_KFULL = B_QFULL + 2;    // [NS] bytes (e4m3: the helpers)
@@ -83,7 +87,9 @@ struct Tile2Cfg {
   static constexpr int B_SFULL = B_REMPTY + NR;  // [2] S of tile x
   static constexpr int B_PFULL = B_SFULL + 2;    // [2] 4 warps
   static constexpr int B_ODONE = B_PFULL + 2;    // [2] O_x += P_x V
-  static constexpr int B_DRAIN = B_ODONE + 2;
+  static constexpr int B_SPLIT = B_ODONE + 2;    // 4 warps: B's half of a split item is final
+  static constexpr int B_JOINED = B_SPLIT + 1;   // 4 warps: A has read it
+  static constexpr int B_DRAIN = B_JOINED + 1;
   static constexpr int NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
@@ -127,6 +133,8 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       mbar_init(bar(C::B_RFULL + s), 1);
       mbar_init(bar(C::B_REMPTY + s), C::HELPERS);
     }
+    mbar_init(bar(C::B_SPLIT), 4);
+    mbar_init(bar(C::B_JOINED), 4);
     mbar_init(bar(C::B_DRAIN), 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -157,8 +165,8 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
   const uint32_t sR = sbase + C::OFF_RAW;
 
   Seg seg;
-  // Whether the item has rows in tile B.
-  auto has_b = [&](const Seg& s) -> bool { return s.w.g.qlen * p.G - s.w.rt * C::BM > 128; };
+  // Whether the item's rows fill one tile only, and its key tiles go in turn to A and B.
+  auto split = [&](const Seg& s) -> bool { return s.w.g.qlen * p.G - s.w.rt * C::BM <= 128; };
 
   if (warp >= 8) {
     reg_decrease<56>();
@@ -246,15 +254,32 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
         auto wait = [&](int b, uint32_t parity) {
           return mbar_wait(bar(b), parity, abort_flag, p.err, kErrTimeoutMma);
         };
-        uint32_t items[2] = {0, 0};  // items whose Q tile x was waited for
-        uint32_t done[2] = {0, 0};   // products P_x V issued
-        // S_x = Q_x K^T of key tile n; `first`: the item's first.
-        auto issue_s = [&](int x, int n, bool first) -> bool {
-          if (first && !wait(C::B_QFULL + x, items[x]++ & 1)) return false;
+        // Parities of the next Q (bits 0, 1) and P (bits 2, 3) of each tile; in
+        // registers, as the issuer's own latency lies between P and O += P V.
+        uint32_t phase = 0;
+        // Products S, in order of the key tiles (A before B), run ahead of the
+        // products P V, which follow in the same order: at most one S a tile is
+        // waiting for its P.  job0 and job1 are those: bit 0 tile, bit 1 the item's
+        // first of the tile, bit 2 the key tile's last use, key tile above.
+        uint32_t job0 = 0, job1 = 0;
+        int waiting = 0, v_tile = -1;
+        seg.start(p, range);
+        bool have = true, sp = split(seg);
+        int t = seg.t0, x = 0, n = 0;
+        bool k_ready = false;
+        auto issue_s = [&]() -> bool {
+          const bool first = sp ? t - seg.t0 < 2 : t == seg.t0;
+          const int st = n % C::NS;
+          if (first) {
+            if (!wait(C::B_QFULL + x, (phase >> x) & 1)) return false;
+            phase ^= 1u << x;
+          }
+          if (!k_ready && !wait(C::B_KFULL + st, (n / C::NS) & 1)) return false;
+          k_ready = true;
           tc_fence_after();
           const uint32_t d_tmem = tmem + x * 128;
           const uint64_t qd = desc_add(q_desc, x * C::TILE);
-          const uint64_t kd = desc_add(k_desc, (n % C::NS) * C::TILE);
+          const uint64_t kd = desc_add(k_desc, st * C::TILE);
           mma_ss_k<ID_S, 0>(d_tmem, qd, kd);
 #pragma unroll
           for (int kk = 1; kk < D / 16; ++kk) {
@@ -262,55 +287,57 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
             mma_ss_k<ID_S, 1>(d_tmem, desc_add(qd, off), desc_add(kd, off));
           }
           mma_commit(bar(C::B_SFULL + x));
+          const bool last = sp || x == 1;
+          if (last) mma_commit(bar(C::B_KEMPTY + st));
+          const uint32_t job = (static_cast<uint32_t>(n) << 3) | (last ? 4u : 0u) |
+                               (first ? 2u : 0u) | static_cast<uint32_t>(x);
+          if (waiting == 0)
+            job0 = job;
+          else
+            job1 = job;
+          ++waiting;
+          // The next S: tile B of the same keys, or the next key tile.
+          x ^= 1;
+          if (last) {
+            ++n;
+            k_ready = false;
+            if (++t == seg.t1) {
+              have = seg.next(p);
+              t = x = 0;
+              sp = have && split(seg);
+            }
+          }
           return true;
         };
-        seg.start(p, range);
-        bool b = has_b(seg), first = true;
-        bool ok = wait(C::B_KFULL, 0) && issue_s(0, 0, true) && (!b || issue_s(1, 0, true));
-        if (ok) mma_commit(bar(C::B_KEMPTY));
-        int t = seg.t0;
-        for (int n = 0; ok; ++n) {
-          const int st = n % C::NS, sn = (n + 1) % C::NS;
-          // The next key tile, of this item or the next.
-          bool more = true, next_b = b, next_first = false;
-          if (++t == seg.t1) {
-            more = seg.next(p);
-            t = 0;
-            next_first = true;
-            next_b = more && has_b(seg);
+        bool ok = true;
+        while (true) {
+          while (ok && have && (waiting == 0 || (waiting == 1 && (job0 & 1) != static_cast<uint32_t>(x))))
+            ok = issue_s();
+          if (!ok || waiting == 0) break;
+          const uint32_t job = job0;
+          job0 = job1;
+          --waiting;
+          const int y = job & 1, tile = job >> 3, st = tile % C::NS;
+          if (tile != v_tile) {
+            ok = (E4M3 || wait(C::B_VFULL + st, (tile / C::NS) & 1)) &&
+                 wait(C::B_VFIX + st, (tile / C::NS) & 1);
+            v_tile = tile;
           }
-          ok = (E4M3 || wait(C::B_VFULL + st, (n / C::NS) & 1)) &&
-               wait(C::B_VFIX + st, (n / C::NS) & 1);
-          bool k_ready = false;
-#pragma unroll 1
-          for (int x = 0; ok && x < 2; ++x) {
-            if (x == 0 || b) {
-              if (!(ok = wait(C::B_PFULL + x, done[x]++ & 1))) break;
-              tc_fence_after();
-              const uint64_t vd = desc_add(v_desc, st * C::TILE);
-              const uint32_t pa = tmem + x * 128;
-              const uint32_t od = tmem + C::COL_O + x * C::DP;
-              if (first)
-                mma_ts_k<ID_O, 0>(od, pa, vd);
-              else
-                mma_ts_k<ID_O, 1>(od, pa, vd);
+          if (!ok || !(ok = wait(C::B_PFULL + y, (phase >> (2 + y)) & 1))) break;
+          phase ^= 4u << y;
+          tc_fence_after();
+          const uint64_t vd = desc_add(v_desc, st * C::TILE);
+          const uint32_t pa = tmem + y * 128;
+          const uint32_t od = tmem + C::COL_O + y * C::DP;
+          if (job & 2)
+            mma_ts_k<ID_O, 0>(od, pa, vd);
+          else
+            mma_ts_k<ID_O, 1>(od, pa, vd);
 #pragma unroll
-              for (int kk = 1; kk < BN / 16; ++kk)
-                mma_ts_k<ID_O, 1>(od, pa + kk * 8, desc_add(vd, kk * 2048));
-              mma_commit(bar(C::B_ODONE + x));
-            }
-            if (more && (x == 0 || next_b)) {
-              if (!k_ready && !(ok = wait(C::B_KFULL + sn, ((n + 1) / C::NS) & 1))) break;
-              k_ready = true;
-              if (!(ok = issue_s(x, n + 1, next_first))) break;
-            }
-          }
-          if (!ok) break;
-          mma_commit(bar(C::B_VEMPTY + st));
-          if (!more) break;
-          mma_commit(bar(C::B_KEMPTY + sn));
-          b = next_b;
-          first = next_first;
+          for (int kk = 1; kk < BN / 16; ++kk)
+            mma_ts_k<ID_O, 1>(od, pa + kk * 8, desc_add(vd, kk * 2048));
+          mma_commit(bar(C::B_ODONE + y));
+          if (job & 4) mma_commit(bar(C::B_VEMPTY + st));
         }
         if (*abort_flag) {
           // Let the MMAs already issued finish before tensor memory is released.
@@ -372,41 +399,50 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
     auto wait = [&](int b, uint32_t parity, uint32_t code) {
       return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, p.err, code)) != 0;
     };
-    // The next item with rows in this tile (the one at hand if it has).
+    // The next item with work for this tile (the one at hand if it has): a
+    // split item of one key tile has none for B.
     auto settle = [&](bool have) {
-      while (have && x == 1 && !has_b(seg)) have = seg.next(p);
+      while (have && x == 1 && split(seg) && seg.t1 - seg.t0 == 1) have = seg.next(p);
       return have;
     };
-    auto load_q = [&](const PagedRow& r) -> float {
+    auto load_q = [&](PagedRow& r) -> float {
+      r = paged_row(p, seg, (split(seg) ? 0 : x * 128) + row);
       const float c = paged_load_q<D, E4M3>(p, r, sQ + x * C::TILE, row);
       fence_proxy_async_smem();
       mbar_arrive_warp(bar(C::B_QFULL + x));
       return c;
     };
+    float2* half_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     seg.start(p, range);
     bool have = settle(true), ok = true;
     PagedRow r{};
     float c = 0.0f;
-    if (have) {
-      r = paged_row(p, seg, x * 128 + row);
-      c = load_q(r);
-    }
-    uint32_t n = 0;  // tiles of this warpgroup
+    if (have) c = load_q(r);
+    uint32_t n = 0;       // key tiles of this warpgroup
+    uint32_t joins = 0;   // split items of both warpgroups
+    bool unread = false;  // B: A may still be reading this O
     while (have) {
       float m = -INFINITY;  // reference maximum, log2 domain
       float l = 0.0f;
-      for (int t = seg.t0; t < seg.t1; ++t, ++n) {
+      const bool sp = split(seg);
+      const int t_first = sp ? seg.t0 + x : seg.t0;
+      for (int t = t_first; t < seg.t1; t += sp ? 2 : 1, ++n) {
         if (!(ok = wait(C::B_SFULL + x, n & 1, kErrTimeoutSoftmax))) break;
         tc_fence_after();
         bool moved;
         const float alpha = paged_softmax<BN, E4M3>(s_addr, t * BN + BN - 1 > r.all_see,
                                                     r.last - t * BN, c, m, l, moved);
-        if (t > seg.t0 && __any_sync(0xffffffffu, moved)) {
+        if (t > t_first && __any_sync(0xffffffffu, moved)) {
           // O is final before it is rescaled (S of this tile was issued after
           // O += P V of the one before, so this does not wait long).
           if (!(ok = wait(C::B_ODONE + x, (n - 1) & 1, kErrTimeoutSoftmax))) break;
           tc_fence_after();
           paged_rescale<D>(o_addr, alpha);
+        }
+        if (unread) {
+          // The product that this P allows overwrites O.
+          if (!(ok = wait(C::B_JOINED, (joins - 1) & 1, kErrTimeoutSoftmax))) break;
+          unread = false;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -417,18 +453,35 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       // Its last scores have been read, so Q's tile is free.
       const PagedRow now = r;
       const bool whole = seg.t0 == 0 && seg.t1 == seg.tiles;
-      const int slot = cta * 2 + (seg.t0 == 0 ? 1 : 0);
+      const bool both = sp && seg.t1 - seg.t0 > 1;
+      const long long part =
+          static_cast<long long>(cta * 2 + (seg.t0 == 0 ? 1 : 0)) * C::BM + (sp ? 0 : x * 128) + row;
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
         p.notes[cta] = paged_note<C::BM, BN>(p, range, seg.w, seg.unit);
       have = settle(seg.next(p));
-      if (have) {
-        r = paged_row(p, seg, x * 128 + row);
-        c = load_q(r);
-      }
+      if (have) c = load_q(r);
       if (!(ok = wait(C::B_ODONE + x, (n - 1) & 1, kErrTimeoutEpilogue))) break;
       tc_fence_after();
-      paged_store_row<D>(p, now, o_addr, whole,
-                         static_cast<long long>(slot) * C::BM + x * 128 + row, m, l);
+      if (!both) {
+        paged_store_row<D, false>(p, now, o_addr, 0, 1.0f, 0.0f, whole, part, m, l);
+      } else if (x == 1) {
+        half_ml[row] = make_float2(m, l);
+        tc_fence_before();
+        mbar_arrive_warp(bar(C::B_SPLIT));
+        ++joins;
+        unread = true;
+      } else {
+        if (!(ok = wait(C::B_SPLIT, joins++ & 1, kErrTimeoutEpilogue))) break;
+        tc_fence_after();
+        const float2 b = half_ml[row];
+        const float m2 = fmaxf(m, b.x);
+        const float ref = m2 == -INFINITY ? 0.0f : m2;
+        const float fa = ex2_approx(m - ref), fb = ex2_approx(b.x - ref);
+        paged_store_row<D, true>(p, now, o_addr, o_addr + C::DP, fa, fb, whole, part, m2,
+                                 l * fa + b.y * fb);
+        tc_fence_before();
+        mbar_arrive_warp(bar(C::B_JOINED));
+      }
       tc_fence_before();
       // (The next item's first O product waits for this thread's next P.)
     }

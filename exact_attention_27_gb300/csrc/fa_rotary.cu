@@ -12,13 +12,13 @@
 // 2^-5 radians.  The top 32 bits, as a signed fraction in [-1/2, 1/2), go to
 // sincospif.
 //
-// Both kernels are bound by memory: they read and write every row once (3
-// operations for 4 bytes of traffic).  The angles of a position are shared by
-// all its heads, so a block takes one position (few positions: blocks for more
-// of the SMs) or four (many: one thread computes one sine and cosine, which
-// 2 x heads values use), keeps the cosines in shared memory, and then streams
-// the rows of all heads, each thread one pair of 16-byte vectors at a time with
-// kBatch of them in flight.
+// Both are bound by memory: they read and write every row once (3 operations
+// for 4 bytes of traffic).  The angles of a position are shared by all its
+// heads: a block takes TOK positions, one thread makes one sine and cosine, and
+// a thread then keeps those of its 8 pairs in registers and goes through the
+// heads, two at a time, the first two loaded before the angles are made.  TOK is
+// 1 for few positions (blocks for more of the SMs), else what gives a thread
+// some heads to go through.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -35,7 +35,7 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;       // units a thread loads before it turns the first
+constexpr int kBatch = 2;       // heads a thread loads at a time
 constexpr int kMaxPairs = 128;  // rot_dim / 2 at d = 256
 
 enum { kTurnOnly = 0, kToBf16 = 1, kToE4m3 = 2 };  // where k (and v) rows go
@@ -67,7 +67,7 @@ struct TurnParams {
   long long page_stride, row_stride, head_stride;
   void* k_pages;
   void* v_pages;
-  float k_descale, v_descale;
+  float k_scale, v_scale;  // 1 / descale
   uint32_t* err;
 };
 
@@ -99,16 +99,16 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// TOK positions a block; a unit is 16 values of a row: two 16-byte vectors
-// that hold 8 whole pairs (or 16 values past rot_dim).
+// A unit is 16 values of a row: two 16-byte vectors that hold 8 whole pairs
+// (or 16 values past rot_dim).  Thread: unit u of token tt, heads hg, hg + HG, ...
 template <int D, int TOK, int TO>
-__global__ void __launch_bounds__(kThreads) fa_turn_kernel(const __grid_constant__ TurnParams p) {
+__global__ void __launch_bounds__(kThreads, 3) fa_turn_kernel(const __grid_constant__ TurnParams p) {
   constexpr int UNITS = D / 16;
+  constexpr int HG = kThreads / (UNITS * TOK);
+  static_assert(HG >= 1, "threads");
   __shared__ float2 cs[TOK][kMaxPairs];
   __shared__ long long place[TOK];  // cache offset of the token's row in head 0; -1: not stored
-  __shared__ int at_b[TOK], at_n[TOK];
   __shared__ int seq_pos[TOK];      // place in the sequence; INT_MIN: no sequence
-  __shared__ unsigned char axis[kMaxPairs];
 
   grid_dependency_wait();
   grid_launch_dependents();
@@ -116,20 +116,51 @@ __global__ void __launch_bounds__(kThreads) fa_turn_kernel(const __grid_constant
   const int tid = threadIdx.x;
   const long long t0 = static_cast<long long>(blockIdx.x) * TOK;
   const int half = p.half;
+  const int u = tid % UNITS, tt = tid / UNITS % TOK, hg = tid / (UNITS * TOK);
+  const long long t = t0 + tt;
+  const bool here = hg < HG && t < p.tokens;
+  const long long b = TO == kTurnOnly ? t / p.N : 0;
+  const long long n = t - b * p.N;
+  // The unit's first vector and the distance to its second, in elements.
+  const bool turned = u < half / 8;
+  const int first = p.interleaved ? 16 * u : turned ? 8 * u : 2 * half + 16 * (u - half / 8);
+  const int gap = p.interleaved || !turned ? 8 : half;
+  const int heads = p.q.heads + p.k.heads + p.v.heads;
+  // Head h counts through q, k and v.
+  auto source = [&](int h) -> const __nv_bfloat16* {
+    if (h < p.q.heads) return p.q.in + (b * p.q.ib + n * p.q.ip + h * p.q.ih + first);
+    h -= p.q.heads;
+    if (h < p.k.heads) return p.k.in + (b * p.k.ib + n * p.k.ip + h * p.k.ih + first);
+    return p.v.in + (n * p.v.ip + (h - p.k.heads) * p.v.ih + first);
+  };
+  uint4 lo[kBatch], hi[kBatch];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * HG;
+      if (here && h < heads) {
+        const __nv_bfloat16* src = source(h);
+        lo[i] = *reinterpret_cast<const uint4*>(src);
+        hi[i] = *reinterpret_cast<const uint4*>(src + gap);
+      }
+    }
+  };
+  load(hg);
+
   if (TO != kTurnOnly) {
-    // Warp w finds token w: its sequence is the number of starts q_start[1..S]
-    // at or below it, counted by all lanes.
-    const int w = tid >> 5, lane = tid & 31;
-    if (w < TOK) {
-      const long long t = t0 + w;
+    // Warp w finds token w (TOK / 8 rounds): its sequence is the number of
+    // starts q_start[1..S] at or below it, counted by all lanes.
+    const int lane = tid & 31;
+    for (int w = tid >> 5; w < TOK; w += kThreads / 32) {
+      const long long tw = t0 + w;
       int below = 0;
-      for (int i = lane; i < p.S; i += 32) below += p.q_start[i + 1] <= t;
+      for (int i = lane; i < p.S; i += 32) below += p.q_start[i + 1] <= tw;
       const int s = __reduce_add_sync(0xffffffffu, below);
       if (lane == 0) {
         int pos = INT_MIN;
         long long where = -1;
-        if (t < p.tokens && s < p.S && t >= p.q_start[s]) {
-          pos = static_cast<int>(p.kv_len[s] - (p.q_start[s + 1] - t));
+        if (tw < p.tokens && s < p.S && tw >= p.q_start[s]) {
+          pos = static_cast<int>(p.kv_len[s] - (p.q_start[s + 1] - tw));
           const int slot = pos < 0 ? 0 : pos / p.page_size;
           if (pos >= 0 && slot < p.max_pages) {
             const int page = p.table[s * p.table_stride + slot];
@@ -143,113 +174,76 @@ __global__ void __launch_bounds__(kThreads) fa_turn_kernel(const __grid_constant
         }
         place[w] = where;
         seq_pos[w] = pos;
-        at_b[w] = 0;
-        at_n[w] = static_cast<int>(t);
       }
     }
-  } else if (tid < TOK) {
-    const long long t = t0 + tid;
-    at_b[tid] = static_cast<int>(t / p.N);
-    at_n[tid] = static_cast<int>(t % p.N);
-    seq_pos[tid] = t < p.tokens ? 0 : INT_MIN;
+    __syncthreads();
   }
-  if (tid < half) axis[tid] = p.axis[tid];
-  __syncthreads();
   for (int i = tid; i < TOK * half; i += kThreads) {
-    const int tt = i / half, pair = i - tt * half;
-    int pos = seq_pos[tt];
-    if (pos == INT_MIN) continue;
-    if (p.positions)
-      pos = p.positions[axis[pair] * p.axis_stride + at_b[tt] * p.batch_stride + at_n[tt]];
-    cs[tt][pair] = cos_sin(pos, turn_fraction(p.inv_freq[pair]), p.sign);
+    const int w = i / half, pair = i - w * half;
+    const long long tw = t0 + w;
+    if (tw >= p.tokens) break;
+    int pos = TO == kTurnOnly ? 0 : seq_pos[w];
+    if (p.positions) {
+      const long long bw = TO == kTurnOnly ? tw / p.N : 0;
+      pos = p.positions[p.axis[pair] * p.axis_stride + bw * p.batch_stride + (tw - bw * p.N)];
+    }
+    cs[w][pair] = cos_sin(pos, turn_fraction(p.inv_freq[pair]), p.sign);
   }
   __syncthreads();
+  if (!here || (TO != kTurnOnly && seq_pos[tt] == INT_MIN)) return;
 
-  const int rows = p.q.heads + p.k.heads + p.v.heads;
-  const int total = rows * TOK * UNITS;
-  const int turned = half / 8;  // units of a row that are turned
-  for (int base = tid; base < total; base += kThreads * kBatch) {
-    uint4 a[kBatch], b[kBatch];
-    // The unit's first vector and the distance to its second, in elements.
-    auto vectors = [&](int u, int& first, int& gap) {
-      if (u >= turned || p.interleaved) {
-        first = p.interleaved || u < turned ? 16 * u : 2 * half + 16 * (u - turned);
-        gap = 8;
-      } else {
-        first = 8 * u;
-        gap = half;
-      }
-    };
-    // Row r: which tensor, and its head.
-    auto tensor = [&](int r, int& h) -> int {
-      if (r < p.q.heads) return h = r, 0;
-      r -= p.q.heads;
-      if (r < p.k.heads) return h = r, 1;
-      return h = r - p.k.heads, 2;
-    };
+  float2 t8[8];
 #pragma unroll
-    for (int n = 0; n < kBatch; ++n) {
-      const int i = base + n * kThreads;
-      const int u = i % UNITS, tt = i / UNITS % TOK;
-      if (i >= total || seq_pos[tt] == INT_MIN) continue;
-      int h, first, gap;
-      const int which = tensor(i / (UNITS * TOK), h);
-      const Rows& R = which == 0 ? p.q : which == 1 ? p.k : p.v;
-      vectors(u, first, gap);
-      const __nv_bfloat16* src = R.in + at_b[tt] * R.ib + h * R.ih + at_n[tt] * R.ip + first;
-      a[n] = *reinterpret_cast<const uint4*>(src);
-      b[n] = *reinterpret_cast<const uint4*>(src + gap);
-    }
+  for (int e = 0; e < 8; ++e) t8[e] = turned ? cs[tt][8 * u + e] : make_float2(1.0f, 0.0f);
+  const long long row = TO == kTurnOnly ? 0 : place[tt];
+  for (int h0 = hg; h0 < heads; h0 += kBatch * HG) {
 #pragma unroll
-    for (int n = 0; n < kBatch; ++n) {
-      const int i = base + n * kThreads;
-      const int u = i % UNITS, tt = i / UNITS % TOK;
-      if (i >= total || seq_pos[tt] == INT_MIN) continue;
-      int h, first, gap;
-      const int which = tensor(i / (UNITS * TOK), h);
-      vectors(u, first, gap);
+    for (int i = 0; i < kBatch; ++i) {
+      int h = h0 + i * HG;
+      if (h >= heads) break;
       float x[8], y[8];
-      unpack8(a[n], x);
-      unpack8(b[n], y);
-      if (which != 2 && u < turned) {
-        const float2* t = &cs[tt][8 * u];
+      unpack8(lo[i], x);
+      unpack8(hi[i], y);
+      const bool is_q = h < p.q.heads, is_v = h >= p.q.heads + p.k.heads;
+      if (turned && !is_v) {
         if (p.interleaved) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float x0 = x[2 * e], x1 = x[2 * e + 1], y0 = y[2 * e], y1 = y[2 * e + 1];
-            x[2 * e] = x0 * t[e].x - x1 * t[e].y;
-            x[2 * e + 1] = x0 * t[e].y + x1 * t[e].x;
-            y[2 * e] = y0 * t[e + 4].x - y1 * t[e + 4].y;
-            y[2 * e + 1] = y0 * t[e + 4].y + y1 * t[e + 4].x;
+            x[2 * e] = x0 * t8[e].x - x1 * t8[e].y;
+            x[2 * e + 1] = x0 * t8[e].y + x1 * t8[e].x;
+            y[2 * e] = y0 * t8[e + 4].x - y1 * t8[e + 4].y;
+            y[2 * e + 1] = y0 * t8[e + 4].y + y1 * t8[e + 4].x;
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float x0 = x[e], y0 = y[e];
-            x[e] = x0 * t[e].x - y0 * t[e].y;
-            y[e] = x0 * t[e].y + y0 * t[e].x;
+            x[e] = x0 * t8[e].x - y0 * t8[e].y;
+            y[e] = x0 * t8[e].y + y0 * t8[e].x;
           }
         }
       }
-      if (TO == kTurnOnly || which == 0) {
-        const Rows& R = which == 0 ? p.q : p.k;
-        __nv_bfloat16* dst = R.out + at_b[tt] * R.ob + h * R.oh + at_n[tt] * R.op + first;
+      if (TO == kTurnOnly || is_q) {
+        const Rows& R = is_q ? p.q : p.k;
+        __nv_bfloat16* dst =
+            R.out + (b * R.ob + n * R.op + (is_q ? h : h - p.q.heads) * R.oh + first);
         *reinterpret_cast<uint4*>(dst) = pack8(x);
         *reinterpret_cast<uint4*>(dst + gap) = pack8(y);
-      } else if (place[tt] >= 0) {
-        const long long off = place[tt] + h * p.head_stride + first;
+      } else if (row >= 0) {
+        h -= is_v ? p.q.heads + p.k.heads : p.q.heads;
+        const long long off = row + h * p.head_stride + first;
         if (TO == kToBf16) {
-          __nv_bfloat16* dst =
-              static_cast<__nv_bfloat16*>(which == 1 ? p.k_pages : p.v_pages) + off;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.v_pages : p.k_pages) + off;
           *reinterpret_cast<uint4*>(dst) = pack8(x);
           *reinterpret_cast<uint4*>(dst + gap) = pack8(y);
         } else {
-          uint8_t* dst = static_cast<uint8_t*>(which == 1 ? p.k_pages : p.v_pages) + off;
-          const float ds = which == 1 ? p.k_descale : p.v_descale;
+          uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + off;
+          const float f = is_v ? p.v_scale : p.k_scale;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            x[e] = x[e] / ds;
-            y[e] = y[e] / ds;
+            x[e] *= f;
+            y[e] *= f;
           }
           *reinterpret_cast<uint2*>(dst) =
               make_uint2(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]));
@@ -258,19 +252,22 @@ __global__ void __launch_bounds__(kThreads) fa_turn_kernel(const __grid_constant
         }
       }
     }
+    load(h0 + kBatch * HG);
   }
 }
 
-// Four positions a block once that still gives every SM several blocks.
-constexpr long long kManyTokens = 4 * 4 * 152;
-
 template <int D, int TO>
 cudaError_t launch_turn_d(const TurnParams& p, cudaStream_t stream) {
-  const bool many = p.tokens >= kManyTokens;
-  const long long grid = many ? (p.tokens + 3) / 4 : p.tokens;
+  const int heads = p.q.heads + p.k.heads + p.v.heads;
+  // One position a block below two blocks an SM of more; then the most that
+  // leaves a thread about four heads.
+  const int tok = p.tokens < 8 * 152 ? 1 : heads * (D / 16) * 16 <= 6 * kThreads ? 16 : 4;
+  const long long grid = (p.tokens + tok - 1) / tok;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_dependent(many ? fa_turn_kernel<D, 4, TO> : fa_turn_kernel<D, 1, TO>,
-                          dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, p);
+  auto kern = tok == 1 ? fa_turn_kernel<D, 1, TO>
+              : tok == 4 ? fa_turn_kernel<D, 4, TO>
+                         : fa_turn_kernel<D, 16, TO>;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, p);
 }
 
 template <int TO>
@@ -439,8 +436,8 @@ fa_status fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* bat
   p.head_stride = cache->head_stride;
   p.k_pages = cache->k;
   p.v_pages = cache->v;
-  p.k_descale = cache->k_descale;
-  p.v_descale = cache->v_descale;
+  p.k_scale = 1.0f / cache->k_descale;
+  p.v_scale = 1.0f / cache->v_descale;
   const cudaError_t e = cache->dtype == FA_CACHE_BF16 ? launch_turn<kToBf16>(p, cache->d, stream)
                                                       : launch_turn<kToE4m3>(p, cache->d, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;

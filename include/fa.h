@@ -363,8 +363,8 @@ typedef struct {
  *   spec   NULL: nothing is turned (q is copied)
  *   positions  device int32, entry (axis, t) at positions[axis * axis_stride + t];
  *          NULL: each token's place in its sequence, on every axis
- * An e4m3 cache stores value / descale rounded once from fp32 (nearest even),
- * saturated at 448.  Rows of k, v and q past q_start[S] belong to no sequence:
+ * An e4m3 cache stores value * (1 / descale), an fp32 product, rounded once
+ * (nearest even) and saturated at 448.  Rows of k, v and q past q_start[S] belong to no sequence:
  * nothing is written for them.  A token whose place lies before position 0, past
  * the table's row or in a page outside the cache is not stored; the last two
  * are reported by fa_last_device_error.  T = 0 or S = 0: FA_OK, nothing done.
