@@ -16,9 +16,9 @@
 // for 4 bytes of traffic).  The angles of a position are shared by all its
 // heads: a block takes TOK positions, one thread makes one sine and cosine, and
 // a thread then keeps those of its 8 pairs in registers and goes through the
-// heads, two at a time, the first two loaded before the angles are made.  TOK is
-// 1 for few positions (blocks for more of the SMs), else what gives a thread
-// some heads to go through.
+// heads, kBatch at a time, the first of them loaded before the angles are made.
+// 16384 positions of 32 + 8 heads at d = 128: 55 us, 6.1 TB/s.  (Four heads at a
+// time at this occupancy spill: 76 us.)
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -26,6 +26,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_paged_host.h"
@@ -102,11 +103,12 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // A unit is 16 values of a row: two 16-byte vectors that hold 8 whole pairs
 // (or 16 values past rot_dim).  Thread: unit u of token tt, heads hg, hg + HG, ...
 template <int D, int TOK, int TO>
-__global__ void __launch_bounds__(kThreads, 3) fa_turn_kernel(const __grid_constant__ TurnParams p) {
+__global__ void __launch_bounds__(kThreads, 4) fa_turn_kernel(const __grid_constant__ TurnParams p) {
   constexpr int UNITS = D / 16;
   constexpr int HG = kThreads / (UNITS * TOK);
   static_assert(HG >= 1, "threads");
-  __shared__ float2 cs[TOK][kMaxPairs];
+  __shared__ __align__(16) float2 cs[TOK][kMaxPairs];
+  __shared__ uint64_t fraction[kMaxPairs];
   __shared__ long long place[TOK];  // cache offset of the token's row in head 0; -1: not stored
   __shared__ int seq_pos[TOK];      // place in the sequence; INT_MIN: no sequence
 
@@ -119,33 +121,28 @@ __global__ void __launch_bounds__(kThreads, 3) fa_turn_kernel(const __grid_const
   const int u = tid % UNITS, tt = tid / UNITS % TOK, hg = tid / (UNITS * TOK);
   const long long t = t0 + tt;
   const bool here = hg < HG && t < p.tokens;
-  const long long b = TO == kTurnOnly ? t / p.N : 0;
+  // (fewer than 2^31 positions in all)
+  const long long b = TO == kTurnOnly ? static_cast<uint32_t>(t) / static_cast<uint32_t>(p.N) : 0;
   const long long n = t - b * p.N;
   // The unit's first vector and the distance to its second, in elements.
   const bool turned = u < half / 8;
   const int first = p.interleaved ? 16 * u : turned ? 8 * u : 2 * half + 16 * (u - half / 8);
   const int gap = p.interleaved || !turned ? 8 : half;
-  const int heads = p.q.heads + p.k.heads + p.v.heads;
-  // Head h counts through q, k and v.
-  auto source = [&](int h) -> const __nv_bfloat16* {
-    if (h < p.q.heads) return p.q.in + (b * p.q.ib + n * p.q.ip + h * p.q.ih + first);
-    h -= p.q.heads;
-    if (h < p.k.heads) return p.k.in + (b * p.k.ib + n * p.k.ip + h * p.k.ih + first);
-    return p.v.in + (n * p.v.ip + (h - p.k.heads) * p.v.ih + first);
-  };
+  // First row of each tensor for this thread, and the step to its next head.
+  const __nv_bfloat16* q_in = p.q.in + (b * p.q.ib + n * p.q.ip + hg * p.q.ih + first);
+  const __nv_bfloat16* k_in = p.k.in + (b * p.k.ib + n * p.k.ip + hg * p.k.ih + first);
   uint4 lo[kBatch], hi[kBatch];
-  auto load = [&](int h0) {
+  auto load = [&](const __nv_bfloat16* src, long long step, int left) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int h = h0 + i * HG;
-      if (here && h < heads) {
-        const __nv_bfloat16* src = source(h);
-        lo[i] = *reinterpret_cast<const uint4*>(src);
-        hi[i] = *reinterpret_cast<const uint4*>(src + gap);
+      if (i * HG < left) {
+        lo[i] = *reinterpret_cast<const uint4*>(src + i * step);
+        hi[i] = *reinterpret_cast<const uint4*>(src + i * step + gap);
       }
     }
   };
-  load(hg);
+  const long long q_step = p.q.ih * HG, k_step = p.k.ih * HG;
+  if (here) load(q_in, q_step, p.q.heads - hg);
 
   if (TO != kTurnOnly) {
     // Warp w finds token w (TOK / 8 rounds): its sequence is the number of
@@ -176,96 +173,124 @@ __global__ void __launch_bounds__(kThreads, 3) fa_turn_kernel(const __grid_const
         seq_pos[w] = pos;
       }
     }
-    __syncthreads();
   }
+  // (fp64 is slow here: once a pair, not once an angle)
+  if (tid < half) fraction[tid] = turn_fraction(p.inv_freq[tid]);
+  __syncthreads();
   for (int i = tid; i < TOK * half; i += kThreads) {
     const int w = i / half, pair = i - w * half;
     const long long tw = t0 + w;
     if (tw >= p.tokens) break;
     int pos = TO == kTurnOnly ? 0 : seq_pos[w];
     if (p.positions) {
-      const long long bw = TO == kTurnOnly ? tw / p.N : 0;
+      const long long bw =
+          TO == kTurnOnly ? static_cast<uint32_t>(tw) / static_cast<uint32_t>(p.N) : 0;
       pos = p.positions[p.axis[pair] * p.axis_stride + bw * p.batch_stride + (tw - bw * p.N)];
     }
-    cs[w][pair] = cos_sin(pos, turn_fraction(p.inv_freq[pair]), p.sign);
+    cs[w][pair] = cos_sin(pos, fraction[pair], p.sign);
   }
   __syncthreads();
   if (!here || (TO != kTurnOnly && seq_pos[tt] == INT_MIN)) return;
 
   float2 t8[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) t8[e] = turned ? cs[tt][8 * u + e] : make_float2(1.0f, 0.0f);
-  const long long row = TO == kTurnOnly ? 0 : place[tt];
-  for (int h0 = hg; h0 < heads; h0 += kBatch * HG) {
+  for (int e = 0; e < 4; ++e) {
+    const float4 v = *reinterpret_cast<const float4*>(&cs[tt][turned ? 8 * u + 2 * e : 0]);
+    t8[2 * e] = make_float2(v.x, v.y);
+    t8[2 * e + 1] = make_float2(v.z, v.w);
+  }
+  auto turn = [&](float (&x)[8], float (&y)[8]) {
+    if (p.interleaved) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      int h = h0 + i * HG;
-      if (h >= heads) break;
-      float x[8], y[8];
-      unpack8(lo[i], x);
-      unpack8(hi[i], y);
-      const bool is_q = h < p.q.heads, is_v = h >= p.q.heads + p.k.heads;
-      if (turned && !is_v) {
-        if (p.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x0 = x[2 * e], x1 = x[2 * e + 1], y0 = y[2 * e], y1 = y[2 * e + 1];
-            x[2 * e] = x0 * t8[e].x - x1 * t8[e].y;
-            x[2 * e + 1] = x0 * t8[e].y + x1 * t8[e].x;
-            y[2 * e] = y0 * t8[e + 4].x - y1 * t8[e + 4].y;
-            y[2 * e + 1] = y0 * t8[e + 4].y + y1 * t8[e + 4].x;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x0 = x[e], y0 = y[e];
-            x[e] = x0 * t8[e].x - y0 * t8[e].y;
-            y[e] = x0 * t8[e].y + y0 * t8[e].x;
-          }
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = x[2 * e], x1 = x[2 * e + 1], y0 = y[2 * e], y1 = y[2 * e + 1];
+        x[2 * e] = x0 * t8[e].x - x1 * t8[e].y;
+        x[2 * e + 1] = x0 * t8[e].y + x1 * t8[e].x;
+        y[2 * e] = y0 * t8[e + 4].x - y1 * t8[e + 4].y;
+        y[2 * e + 1] = y0 * t8[e + 4].y + y1 * t8[e + 4].x;
       }
-      if (TO == kTurnOnly || is_q) {
-        const Rows& R = is_q ? p.q : p.k;
-        __nv_bfloat16* dst =
-            R.out + (b * R.ob + n * R.op + (is_q ? h : h - p.q.heads) * R.oh + first);
-        *reinterpret_cast<uint4*>(dst) = pack8(x);
-        *reinterpret_cast<uint4*>(dst + gap) = pack8(y);
-      } else if (row >= 0) {
-        h -= is_v ? p.q.heads + p.k.heads : p.q.heads;
-        const long long off = row + h * p.head_stride + first;
-        if (TO == kToBf16) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? p.v_pages : p.k_pages) + off;
-          *reinterpret_cast<uint4*>(dst) = pack8(x);
-          *reinterpret_cast<uint4*>(dst + gap) = pack8(y);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x0 = x[e], y0 = y[e];
+        x[e] = x0 * t8[e].x - y0 * t8[e].y;
+        y[e] = x0 * t8[e].y + y0 * t8[e].x;
+      }
+    }
+  };
+  // The heads hg, hg + HG, ... of one tensor, the first kBatch in lo and hi; to
+  // bf16 rows at dst, or to e4m3 rows times `scale`.
+  auto rows = [&](const __nv_bfloat16* src, long long step, int heads, auto* dst,
+                  long long dst_step, bool turns, float scale) {
+    for (int left = heads - hg; left > 0;) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (i * HG >= left) break;
+        float x[8], y[8];
+        if (sizeof(*dst) == 2 && !turns) {
+          *reinterpret_cast<uint4*>(dst + i * dst_step) = lo[i];
+          *reinterpret_cast<uint4*>(dst + i * dst_step + gap) = hi[i];
+          continue;
+        }
+        unpack8(lo[i], x);
+        unpack8(hi[i], y);
+        if (turns) turn(x, y);
+        if constexpr (sizeof(*dst) == 2) {
+          *reinterpret_cast<uint4*>(dst + i * dst_step) = pack8(x);
+          *reinterpret_cast<uint4*>(dst + i * dst_step + gap) = pack8(y);
         } else {
-          uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + off;
-          const float f = is_v ? p.v_scale : p.k_scale;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            x[e] *= f;
-            y[e] *= f;
+            x[e] *= scale;
+            y[e] *= scale;
           }
-          *reinterpret_cast<uint2*>(dst) =
+          *reinterpret_cast<uint2*>(dst + i * dst_step) =
               make_uint2(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]));
-          *reinterpret_cast<uint2*>(dst + gap) =
+          *reinterpret_cast<uint2*>(dst + i * dst_step + gap) =
               make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
         }
       }
+      src += kBatch * step;
+      dst += kBatch * dst_step;
+      left -= kBatch * HG;
+      load(src, step, left);
     }
-    load(h0 + kBatch * HG);
+  };
+  rows(q_in, q_step, p.q.heads,
+       p.q.out + (b * p.q.ob + n * p.q.op + hg * p.q.oh + first), p.q.oh * HG, turned, 1.0f);
+  load(k_in, k_step, p.k.heads - hg);
+  if constexpr (TO == kTurnOnly) {
+    rows(k_in, k_step, p.k.heads,
+         p.k.out + (b * p.k.ob + n * p.k.op + hg * p.k.oh + first), p.k.oh * HG, turned, 1.0f);
+  } else {
+    if (place[tt] < 0) return;
+    using Elem = std::conditional_t<TO == kToBf16, __nv_bfloat16, uint8_t>;
+    const long long off = place[tt] + hg * p.head_stride + first;
+    const __nv_bfloat16* v_in = p.v.in + (n * p.v.ip + hg * p.v.ih + first);
+    rows(k_in, k_step, p.k.heads, static_cast<Elem*>(p.k_pages) + off, p.head_stride * HG, turned,
+         p.k_scale);
+    load(v_in, p.v.ih * HG, p.v.heads - hg);
+    rows(v_in, p.v.ih * HG, p.v.heads, static_cast<Elem*>(p.v_pages) + off, p.head_stride * HG,
+         false, p.v_scale);
   }
 }
 
 template <int D, int TO>
 cudaError_t launch_turn_d(const TurnParams& p, cudaStream_t stream) {
   const int heads = p.q.heads + p.k.heads + p.v.heads;
-  // One position a block below two blocks an SM of more; then the most that
-  // leaves a thread about four heads.
-  const int tok = p.tokens < 8 * 152 ? 1 : heads * (D / 16) * 16 <= 6 * kThreads ? 16 : 4;
+  // The most positions a block that leave a block for every SM and a thread at
+  // most ten heads: the angles' cost is shared, and a short loop ends evenly.
+  // Measured with 1 / 4 / 8 / 16: 8192 positions of 16 heads, d = 64: 38 / 14.5 /
+  // 10.1 / 8.7 us; 16384 of 40, d = 128: 107 / 54.6 / 55.7 / 57.9; 1025 of 32, d =
+  // 96: 6.3 / 4.5 / 4.9 / 7.2; 4 of 48, d = 128: 4.0 / 4.8 / 5.8 / 8.5.
+  int tok = 1;
+  for (int more : {4, 8, 16})
+    if (p.tokens >= 152LL * more && heads * (D / 16) * more <= 10 * kThreads) tok = more;
   const long long grid = (p.tokens + tok - 1) / tok;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kern = tok == 1 ? fa_turn_kernel<D, 1, TO>
               : tok == 4 ? fa_turn_kernel<D, 4, TO>
+              : tok == 8 ? fa_turn_kernel<D, 8, TO>
                          : fa_turn_kernel<D, 16, TO>;
   return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, p);
 }
