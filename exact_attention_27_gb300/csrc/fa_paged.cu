@@ -1,11 +1,11 @@
 // Attention of new tokens over a paged cache for few rows a sequence (single
 // tokens, short drafts): bound by the bytes of K and V.
 //
-// An item is 16 RW rows (tokens x grouped query heads) of one sequence and
+// An item is 16 rows (tokens x grouped query heads) of one sequence and
 // key/value head; fa_paged.cuh says how the key tiles of all items are divided
 // among the CTAs.  Per key tile of 64 keys a producer warp copies K and V into
 // a ring of shared memory, one box per page and 128-byte column block, and
-// 4 RW warps take 16 keys of 16 rows each, with their own running maximum, sum
+// four warps take 16 keys each, with their own running maximum, sum
 // and O in registers, so that they meet only at the end of an item:
 //     S = Q K^T;  m' = max(m, max S);  p = 2^(S - m');
 //     l = l 2^(m - m') + sum p;  O = O 2^(m - m') + p V.
@@ -44,29 +44,28 @@ namespace {
 constexpr float kRescaleThreshold = 8.0f;
 constexpr int kTK = 64;  // keys per tile
 
-template <int D_, bool E4M3_, int RW_>
+template <int D_, bool E4M3_>
 struct RowsCfg {
   static constexpr int D = D_;
   static constexpr bool E4M3 = E4M3_;
-  static constexpr int RW = RW_;         // groups of 16 rows
-  static constexpr int ROWS = 16 * RW;
-  static constexpr int WARPS = 4 * RW;   // consumers
+  static constexpr int ROWS = 16;
+  static constexpr int WARPS = 4;        // consumers
   static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int SUB = (D * (E4M3 ? 1 : 2) + 127) / 128;  // 128-byte column blocks
   static constexpr int BLOCK = kTK * 128;
   static constexpr int STAGE = 2 * SUB * BLOCK;                 // K and V
   static constexpr int MERGE = 2 * ROWS * D * 4;                // two of the four key groups' O
-  static constexpr int OCC = RW == 1 && D <= 128 ? 2 : 1;       // CTAs an SM
+  static constexpr int OCC = D <= 128 ? 2 : 1;       // CTAs an SM
   static constexpr int BUDGET = (OCC == 2 ? 112 : 224) * 1024;
   // At d = 256 the fragments of Q (64 registers) lie in shared memory.
   static constexpr bool QS = D == 256;
-  static constexpr int QBYTES = QS ? RW * 16 * D * 2 : 0;
+  static constexpr int QBYTES = QS ? ROWS * D * 2 : 0;
   static constexpr int FIT = (BUDGET - MERGE - QBYTES - 3072) / STAGE;
   static constexpr int NS = FIT > 8 ? 8 : FIT;
   static constexpr int OFF_MERGE = NS * STAGE;
-  static constexpr int OFF_Q = OFF_MERGE + MERGE;               // [RW][D / 16][32 lanes] fragments
-  static constexpr int OFF_ML = OFF_Q + QBYTES;                 // [RW][4][16] (m, l)
-  static constexpr int OFF_SCR = OFF_ML + RW * 4 * 16 * 8;
+  static constexpr int OFF_Q = OFF_MERGE + MERGE;               // [D / 16][32 lanes] fragments
+  static constexpr int OFF_ML = OFF_Q + QBYTES;                 // [4][16] (m, l)
+  static constexpr int OFF_SCR = OFF_ML + 4 * 16 * 8;
   static constexpr int OFF_BAR = OFF_SCR + 40 * 8;
   static constexpr int OFF_MISC = OFF_BAR + 2 * NS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
@@ -110,16 +109,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Barrier among the four warps of a row group.
-__device__ __forceinline__ void group_sync(int rw) {
-  asm volatile("bar.sync %0, 128;" ::"r"(rw + 1) : "memory");
+// Barrier among the consumer warps.
+__device__ __forceinline__ void group_sync() {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
-template <int D, bool E4M3, int RW>
-__global__ void __launch_bounds__(RowsCfg<D, E4M3, RW>::THREADS, RowsCfg<D, E4M3, RW>::OCC)
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::OCC)
     fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tmK,
-                         const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
-  using C = RowsCfg<D, E4M3, RW>;
+                         const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ PagedParams p) {
+  using C = RowsCfg<D, E4M3>;
   using Walk = PagedWalk<C::ROWS, kTK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -205,12 +205,12 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, RW>::THREADS, RowsCfg<D, E4M3
         mbar_wait_timed(full(i % C::NS), (i / C::NS) & 1);
   } else {
     // ------------------------------------------------------------ consumers
-    const int kg = warp & 3, rw = warp >> 2;
+    const int kg = warp;                    // which 16 keys of a tile
     const int g = lane >> 2, c = lane & 3;  // row (and row + 8), column quad of the fragments
     constexpr int NT = D / 8;               // 8-column tiles of O
-    float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE) + rw * 2 * 16 * D;
-    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML) + rw * 4 * 16;
-    uint4* qs = reinterpret_cast<uint4*>(smem + C::OFF_Q) + rw * (D / 16) * 32;
+    float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    uint4* qs = reinterpret_cast<uint4*>(smem + C::OFF_Q);
     int n = 0;
     bool ok = true;
     while (unit < range.end) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, RW>::THREADS, RowsCfg<D, E4M3
       const long long unit0 = unit;
       unit += t_end - t;
       const int rows = w.g.qlen * p.G;
-      const int r0 = w.rt * C::ROWS + rw * 16;  // this warp's first row
+      const int r0 = w.rt * C::ROWS;  // first row
       // Rows r0 + g and r0 + g + 8: token, query head, last key seen.
       int tok[2], head[2], last[2];
       bool live[2];
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, RW>::THREADS, RowsCfg<D, E4M3
           for (int kk = 0; kk < D / 16; ++kk)
             qs[kk * 32 + lane] = make_uint4(qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3]);
         }
-        group_sync(rw);
+        group_sync();
       }
       auto q_frag = [&](int kk, uint32_t (&a)[4]) {
         if constexpr (C::QS) {
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, RW>::THREADS, RowsCfg<D, E4M3
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
         if (c == 0) ml[kg * 16 + g + 8 * i] = make_float2(m[i], l[i]);
       }
-      group_sync(rw);
+      group_sync();
       float M[2], L[2], f[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -488,31 +488,30 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, RW>::THREADS, RowsCfg<D, E4M3
         for (int k = 0; k < 4; ++k) L[i] += x[k].y * ex2_approx(x[k].x - ref);
         f[i] = ex2_approx(m[i] - ref);
       }
+      auto halves = [&](auto&& go) {  // rows g, and g + 8 if there are any
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < NT * 2; ++i) go(i >> 1, i & 1, i * 32 + lane, f[0]);
+        if (rows - r0 > 8) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) o[i][x] *= f[x >> 1];
-      if (kg >= 2) {
-#pragma unroll
-        for (int i = 0; i < NT * 4; ++i)
-          merge[(kg - 2) * 16 * D + i * 32 + lane] = o[i >> 2][i & 3];
-      }
-      group_sync(rw);
-      if (kg < 2) {
-#pragma unroll
-        for (int i = 0; i < NT * 4; ++i) {
-          o[i >> 2][i & 3] += merge[kg * 16 * D + i * 32 + lane];
-          if (kg == 1) merge[16 * D + i * 32 + lane] = o[i >> 2][i & 3];
+          for (int i = 0; i < NT * 2; ++i)
+            go(i >> 1, 2 + (i & 1), (NT * 2 + i) * 32 + lane, f[1]);
         }
-      }
-      group_sync(rw);
+      };
+      if (kg >= 2)
+        halves([&](int nt, int x, int at, float s) { merge[(kg - 2) * 16 * D + at] = o[nt][x] * s; });
+      group_sync();
+      if (kg < 2)
+        halves([&](int nt, int x, int at, float s) {
+          o[nt][x] = o[nt][x] * s + merge[kg * 16 * D + at];
+          if (kg == 1) merge[16 * D + at] = o[nt][x];
+        });
+      group_sync();
+      const bool whole = t_begin == 0 && t_end == tiles;
       if (kg == 0 && ok) {
-        const bool whole = t_begin == 0 && t_end == tiles;
         const int slot = cta * 2 + (t_begin == 0 ? 1 : 0);
-        float* po = p.part_o + (static_cast<long long>(slot) * C::ROWS + rw * 16) * D;
-        float2* pml = p.part_ml + static_cast<long long>(slot) * C::ROWS + rw * 16;
-#pragma unroll
-        for (int i = 0; i < NT * 4; ++i) o[i >> 2][i & 3] += merge[16 * D + i * 32 + lane];
+        float* po = p.part_o + static_cast<long long>(slot) * C::ROWS * D;
+        float2* pml = p.part_ml + static_cast<long long>(slot) * C::ROWS;
+        halves([&](int nt, int x, int at, float) { o[nt][x] += merge[16 * D + at]; });
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!live[i]) continue;
@@ -548,7 +547,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, RW>::THREADS, RowsCfg<D, E4M3
                   L[i] > 0.0f ? (M[i] + log2f(L[i])) * kPagedLn2 : -INFINITY;
           }
         }
-        if (rw == 0 && lane == 0 && t_begin == 0 && t_end < tiles)
+        if (lane == 0 && t_begin == 0 && t_end < tiles)
           p.notes[cta] = paged_note<C::ROWS, kTK>(p, range, w, unit0);
       }
       if (unit < range.end) w.next(p);
@@ -659,11 +658,10 @@ int sm_count() {
   return n;
 }
 
-// Rows of an item, which says the kernel: sequences of at most 32 rows go 16 or
-// 32 rows an item to the kernel above, anything longer to the tcgen05 kernels.
-int rows_for(long long most, int d) {
-  return most <= 16 ? 16 : most <= 32 ? 32 : paged_tile_rows(d);
-}
+// Rows of an item, which says the kernel: sequences of at most 16 rows go to the
+// kernel above, anything longer to the tcgen05 kernels (64 sequences of 100 to
+// 8000 keys, 32 rows each, d = 128: 225 us there, 269 us 32 rows a time here).
+int rows_for(long long most, int d) { return most <= 16 ? 16 : paged_tile_rows(d); }
 
 // CTAs of a launch with `rows` rows an item.
 int ctas_for(int sms, int rows, int d) { return sms * (rows == 16 && d <= 128 ? 2 : 1); }
@@ -681,31 +679,24 @@ PartLayout part_layout(int ctas, int rows, int d) {
   return l;
 }
 
-template <int D, bool E4M3, int RW>
+template <int D, bool E4M3>
 cudaError_t launch_rows_t(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
                           int ctas, cudaStream_t stream) {
-  using C = RowsCfg<D, E4M3, RW>;
-  cudaError_t e = set_smem_limit_once<fa_paged_rows_kernel<D, E4M3, RW>>(C::SMEM_BYTES);
+  using C = RowsCfg<D, E4M3>;
+  const cudaError_t e = set_smem_limit_once<fa_paged_rows_kernel<D, E4M3>>(C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return launch_dependent(fa_paged_rows_kernel<D, E4M3, RW>, dim3(ctas), dim3(C::THREADS),
+  return launch_dependent(fa_paged_rows_kernel<D, E4M3>, dim3(ctas), dim3(C::THREADS),
                           C::SMEM_BYTES, stream, tk, tv, p);
-}
-
-template <int D, bool E4M3>
-cudaError_t launch_rows_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
-                          int rows, int ctas, cudaStream_t stream) {
-  return rows == 16 ? launch_rows_t<D, E4M3, 1>(tk, tv, p, ctas, stream)
-                    : launch_rows_t<D, E4M3, 2>(tk, tv, p, ctas, stream);
 }
 
 template <bool E4M3>
 cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int d,
-                        int rows, int ctas, cudaStream_t stream) {
+                        int ctas, cudaStream_t stream) {
   switch (d) {
-    case 64: return launch_rows_d<64, E4M3>(tk, tv, p, rows, ctas, stream);
-    case 96: return launch_rows_d<96, E4M3>(tk, tv, p, rows, ctas, stream);
-    case 128: return launch_rows_d<128, E4M3>(tk, tv, p, rows, ctas, stream);
-    case 256: return launch_rows_d<256, E4M3>(tk, tv, p, rows, ctas, stream);
+    case 64: return launch_rows_t<64, E4M3>(tk, tv, p, ctas, stream);
+    case 96: return launch_rows_t<96, E4M3>(tk, tv, p, ctas, stream);
+    case 128: return launch_rows_t<128, E4M3>(tk, tv, p, ctas, stream);
+    case 256: return launch_rows_t<256, E4M3>(tk, tv, p, ctas, stream);
   }
   return cudaErrorInvalidValue;
 }
@@ -715,7 +706,7 @@ cudaError_t launch_join(const PagedParams& p, int rows, int d, int ctas, cudaStr
               : d == 96  ? fa_paged_join_kernel<96>
               : d == 128 ? fa_paged_join_kernel<128>
                          : fa_paged_join_kernel<256>;
-  return launch_dependent(kern, dim3(ctas, rows <= 32 ? 4 : 16), dim3(kJoinThreads), 0, stream, p,
+  return launch_dependent(kern, dim3(ctas, rows == 16 ? 4 : 16), dim3(kJoinThreads), 0, stream, p,
                           rows);
 }
 
@@ -789,7 +780,10 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   p.causal = causal;
   p.rows_min = 1;
   p.rows_max = 0x7fffffff;
-  p.min_units = 1;
+  // A CTA starts for one tile of 64 keys (two sequences of a thousand keys: 10.8 us,
+  // 13 to 19 us with 2 to 8 at least), but for four of the tcgen05 kernels, whose
+  // parts are larger (128 rows of 4096 keys: 14.5 us, 21.8 us with one).
+  p.min_units = rows == 16 ? 1 : 4;
   p.scale_log2 = s_eff * kPagedLog2e;
   p.v_scale = cache->v_descale;
   char* ws = static_cast<char*>(workspace);
@@ -797,15 +791,15 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   p.part_o = reinterpret_cast<float*>(ws + lay.o);
   CUtensorMap tk, tv;
-  const bool tile = rows > 32;
+  const bool tile = rows > 16;
   const bool e4m3 = cache->dtype == FA_CACHE_E4M3;
   const int box = std::min(cache->page_size, tile ? paged_tile_keys(d) : kTK);
   if (!encode_map_pages(&tk, *cache, cache->k, box) || !encode_map_pages(&tv, *cache, cache->v, box))
     return FA_ERR_CUDA;
   cudaError_t e = tile   ? d == 256 ? launch_paged_tile(tk, tv, p, e4m3, ctas, stream)
                                     : launch_paged_tile2(tk, tv, p, d, e4m3, ctas, stream)
-                  : e4m3 ? launch_rows<true>(tk, tv, p, d, rows, ctas, stream)
-                         : launch_rows<false>(tk, tv, p, d, rows, ctas, stream);
+                  : e4m3 ? launch_rows<true>(tk, tv, p, d, ctas, stream)
+                         : launch_rows<false>(tk, tv, p, d, ctas, stream);
   if (e == cudaSuccess) e = launch_join(p, rows, d, ctas, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

