@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
                          const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ PagedParams p) {
   using C = RowsCfg<D, E4M3>;
-  using Walk = PagedWalk<C::ROWS, kTK>;
+  using Walk = PagedWalk<C::ROWS, kTK, 1>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -144,16 +144,14 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  const PagedRange range = paged_range<C::ROWS, kTK, C::THREADS>(
-      p, reinterpret_cast<long long*>(smem + C::OFF_SCR));
+  const PagedRange range =
+      paged_range<Walk, C::THREADS>(p, reinterpret_cast<long long*>(smem + C::OFF_SCR));
   __syncthreads();
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) p.notes[cta].last = -1;
-  if (range.end <= range.first) return;  // block-uniform, no copies in flight
-
-  Walk w;
-  int t = w.start(p, range.seq, range.rem);
-  long long unit = range.first;
+  PagedSegments<Walk> seg;
+  if (!seg.start(p, range)) return;  // block-uniform, no copies in flight
+  bool more = true;
 
   if (warp == C::WARPS) {
     // ------------------------------------------------------------ producer
@@ -168,18 +166,14 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
     const uint32_t dst0 = sbase + (is_v * C::SUB + sub) * C::BLOCK + row0 * 128;
     int n = 0;  // tiles issued
     bool ok = true;
-    while (ok && unit < range.end) {
-      const int keys = w.my_keys(p);
-      const int t_end = static_cast<int>(min(static_cast<long long>(w.my_tiles(p)),
-                                             t + (range.end - unit)));
-      unit += t_end - t;
-      for (; t < t_end; ++t, ++n) {
+    for (; ok && more; more = seg.next(p)) {
+      for (int t = seg.t0; t < seg.t1; ++t, ++n) {
         const int st = n % C::NS;
         const int key0 = t * kTK + row0;
-        bool issue = mine && key0 < keys;
+        bool issue = mine && key0 < seg.keys;
         int id = 0;
         if (issue) {
-          id = p.table[w.s * p.table_stride + (key0 >> p.page_shift)];
+          id = p.table[seg.w.s * p.table_stride + (key0 >> p.page_shift)];
           if (id < 0 || id >= p.n_pages) {
             atomicOr(p.err, kErrBadPage);
             issue = false;
@@ -194,10 +188,8 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
         __syncwarp();
         if (issue)
           tma_load_4d(dst0 + st * C::STAGE, is_v ? &tmV : &tmK, full(st), sub * 128,
-                      key0 & (page - 1), w.h, id);
+                      key0 & (page - 1), seg.w.h, id);
       }
-      t = 0;
-      if (unit < range.end) w.next(p);
     }
     // On the abort path the copies already issued land before the CTA's memory is released.
     if (*abort_flag)
@@ -213,14 +205,9 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
     uint4* qs = reinterpret_cast<uint4*>(smem + C::OFF_Q);
     int n = 0;
     bool ok = true;
-    while (unit < range.end) {
-      const int tiles = w.my_tiles(p);
-      const int keys = w.my_keys(p);
-      const int t_begin = t;
-      const int t_end =
-          static_cast<int>(min(static_cast<long long>(tiles), t + (range.end - unit)));
-      const long long unit0 = unit;
-      unit += t_end - t;
+    for (; more; more = seg.next(p)) {
+      const Walk& w = seg.w;
+      const int keys = seg.keys;
       const int rows = w.g.qlen * p.G;
       const int r0 = w.rt * C::ROWS;  // first row
       // Rows r0 + g and r0 + g + 8: token, query head, last key seen.
@@ -308,7 +295,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
         for (int x = 0; x < 4; ++x) o[i][x] = 0.0f;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-      for (; t < t_end; ++t, ++n) {
+      for (int t = seg.t0; t < seg.t1; ++t, ++n) {
         const int st = n % C::NS;
         // Warp-uniform.  After a timeout the warp still goes through every
         // item's barriers, without work.
@@ -463,7 +450,6 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
         }
         mbar_arrive_warp(empty(st));
       }
-      t = 0;
 
       // ---------------------------------------------------------- end of the item
       // The four key groups join: common maximum, then O of groups 2 and 3
@@ -506,9 +492,9 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
           if (kg == 1) merge[16 * D + at] = o[nt][x];
         });
       group_sync();
-      const bool whole = t_begin == 0 && t_end == tiles;
+      const bool whole = seg.t0 == 0 && seg.t1 == seg.tiles;
       if (kg == 0 && ok) {
-        const int slot = cta * 2 + (t_begin == 0 ? 1 : 0);
+        const int slot = cta * 2 + (seg.t0 == 0 ? 1 : 0);
         float* po = p.part_o + static_cast<long long>(slot) * C::ROWS * D;
         float2* pml = p.part_ml + static_cast<long long>(slot) * C::ROWS;
         halves([&](int nt, int x, int at, float) { o[nt][x] += merge[16 * D + at]; });
@@ -547,10 +533,9 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
                   L[i] > 0.0f ? (M[i] + log2f(L[i])) * kPagedLn2 : -INFINITY;
           }
         }
-        if (lane == 0 && t_begin == 0 && t_end < tiles)
-          p.notes[cta] = paged_note<C::ROWS, kTK>(p, range, w, unit0);
+        if (lane == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
+          p.notes[cta] = paged_note(p, range, seg);
       }
-      if (unit < range.end) w.next(p);
     }
   }
   __syncthreads();
@@ -778,8 +763,6 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   p.max_pages = batch->max_pages;
   p.n_pages = cache->n_pages;
   p.causal = causal;
-  p.rows_min = 1;
-  p.rows_max = 0x7fffffff;
   // A CTA starts for one tile of 64 keys (two sequences of a thousand keys: 10.8 us,
   // 13 to 19 us with 2 to 8 at least), but for four of the tcgen05 kernels, whose
   // parts are larger (128 rows of 4096 keys: 14.5 us, 21.8 us with one).

@@ -1,7 +1,7 @@
 // Shared by the kernels of fa_forward_paged: the step's geometry, the division
 // of its key tiles among the CTAs, and the partial results of what is divided.
 //
-// Work is counted in units of one key tile of one item; an item is a tile of
+// Work is counted in units of about one key tile of one item; an item is a tile of
 // ROWS query rows of one (sequence, key/value head), its rows being the
 // head's tokens x the G query heads that share it (row r: token r / G, head
 // r % G), so that grouped heads read K and V once.  Items stand in order of
@@ -80,7 +80,6 @@ struct PagedParams {
   int S, T, Hq, Hkv, G;
   int page_shift, max_pages, n_pages;
   int causal;
-  int rows_min, rows_max;  // sequences whose row count lies outside are another kernel's
   int min_units;           // units that are worth a CTA
   float scale_log2;        // scale * log2(e) * k_descale
   float v_scale;
@@ -110,52 +109,85 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int s) {
   return g;
 }
 
-template <int ROWS, int TK>
+// Items of ROWS rows and key tiles of TK keys.  An item counts for its key
+// tiles and OVER units more, about what starting and ending one costs.
+template <int ROWS_, int TK_, int OVER_>
 struct PagedWalk {
+  static constexpr int ROWS = ROWS_, TK = TK_, OVER = OVER_;
   int s, h, rt, n_rt;
   PagedSeq g;
 
   static __device__ __forceinline__ int row_tiles(const PagedParams& p, const PagedSeq& g) {
-    const int rows = g.qlen * p.G;
-    return rows < p.rows_min || rows > p.rows_max ? 0 : (rows + ROWS - 1) / ROWS;
+    return (g.qlen * p.G + ROWS - 1) / ROWS;
   }
   // Keys that the last row of row tile rt sees.
   static __device__ __forceinline__ int keys(const PagedParams& p, const PagedSeq& g, int rt) {
     if (!p.causal) return g.klen;
-    const int tokens = min(g.qlen, (rt * ROWS + ROWS - 1) / p.G + 1);
+    const int tokens =
+        min(g.qlen, static_cast<int>(static_cast<uint32_t>(rt * ROWS + ROWS - 1) /
+                                     static_cast<uint32_t>(p.G)) + 1);
     return max(g.klen - g.qlen + tokens, 0);
   }
   // Its key tiles: one at least, so that rows without keys are written too.
   static __device__ __forceinline__ int tiles(const PagedParams& p, const PagedSeq& g, int rt) {
     return max((keys(p, g, rt) + TK - 1) / TK, 1);
   }
-  // Key tiles of one head of the sequence.
+  static __device__ __forceinline__ int units(const PagedParams& p, const PagedSeq& g, int rt) {
+    return tiles(p, g, rt) + OVER;
+  }
+  // Units of one head of the sequence of each lane; the whole warp calls this.
   static __device__ __forceinline__ long long head_units(const PagedParams& p, const PagedSeq& g) {
+    constexpr int SHORT = 4;
     const int n = row_tiles(p, g);
-    if (n == 0) return 0;
-    if (!p.causal) return static_cast<long long>(n) * tiles(p, g, 0);
+    if (!p.causal) return n == 0 ? 0 : static_cast<long long>(n) * units(p, g, 0);
     long long u = 0;
-    for (int rt = 0; rt < n; ++rt) u += tiles(p, g, rt);
+    if (n <= SHORT) {
+      for (int rt = 0; rt < n; ++rt) u += units(p, g, rt);
+    }
+    // Long chunks: all lanes, one sequence after the other.
+    const int lane = lane_id();
+    for (unsigned todo = __ballot_sync(0xffffffffu, n > SHORT); todo != 0; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      PagedSeq x;
+      x.q0 = 0;
+      x.qlen = __shfl_sync(0xffffffffu, g.qlen, src);
+      x.klen = __shfl_sync(0xffffffffu, g.klen, src);
+      const int m = __shfl_sync(0xffffffffu, n, src);
+      long long sum = 0;
+      for (int rt = lane; rt < m; rt += 32) sum += units(p, x, rt);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == src) u = sum;
+    }
     return u;
   }
 
-  __device__ __forceinline__ int my_keys(const PagedParams& p) const { return keys(p, g, rt); }
-  __device__ __forceinline__ int my_tiles(const PagedParams& p) const { return tiles(p, g, rt); }
-
-  // Starts at unit `rem` of sequence s0; returns the key tile.
-  __device__ __forceinline__ int start(const PagedParams& p, int s0, long long rem) {
+  // Goes to unit `rem` of sequence s0, whose heads have per_head units; the
+  // whole warp calls this.  Returns the unit within the item.
+  __device__ __forceinline__ int start(const PagedParams& p, int s0, long long rem,
+                                       long long per_head) {
     s = s0;
     g = paged_seq(p, s);
     n_rt = row_tiles(p, g);
-    const long long per_head = head_units(p, g);
     h = static_cast<int>(paged_div(rem, per_head));
     rem -= h * per_head;
-    for (rt = 0; rt < n_rt - 1; ++rt) {
-      const int t = my_tiles(p);
-      if (rem < t) break;
-      rem -= t;
+    const int lane = lane_id();
+    for (int base = 0;; base += 32) {
+      const int mine = base + lane < n_rt ? units(p, g, base + lane) : 0;
+      int x = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, rem < x);
+      if (past != 0 || base + 32 >= n_rt) {
+        const int at = past != 0 ? __ffs(past) - 1 : 0;
+        rt = min(base + at, n_rt - 1);
+        return static_cast<int>(rem) - __shfl_sync(0xffffffffu, x - mine, at);
+      }
+      rem -= __shfl_sync(0xffffffffu, x, 31);
     }
-    return static_cast<int>(rem);
   }
   __device__ __forceinline__ void next(const PagedParams& p) {
     if (++rt < n_rt) return;
@@ -174,7 +206,7 @@ struct PagedRange {
   long long units, first, end;  // all units; this CTA's
   int ctas;                     // CTAs with units
   int seq;                      // where `first` lies
-  long long rem;
+  long long rem, per_head;      // its unit in that sequence; units of a head there
   // CTA whose range holds unit u.
   __device__ __forceinline__ int owner(long long u) const {
     return static_cast<int>(paged_div((u + 1) * ctas - 1, units));
@@ -182,9 +214,8 @@ struct PagedRange {
 };
 
 // Every thread of the block calls this; `scratch`: 40 long longs of shared memory.
-template <int ROWS, int TK, int THREADS>
+template <typename Walk, int THREADS>
 __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long long* scratch) {
-  using Walk = PagedWalk<ROWS, TK>;
   constexpr int WARPS = THREADS / 32;
   static_assert(WARPS <= 32, "scratch");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -208,23 +239,18 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
     return before + x - mine;
   };
   auto units_of = [&](int s) -> long long {
-    if (s >= p.S) return 0;
-    const PagedSeq g = paged_seq(p, s);
-    if (blockIdx.x == 0 && p.kv_len[s] > g.klen) atomicOr(p.err, kErrBadPage);
+    PagedSeq g{0, 0, 0};
+    if (s < p.S) {
+      g = paged_seq(p, s);
+      if (blockIdx.x == 0 && p.kv_len[s] > g.klen) atomicOr(p.err, kErrBadPage);
+    }
     return Walk::head_units(p, g) * p.Hkv;
   };
   PagedRange r;
   r.seq = 0;
   r.rem = 0;
+  r.per_head = 1;
   r.first = r.end = 0;
-  auto divide = [&]() -> bool {  // false: no units for this CTA
-    r.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x),
-                                  paged_div(r.units + p.min_units - 1, p.min_units)));
-    if (static_cast<int>(blockIdx.x) >= r.ctas) return false;
-    r.first = paged_div(blockIdx.x * r.units, r.ctas);
-    r.end = paged_div((blockIdx.x + 1) * r.units, r.ctas);
-    return true;
-  };
   long long mine = units_of(tid), all;
   long long pre = scan(mine, all);
   r.units = all;
@@ -232,8 +258,16 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
     scan(units_of(base + tid), all);
     r.units += all;
   }
-  if (r.units == 0 || !divide()) return r;  // block-uniform
-  if (tid == 0) scratch[32] = scratch[33] = 0;
+  if (r.units == 0) return r;  // (block-uniform, as below)
+  r.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x),
+                                paged_div(r.units + p.min_units - 1, p.min_units)));
+  if (static_cast<int>(blockIdx.x) >= r.ctas) return r;
+  r.first = paged_div(blockIdx.x * r.units, r.ctas);
+  r.end = paged_div((blockIdx.x + 1) * r.units, r.ctas);
+  if (tid == 0) {
+    scratch[32] = scratch[33] = 0;
+    scratch[34] = 1;
+  }
   __syncthreads();
   long long done = 0;
   for (int base = 0; base < p.S; base += THREADS) {
@@ -248,6 +282,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
     if (r.first >= done + pre && r.first < done + pre + mine) {
       scratch[32] = base + tid;
       scratch[33] = r.first - done - pre;
+      scratch[34] = paged_div(mine, p.Hkv);
     }
     __syncthreads();
     if (r.first < done + all) break;
@@ -255,18 +290,53 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
   }
   r.seq = static_cast<int>(scratch[32]);
   r.rem = scratch[33];
+  r.per_head = scratch[34];
   return r;
 }
 
+// A CTA's segments: the items of its range one after the other, each with the
+// key tiles [t0, t1) that lie in the range.  Every role walks them on its own,
+// from a common start.
+template <typename Walk>
+struct PagedSegments {
+  Walk w;
+  long long unit, end;  // where the item's part of the range begins; the range's end
+  int t0, t1, tiles, keys, used;
+  __device__ __forceinline__ void load(const PagedParams& p, int at) {
+    tiles = Walk::tiles(p, w.g, w.rt);
+    keys = Walk::keys(p, w.g, w.rt);
+    used = static_cast<int>(min(static_cast<long long>(tiles + Walk::OVER - at), end - unit));
+    t0 = min(at, tiles);
+    t1 = min(at + used, tiles);
+  }
+  // False if the range holds no key tile.  The whole warp calls this.
+  __device__ __forceinline__ bool start(const PagedParams& p, const PagedRange& r) {
+    unit = r.first;
+    end = r.end;
+    if (unit >= end) return false;
+    load(p, w.start(p, r.seq, r.rem, r.per_head));
+    return t0 < t1 || next(p);
+  }
+  // False when the range is done.
+  __device__ __forceinline__ bool next(const PagedParams& p) {
+    unit += used;
+    if (unit >= end) return false;
+    w.next(p);
+    load(p, 0);
+    return true;
+  }
+};
+
 // What a CTA notes about the item that starts in its range and goes on past it.
-template <int ROWS, int TK>
+template <typename Walk>
 __device__ __forceinline__ PagedNote paged_note(const PagedParams& p, const PagedRange& r,
-                                                const PagedWalk<ROWS, TK>& w, long long unit0) {
+                                                const PagedSegments<Walk>& seg) {
+  const Walk& w = seg.w;
   PagedNote n{};
-  n.last = r.owner(unit0 + w.my_tiles(p) - 1);
+  n.last = r.owner(seg.unit + seg.tiles - 1);
   n.q0 = w.g.q0;
   n.rows = w.g.qlen * p.G;
-  n.tile0 = w.rt * ROWS;
+  n.tile0 = w.rt * Walk::ROWS;
   n.head = w.h;
   return n;
 }

@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(384, 1)
                          const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
   using C = TileCfg<D, E4M3>;
   constexpr int BN = C::BN;
+  using Walk = PagedWalk<C::BM, BN, 2>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -149,12 +150,22 @@ __global__ void __launch_bounds__(384, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  const PagedRange range =
-      paged_range<C::BM, BN, C::THREADS>(p, reinterpret_cast<long long*>(smem + C::OFF_SCR));
+  long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_SCR);
   const int cta = blockIdx.x;
-  if (threadIdx.x == 0) p.notes[cta].last = -1;
-  if (range.end <= range.first) return;  // block-uniform, nothing in flight
-
+  {
+    // The roles take their start from shared memory: registers that live
+    // across the change of the register budgets would be spilled.
+    const PagedRange r = paged_range<Walk, C::THREADS>(p, scratch);
+    if (threadIdx.x == 0) p.notes[cta].last = -1;
+    PagedSegments<Walk> first;
+    if (!first.start(p, r)) return;  // block-uniform, nothing in flight
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      *reinterpret_cast<PagedRange*>(scratch) = r;
+      *reinterpret_cast<PagedSegments<Walk>*>(scratch + 10) = first;
+    }
+  }
+  static_assert(sizeof(PagedRange) <= 80 && sizeof(PagedSegments<Walk>) <= 240, "scratch");
   if (warp == 9) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
@@ -169,12 +180,11 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t sR = sbase + C::OFF_RAW;
   float* q_scale = reinterpret_cast<float*>(smem + C::OFF_SCALE);
 
-  PagedSegments<128, BN> seg;
-
   if (warp >= 8) {
     reg_decrease<104>();
     if (warp == 8) {
       // ---------------------------------------------------------- TMA producer
+      PagedSegments<Walk> seg = *reinterpret_cast<const PagedSegments<Walk>*>(scratch + 10);
       const int page = 1 << p.page_shift;
       const int box_rows = min(page, BN);
       constexpr int BLOCKS = E4M3 ? C::RSUB : C::SUB;
@@ -195,7 +205,6 @@ __global__ void __launch_bounds__(384, 1)
       };
       int nk = 0, nv = 0;  // K and V tiles issued
       bool ok = true;
-      seg.start(p, range);
       do {
         for (int t = seg.t0; ok && t < seg.t1; ++t) {
           const int key0 = t * BN + row0;
@@ -247,6 +256,7 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer
       if (elect_one()) {
+        PagedSegments<Walk> seg = *reinterpret_cast<const PagedSegments<Walk>*>(scratch + 10);
         constexpr uint32_t ID_S = E4M3 ? idesc_f16_f32(128, BN, false)
                                        : idesc_bf16_f32(128, BN, false, false);
         constexpr uint32_t ID_O = E4M3 ? idesc_f16_f32(128, D, true)
@@ -258,8 +268,7 @@ __global__ void __launch_bounds__(384, 1)
           return mbar_wait(bar(b), parity, abort_flag, p.err, kErrTimeoutMma);
         };
         // The S products run two tiles ahead of the P V products.
-        PagedSegments<128, BN> ahead;
-        ahead.start(p, range);
+        PagedSegments<Walk> ahead = seg;
         bool more = true;  // S products are left
         int ta = ahead.t0, na = 0, ia = 0;  // its tile, running number, item
         auto issue_s = [&]() -> bool {
@@ -289,8 +298,7 @@ __global__ void __launch_bounds__(384, 1)
         bool ok = issue_s();
         if (ok && more) ok = issue_s();
         int n = 0;
-        seg.start(p, range);
-        do {
+          do {
           for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
             const int st = n % C::NS, bf = n % C::NB;
             ok = (E4M3 || wait(C::B_VFULL + st, (n / C::NS) & 1)) &&
@@ -322,13 +330,14 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ Q, V's tail, conversion
     reg_decrease<160>();
+    PagedSegments<Walk> seg = *reinterpret_cast<const PagedSegments<Walk>*>(scratch + 10);
     const int row = threadIdx.x & 127;
     auto wait = [&](int b, uint32_t parity) {
       return __all_sync(0xffffffffu,
                         mbar_wait(bar(b), parity, abort_flag, p.err, kErrTimeoutLoad)) != 0;
     };
     // Q of item `i` (segment s): row `row`, zeros past the sequence's rows.
-    auto load_q = [&](const PagedSegments<128, BN>& s, int i) -> bool {
+    auto load_q = [&](const PagedSegments<Walk>& s, int i) -> bool {
       const int qs = i % C::NQ;
       if (i >= C::NQ && !wait(C::B_QEMPTY + qs, ((i / C::NQ) - 1) & 1)) return false;
       q_scale[qs * C::BM + row] =
@@ -337,7 +346,6 @@ __global__ void __launch_bounds__(384, 1)
       mbar_arrive_warp(bar(C::B_QFULL + qs));
       return true;
     };
-    seg.start(p, range);
     int n = 0, i = 0;
     bool ok = load_q(seg, 0), more = true;
     do {
@@ -374,6 +382,7 @@ __global__ void __launch_bounds__(384, 1)
   } else {
     // ------------------------------------------------------------ softmax (rows)
     reg_increase<240>();
+    PagedSegments<Walk> seg = *reinterpret_cast<const PagedSegments<Walk>*>(scratch + 10);
     const int row = threadIdx.x;
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     // Waits are made warp-uniform: the TMEM loads and stores are
@@ -383,7 +392,6 @@ __global__ void __launch_bounds__(384, 1)
     };
     int n = 0, i = 0;
     bool ok = true;
-    seg.start(p, range);
     do {
       const PagedRow x = paged_row(p, seg, row);
       const int qs = i % C::NQ;
@@ -420,7 +428,7 @@ __global__ void __launch_bounds__(384, 1)
                                 seg.t0 == 0 && seg.t1 == seg.tiles,
                                 static_cast<long long>(slot) * C::BM + row, m_used, l);
       if (row == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
-        p.notes[cta] = paged_note<C::BM, BN>(p, range, seg.w, seg.unit);
+        p.notes[cta] = paged_note(p, *reinterpret_cast<const PagedRange*>(scratch), seg);
       // (The next item's first O product follows this thread's next P, after a fence.)
       ++i;
     } while (seg.next(p));

@@ -36,34 +36,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
-// A CTA's segments: the items of its range one after the other, each with the
-// key tiles [t0, t1) that lie in the range.  Every role walks them on its own.
-template <int ROWS, int BN>
-struct PagedSegments {
-  PagedWalk<ROWS, BN> w;
-  long long unit, end;
-  int t0, t1, tiles, keys;
-  __device__ __forceinline__ void load(const PagedParams& p, int t) {
-    tiles = w.my_tiles(p);
-    keys = w.my_keys(p);
-    t0 = t;
-    t1 = static_cast<int>(min(static_cast<long long>(tiles), t + (end - unit)));
-  }
-  __device__ __forceinline__ void start(const PagedParams& p, const PagedRange& r) {
-    unit = r.first;
-    end = r.end;
-    load(p, w.start(p, r.seq, r.rem));
-  }
-  // False when the range is done.
-  __device__ __forceinline__ bool next(const PagedParams& p) {
-    unit += t1 - t0;
-    if (unit >= end) return false;
-    w.next(p);
-    load(p, 0);
-    return true;
-  }
-};
-
 // One row of an item, as its thread sees it.
 struct PagedRow {
   bool live;       // a row of the sequence
@@ -73,61 +45,76 @@ struct PagedRow {
   long long token;
 };
 
-template <int ROWS, int BN>
-__device__ __forceinline__ PagedRow paged_row(const PagedParams& p,
-                                              const PagedSegments<ROWS, BN>& s, int row) {
+template <typename Walk>
+__device__ __forceinline__ PagedRow paged_row(const PagedParams& p, const PagedSegments<Walk>& s,
+                                              int row) {
   PagedRow x;
-  const int r = s.w.rt * ROWS + row;
+  const int r = s.w.rt * Walk::ROWS + row;
   x.live = r < s.w.g.qlen * p.G;
   const int tok = x.live ? r / p.G : 0;
   x.head = s.w.h * p.G + (x.live ? r - tok * p.G : 0);
   const int base = s.w.g.klen - s.w.g.qlen;
   x.last = p.causal ? base + tok : s.w.g.klen - 1;
-  x.all_see = p.causal ? base + s.w.rt * ROWS / p.G : s.w.g.klen - 1;
+  x.all_see = p.causal ? base + s.w.rt * Walk::ROWS / p.G : s.w.g.klen - 1;
   x.token = s.w.g.q0 + tok;
   return x;
 }
 
-// Row `row` of a Q tile at `q` (128-byte swizzle, blocks of 128 rows x 64
-// values) from global memory, zeros for a row that is none.  Returns the scale
-// of the row's scores: e4m3 pages want Q as fp16, scaled by 2^e to a largest
-// element in [2^7, 2^8).
+// A warp's 32 rows of a Q tile at `q` (128-byte swizzle, blocks of 128 rows x 64
+// values) from global memory, zeros for rows that are none; `row`: this lane's
+// row in the tile, x what it is.  A row's vectors lie with neighbouring lanes,
+// several rows an instruction.  Returns the scale of the lane's row's scores:
+// e4m3 pages want Q as fp16, scaled by 2^e to a largest element in [2^7, 2^8).
 template <int D, bool E4M3>
 __device__ __forceinline__ float paged_load_q(const PagedParams& p, const PagedRow& x, uint32_t q,
                                               int row) {
-  const uint4* src =
-      reinterpret_cast<const uint4*>(p.q + x.token * p.q_token + x.head * p.q_head);
-  auto at = [&](int c) -> uint32_t {  // 16-byte chunk c of the row
-    return q + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-  };
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  if constexpr (!E4M3) {
-#pragma unroll 8
-    for (int c = 0; c < D / 8; ++c) sts128(at(c), x.live ? src[c] : zero);
-    return p.scale_log2;
-  } else {
-    float mx = 0.0f;
-#pragma unroll 8
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 v = x.live ? src[c] : zero;
-      for (uint32_t y : {v.x, v.y, v.z, v.w})
-        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(y << 16)),
-                             fabsf(__uint_as_float(y & 0xffff0000u))));
+  constexpr int LPR = D == 64 ? 8 : D == 256 ? 32 : 16;  // lanes a row
+  constexpr int RPI = 32 / LPR;                          // rows an instruction
+  constexpr int N = LPR < 8 ? LPR : 8;                   // instructions in flight
+  const int lane = lane_id();
+  const int chunk = lane % LPR, grp = lane / LPR;
+  const unsigned long long mine = reinterpret_cast<unsigned long long>(
+      x.live ? p.q + x.token * p.q_token + x.head * p.q_head : nullptr);
+  float c = p.scale_log2;
+#pragma unroll 1
+  for (int i0 = 0; i0 < LPR; i0 += N) {
+    uint4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned long long src =
+          __shfl_sync(0xffffffffu, mine, (i0 + i) * RPI + grp);
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (src != 0 && chunk < D / 8) v[i] = reinterpret_cast<const uint4*>(src)[chunk];
     }
-    int e = 134 - static_cast<int>(__float_as_uint(mx) >> 23);
-    if (mx == 0.0f || !(mx < INFINITY)) e = 0;
-    e = min(max(e, -120), 120);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    auto half = [&](uint32_t y) {
-      return pack_f16x2(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
-    };
-#pragma unroll 8
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 v = x.live ? src[c] : zero;
-      sts128(at(c), make_uint4(half(v.x), half(v.y), half(v.z), half(v.w)));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = (row & ~31) + (i0 + i) * RPI + grp;
+      if constexpr (E4M3) {
+        float mx = 0.0f;
+        for (uint32_t y : {v[i].x, v[i].y, v[i].z, v[i].w})
+          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(y << 16)),
+                               fabsf(__uint_as_float(y & 0xffff0000u))));
+#pragma unroll
+        for (int d = 1; d < LPR; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        int e = 134 - static_cast<int>(__float_as_uint(mx) >> 23);
+        if (mx == 0.0f || !(mx < INFINITY)) e = 0;
+        e = min(max(e, -120), 120);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        auto half = [&](uint32_t y) {
+          return pack_f16x2(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
+        };
+        v[i] = make_uint4(half(v[i].x), half(v[i].y), half(v[i].z), half(v[i].w));
+        // The scale to the row's own lane.
+        const float down =
+            __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 - e) << 23),
+                        (lane % RPI) * LPR);
+        if (lane / RPI == i0 + i) c = p.scale_log2 * down;
+      }
+      if (chunk < D / 8)
+        sts128(q + (chunk >> 3) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), v[i]);
     }
-    return p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   }
+  return c;
 }
 
 // A tile of BN keys from e4m3 bytes (at `raw`, as the copies leave them) to the
@@ -251,6 +238,13 @@ __device__ __forceinline__ void paged_rescale(uint32_t o_addr, float alpha) {
   }
 }
 
+// 32 bytes to a 32-byte boundary: a whole sector a lane.
+__device__ __forceinline__ void stg256(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // A row's O out of TMEM (TWO: fa times the one at o_addr plus fb times the one
 // at o_addr2): the result if its item lies whole in this CTA, else its part, at
 // row `part_row` of the parts.
@@ -262,6 +256,7 @@ __device__ __forceinline__ void paged_store_row(const PagedParams& p, const Page
   const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
   __nv_bfloat16* dst = p.o + x.token * p.o_token + x.head * p.o_head;
   float* part = p.part_o + part_row * D;
+  const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll 1
   for (int q4 = 0; q4 < D / 32; ++q4) {
     uint32_t v[32];
@@ -278,20 +273,22 @@ __device__ __forceinline__ void paged_store_row(const PagedParams& p, const Page
     }
     if (!x.live) continue;
     if (whole) {
+      uint32_t y[16];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t y[4];
+      for (int u = 0; u < 16; ++u)
+        y[u] = pack_bf16x2(__uint_as_float(v[2 * u]) * inv, __uint_as_float(v[2 * u + 1]) * inv);
+      if (wide) {
+        stg256(dst + q4 * 32, y);
+        stg256(dst + q4 * 32 + 16, y + 8);
+      } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          y[u] = pack_bf16x2(__uint_as_float(v[8 * k + 2 * u]) * inv,
-                             __uint_as_float(v[8 * k + 2 * u + 1]) * inv);
-        reinterpret_cast<uint4*>(dst + q4 * 32)[k] = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int k = 0; k < 4; ++k)
+          reinterpret_cast<uint4*>(dst + q4 * 32)[k] =
+              make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        reinterpret_cast<uint4*>(part + q4 * 32)[k] =
-            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      for (int k = 0; k < 4; ++k) stg256(part + q4 * 32 + 8 * k, v + 8 * k);
     }
   }
   if (x.live) {

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
                           const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
   using C = Tile2Cfg<D, E4M3>;
   constexpr int BN = C::BN;
-  using Seg = PagedSegments<C::BM, BN>;
+  using Walk = PagedWalk<C::BM, BN, 2>;
+  using Seg = PagedSegments<Walk>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -145,12 +146,22 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  const PagedRange range =
-      paged_range<C::BM, BN, C::THREADS>(p, reinterpret_cast<long long*>(smem + C::OFF_SCR));
+  long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_SCR);
   const int cta = blockIdx.x;
-  if (threadIdx.x == 0) p.notes[cta].last = -1;
-  if (range.end <= range.first) return;  // block-uniform, nothing in flight
-
+  {
+    // The roles take their start from shared memory: registers that live
+    // across the change of the register budgets would be spilled.
+    const PagedRange r = paged_range<Walk, C::THREADS>(p, scratch);
+    if (threadIdx.x == 0) p.notes[cta].last = -1;
+    Seg first;
+    if (!first.start(p, r)) return;  // block-uniform, nothing in flight
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      *reinterpret_cast<PagedRange*>(scratch) = r;
+      *reinterpret_cast<Seg*>(scratch + 10) = first;
+    }
+  }
+  static_assert(sizeof(PagedRange) <= 80 && sizeof(Seg) <= 240, "scratch");
   if (warp == 9) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
@@ -164,7 +175,6 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
   const uint32_t sV = sbase + C::OFF_V;
   const uint32_t sR = sbase + C::OFF_RAW;
 
-  Seg seg;
   // Whether the item's rows fill one tile only, and its key tiles go in turn to A and B.
   auto split = [&](const Seg& s) -> bool { return s.w.g.qlen * p.G - s.w.rt * C::BM <= 128; };
 
@@ -172,6 +182,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
     reg_decrease<56>();
     if (warp == 8) {
       // ---------------------------------------------------------- TMA producer
+      Seg seg = *reinterpret_cast<const Seg*>(scratch + 10);
       const int page = 1 << p.page_shift;
       const int box_rows = min(page, BN);
       constexpr int BLOCKS = E4M3 ? 1 : C::SUB;
@@ -192,7 +203,6 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       };
       int nk = 0, nv = 0;  // K and V tiles issued
       bool ok = true;
-      seg.start(p, range);
       do {
         for (int t = seg.t0; ok && t < seg.t1; ++t) {
           const int key0 = t * BN + row0;
@@ -244,6 +254,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer
       if (elect_one()) {
+        Seg seg = *reinterpret_cast<const Seg*>(scratch + 10);
         constexpr uint32_t ID_S = E4M3 ? idesc_f16_f32(128, BN, false)
                                        : idesc_bf16_f32(128, BN, false, false);
         constexpr uint32_t ID_O = E4M3 ? idesc_f16_f32(128, D, true)
@@ -263,8 +274,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
         // first of the tile, bit 2 the key tile's last use, key tile above.
         uint32_t job0 = 0, job1 = 0;
         int waiting = 0, v_tile = -1;
-        seg.start(p, range);
-        bool have = true, sp = split(seg);
+          bool have = true, sp = split(seg);
         int t = seg.t0, x = 0, n = 0;
         bool k_ready = false;
         auto issue_s = [&]() -> bool {
@@ -347,6 +357,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       }
     } else if (warp >= (E4M3 ? 12 : 10)) {
       // ---------------------------------------------------------- helpers
+      Seg seg = *reinterpret_cast<const Seg*>(scratch + 10);
       const int tid = threadIdx.x - 32 * (E4M3 ? 12 : 10);
       auto wait = [&](int b, uint32_t parity) {
         return __all_sync(0xffffffffu,
@@ -354,7 +365,6 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       };
       int n = 0;
       bool ok = true;
-      seg.start(p, range);
       do {
         for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
           const int st = n % C::NS;
@@ -389,6 +399,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       reg_increase<200>();
     else
       reg_increase<224>();
+    Seg seg = *reinterpret_cast<const Seg*>(scratch + 10);
     const int x = warp >> 2;            // tile of this warpgroup
     const int row = threadIdx.x & 127;  // row within the tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -413,7 +424,6 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       return c;
     };
     float2* half_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-    seg.start(p, range);
     bool have = settle(true), ok = true;
     PagedRow r{};
     float c = 0.0f;
@@ -457,7 +467,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       const long long part =
           static_cast<long long>(cta * 2 + (seg.t0 == 0 ? 1 : 0)) * C::BM + (sp ? 0 : x * 128) + row;
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
-        p.notes[cta] = paged_note<C::BM, BN>(p, range, seg.w, seg.unit);
+        p.notes[cta] = paged_note(p, *reinterpret_cast<const PagedRange*>(scratch), seg);
       have = settle(seg.next(p));
       if (have) c = load_q(r);
       if (!(ok = wait(C::B_ODONE + x, (n - 1) & 1, kErrTimeoutEpilogue))) break;
