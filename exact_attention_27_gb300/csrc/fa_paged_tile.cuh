@@ -60,6 +60,18 @@ __device__ __forceinline__ PagedRow paged_row(const PagedParams& p, const PagedS
   return x;
 }
 
+// 16 bytes global -> shared without registers or an L1 line (the shared memory
+// of these kernels leaves L1 some 20 KB, which the rows of two Q tiles in
+// flight would overrun); zeros where `bytes` is 0.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // A warp's 32 rows of a Q tile at `q` (128-byte swizzle, blocks of 128 rows x 64
 // values) from global memory, zeros for rows that are none; `row`: this lane's
 // row in the tile, x what it is.  A row's vectors lie with neighbouring lanes,
@@ -70,48 +82,47 @@ __device__ __forceinline__ float paged_load_q(const PagedParams& p, const PagedR
                                               int row) {
   constexpr int LPR = D == 64 ? 8 : D == 256 ? 32 : 16;  // lanes a row
   constexpr int RPI = 32 / LPR;                          // rows an instruction
-  constexpr int N = LPR < 8 ? LPR : 8;                   // instructions in flight
   const int lane = lane_id();
   const int chunk = lane % LPR, grp = lane / LPR;
+  const bool has = chunk < D / 8;
   const unsigned long long mine = reinterpret_cast<unsigned long long>(
-      x.live ? p.q + x.token * p.q_token + x.head * p.q_head : nullptr);
+      p.q + x.token * p.q_token + x.head * p.q_head);  // (of a row that is none: its item's first)
+  const unsigned alive = __ballot_sync(0xffffffffu, x.live);
+  auto at = [&](int i) -> uint32_t {  // where this lane's vector of instruction i goes
+    const int r = (row & ~31) + i * RPI + grp;
+    return q + (chunk >> 3) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+  };
+#pragma unroll 8
+  for (int i = 0; i < LPR; ++i) {
+    const int r = i * RPI + grp;
+    const unsigned long long src = __shfl_sync(0xffffffffu, mine, r);
+    if (has)
+      cp_async16(at(i), reinterpret_cast<const uint4*>(src) + chunk, (alive >> r) & 1 ? 16 : 0);
+  }
+  cp_async_wait_all();
   float c = p.scale_log2;
-#pragma unroll 1
-  for (int i0 = 0; i0 < LPR; i0 += N) {
-    uint4 v[N];
+  if constexpr (E4M3) {
+#pragma unroll 4
+    for (int i = 0; i < LPR; ++i) {
+      uint4 v = has ? lds128(at(i)) : make_uint4(0, 0, 0, 0);
+      float mx = 0.0f;
+      for (uint32_t y : {v.x, v.y, v.z, v.w})
+        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(y << 16)),
+                             fabsf(__uint_as_float(y & 0xffff0000u))));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const unsigned long long src =
-          __shfl_sync(0xffffffffu, mine, (i0 + i) * RPI + grp);
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (src != 0 && chunk < D / 8) v[i] = reinterpret_cast<const uint4*>(src)[chunk];
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int r = (row & ~31) + (i0 + i) * RPI + grp;
-      if constexpr (E4M3) {
-        float mx = 0.0f;
-        for (uint32_t y : {v[i].x, v[i].y, v[i].z, v[i].w})
-          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(y << 16)),
-                               fabsf(__uint_as_float(y & 0xffff0000u))));
-#pragma unroll
-        for (int d = 1; d < LPR; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        int e = 134 - static_cast<int>(__float_as_uint(mx) >> 23);
-        if (mx == 0.0f || !(mx < INFINITY)) e = 0;
-        e = min(max(e, -120), 120);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        auto half = [&](uint32_t y) {
-          return pack_f16x2(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
-        };
-        v[i] = make_uint4(half(v[i].x), half(v[i].y), half(v[i].z), half(v[i].w));
-        // The scale to the row's own lane.
-        const float down =
-            __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 - e) << 23),
-                        (lane % RPI) * LPR);
-        if (lane / RPI == i0 + i) c = p.scale_log2 * down;
-      }
-      if (chunk < D / 8)
-        sts128(q + (chunk >> 3) * (128 * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), v[i]);
+      for (int d = 1; d < LPR; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      int e = 134 - static_cast<int>(__float_as_uint(mx) >> 23);
+      if (mx == 0.0f || !(mx < INFINITY)) e = 0;
+      e = min(max(e, -120), 120);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      auto half = [&](uint32_t y) {
+        return pack_f16x2(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xffff0000u) * up);
+      };
+      if (has) sts128(at(i), make_uint4(half(v.x), half(v.y), half(v.z), half(v.w)));
+      // The scale to the row's own lane.
+      const float down = __shfl_sync(
+          0xffffffffu, __uint_as_float(static_cast<uint32_t>(127 - e) << 23), (lane % RPI) * LPR);
+      if (lane / RPI == i) c = p.scale_log2 * down;
     }
   }
   return c;
