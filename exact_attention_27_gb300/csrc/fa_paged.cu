@@ -44,6 +44,12 @@ namespace {
 constexpr float kRescaleThreshold = 8.0f;
 constexpr int kTK = 64;  // keys per tile
 
+// CTAs an SM.  A CTA's four warps each wait for loads, conversions and products
+// in turn, so more of them hide more, as registers and shared memory allow; with
+// bytes half as many, e4m3 pages want three (120,000 keys of 8 heads, d = 128: 59
+// us with two).
+constexpr int rows_occupancy(int d, bool e4m3) { return d == 256 ? 1 : e4m3 ? 3 : 2; }
+
 template <int D_, bool E4M3_>
 struct RowsCfg {
   static constexpr int D = D_;
@@ -55,10 +61,11 @@ struct RowsCfg {
   static constexpr int BLOCK = kTK * 128;
   static constexpr int STAGE = 2 * SUB * BLOCK;                 // K and V
   static constexpr int MERGE = 2 * ROWS * D * 4;                // two of the four key groups' O
-  static constexpr int OCC = D <= 128 ? 2 : 1;       // CTAs an SM
-  static constexpr int BUDGET = (OCC == 2 ? 112 : 224) * 1024;
-  // At d = 256 the fragments of Q (64 registers) lie in shared memory.
-  static constexpr bool QS = D == 256;
+  static constexpr int OCC = rows_occupancy(D, E4M3);           // CTAs an SM
+  static constexpr int BUDGET = (OCC == 3 ? 74 : OCC == 2 ? 112 : 224) * 1024;
+  // At d = 256 and with three CTAs the fragments of Q (64 or 32 registers) lie
+  // in shared memory.
+  static constexpr bool QS = D == 256 || OCC == 3;
   static constexpr int QBYTES = QS ? ROWS * D * 2 : 0;
   static constexpr int FIT = (BUDGET - MERGE - QBYTES - 3072) / STAGE;
   static constexpr int NS = FIT > 8 ? 8 : FIT;
@@ -142,8 +149,8 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
   const PagedRange range =
       paged_range<Walk, C::THREADS>(p, reinterpret_cast<long long*>(smem + C::OFF_SCR));
   __syncthreads();
@@ -557,8 +564,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   constexpr int GROUPS = kJoinThreads / LANES;
   __shared__ float4 acc[GROUPS][LANES];
   __shared__ float2 state[GROUPS];
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
   const int cta = blockIdx.x;
   const PagedNote note = p.notes[cta];
   if (note.last < 0) return;
@@ -649,7 +656,9 @@ int sm_count() {
 int rows_for(long long most, int d) { return most <= 16 ? 16 : paged_tile_rows(d); }
 
 // CTAs of a launch with `rows` rows an item.
-int ctas_for(int sms, int rows, int d) { return sms * (rows == 16 && d <= 128 ? 2 : 1); }
+int ctas_for(int sms, int rows, int d, bool e4m3) {
+  return sms * (rows == 16 ? rows_occupancy(d, e4m3) : 1);
+}
 
 // Workspace: notes, (m, l), O; each part 256-byte aligned.
 struct PartLayout {
@@ -708,7 +717,7 @@ size_t fa_forward_paged_workspace_bytes(int H_q, int H_kv, int d, int T, int max
   if (d != 64 && d != 96 && d != 128 && d != 256) return 0;
   const long long most = static_cast<long long>(std::min(T, max_q_len)) * (H_q / H_kv);
   const int rows = rows_for(most, d);
-  return part_layout(ctas_for(sm_count(), rows, d), rows, d).total;
+  return part_layout(ctas_for(sm_count(), rows, d, true), rows, d).total;  // (the most)
 }
 
 fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* q,
@@ -736,7 +745,7 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   const int G = H_q / H;
   const long long most = static_cast<long long>(std::min(T, batch->max_q_len)) * G;
   const int rows = rows_for(most, d);
-  const int ctas = ctas_for(sms, rows, d);
+  const int ctas = ctas_for(sms, rows, d, cache->dtype == FA_CACHE_E4M3);
   const PartLayout lay = part_layout(ctas, rows, d);
   if (!workspace || !aligned16(workspace) || workspace_bytes < lay.total)
     return FA_ERR_INVALID_ARGUMENT;

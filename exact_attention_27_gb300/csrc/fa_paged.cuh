@@ -213,7 +213,8 @@ struct PagedRange {
   }
 };
 
-// Every thread of the block calls this; `scratch`: 40 long longs of shared memory.
+// Every thread of the block calls this; `scratch`: 40 long longs of shared
+// memory, free again after the block's next barrier.
 template <typename Walk, int THREADS>
 __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long long* scratch) {
   constexpr int WARPS = THREADS / 32;
@@ -251,6 +252,31 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
   r.rem = 0;
   r.per_head = 1;
   r.first = r.end = 0;
+  auto divide = [&]() -> bool {  // false: no units for this CTA
+    if (r.units == 0) return false;
+    r.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x),
+                                  paged_div(r.units + p.min_units - 1, p.min_units)));
+    if (static_cast<int>(blockIdx.x) >= r.ctas) return false;
+    r.first = paged_div(blockIdx.x * r.units, r.ctas);
+    r.end = paged_div((blockIdx.x + 1) * r.units, r.ctas);
+    return true;
+  };
+  if (p.S <= 32) {
+    // Every warp for itself, without barriers.
+    const long long mine = units_of(lane);
+    long long x = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    r.units = __shfl_sync(0xffffffffu, x, 31);
+    if (!divide()) return r;
+    r.seq = __ffs(__ballot_sync(0xffffffffu, r.first < x)) - 1;
+    r.rem = r.first - __shfl_sync(0xffffffffu, x - mine, r.seq);
+    r.per_head = paged_div(__shfl_sync(0xffffffffu, mine, r.seq), p.Hkv);
+    return r;
+  }
   long long mine = units_of(tid), all;
   long long pre = scan(mine, all);
   r.units = all;
@@ -258,12 +284,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
     scan(units_of(base + tid), all);
     r.units += all;
   }
-  if (r.units == 0) return r;  // (block-uniform, as below)
-  r.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x),
-                                paged_div(r.units + p.min_units - 1, p.min_units)));
-  if (static_cast<int>(blockIdx.x) >= r.ctas) return r;
-  r.first = paged_div(blockIdx.x * r.units, r.ctas);
-  r.end = paged_div((blockIdx.x + 1) * r.units, r.ctas);
+  if (!divide()) return r;  // block-uniform
   if (tid == 0) {
     scratch[32] = scratch[33] = 0;
     scratch[34] = 1;

@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
   long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_SCR);
   const int cta = blockIdx.x;
   {

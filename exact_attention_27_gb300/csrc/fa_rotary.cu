@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kThreads, 4) fa_turn_kernel(const __grid_const
   __shared__ long long place[TOK];  // cache offset of the token's row in head 0; -1: not stored
   __shared__ int seq_pos[TOK];      // place in the sequence; INT_MIN: no sequence
 
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
 
   const int tid = threadIdx.x;
   const long long t0 = static_cast<long long>(blockIdx.x) * TOK;
