@@ -223,13 +223,10 @@ def _rotary_rows(x, out, device, name):
                            shape[1])
 
 
-def _turn(fn, q, q_out, k, k_out, positions, rotary, stream):
+def _launch_turn(fn, rows_q, rows_k, shape, k, positions, rotary, stream):
+    B, _, N, d = shape
     device = rotary.device
-    rows_q = _rotary_rows(q, q_out, device, "q")
-    B, _, N, d = q.shape
-    rows_k = None
     if k is not None:
-        rows_k = _rotary_rows(k, k_out, device, "k")
         Bk, _, Nk, dk = k.shape
         if Bk != B or Nk != N or dk != d:
             raise ValueError("k must be [B, H_kv, N, d] with q's B, N and d")
@@ -251,6 +248,13 @@ def _turn(fn, q, q_out, k, k_out, positions, rotary, stream):
         raise FaError(status, fn)
 
 
+def _turn(fn, q, q_out, k, k_out, positions, rotary, stream):
+    device = rotary.device
+    _launch_turn(fn, _rotary_rows(q, q_out, device, "q"),
+                 None if k is None else _rotary_rows(k, k_out, device, "k"), q.shape, k, positions,
+                 rotary, stream)
+
+
 def fa_rotary(q, q_out, k, k_out, positions, rotary, stream=None):
     """fa_rotary of include/fa.h on torch tensors: q [B, H_q, N, d] (and k [B, H_kv, N, d], or
     None) bf16 views turned into q_out and k_out, which may be q and k; positions
@@ -265,7 +269,8 @@ def fa_rotary_backward(dq_out, dq, dk_out, dk, positions, rotary, stream=None):
 
 
 def rotary_forward(q, k, positions, rotary, stream=None):
-    """Allocates and returns q and k (None: only q) turned by their positions."""
+    """Allocates and returns q and k (None: only q) turned by their positions, contiguous (what
+    attention_forward takes)."""
     return _new_turn("fa_rotary", q, k, positions, rotary, stream)
 
 
@@ -275,22 +280,34 @@ def rotary_backward(dq, dk, positions, rotary, stream=None):
     return _new_turn("fa_rotary_backward", dq, dk, positions, rotary, stream)
 
 
-def _empty_rows(x):
-    # (an expanded view's layout would keep its zero strides)
-    if 0 in x.stride():
-        return _torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    return _torch.empty_like(x)
+def _new_rows(x, device, name):
+    """A contiguous output for x, and the rows of both."""
+    shape, a = x.shape, x.stride()
+    if x.dtype is not _BF16 or x.get_device() != device or len(a) != 4 or a[3] != 1 or \
+            (a[0] | a[1] | a[2]) & 7:
+        a = _strides(name, x, 4, device)
+    # (empty_like is the quicker call)
+    out = _torch.empty_like(x) if x.is_contiguous() else \
+        _torch.empty(shape, dtype=_BF16, device=x.device)
+    _, H, N, d = shape
+    return out, _lib.RotaryRows(x.data_ptr(), out.data_ptr(), a[0], a[1], a[2], H * N * d, N * d, d,
+                                H)
 
 
 def _new_turn(fn, q, k, positions, rotary, stream):
     if stream is not None:
         with _on(stream):
-            q_out = _empty_rows(q)
-            k_out = None if k is None else _empty_rows(k)
-    else:
-        q_out = _empty_rows(q)
-        k_out = None if k is None else _empty_rows(k)
-    _turn(fn, q, q_out, k, k_out, positions, rotary, stream)
+            return _new_turn_here(fn, q, k, positions, rotary, stream)
+    return _new_turn_here(fn, q, k, positions, rotary, None)
+
+
+def _new_turn_here(fn, q, k, positions, rotary, stream):
+    device = rotary.device
+    q_out, rows_q = _new_rows(q, device, "q")
+    k_out = rows_k = None
+    if k is not None:
+        k_out, rows_k = _new_rows(k, device, "k")
+    _launch_turn(fn, rows_q, rows_k, q.shape, k, positions, rotary, stream)
     return q_out, k_out
 
 
