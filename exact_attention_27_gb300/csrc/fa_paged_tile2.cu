@@ -34,9 +34,9 @@
 // 200 / 56 / 56 (the sums are the launch totals 504 and 512).
 //
 // Tensor memory: S of tile x at columns 128 x (P, packed in pairs, over its
-// first half), O at 256 + DP x.  A tile's next S follows its own O += P V, and
-// its O is first written for an item by a product that waits for a P made
-// after the epilogue of the item before.
+// first half), O at 256 + DP x.  A tile's next S follows its own O += P V.  The
+// products of an item begin with tile A's, and wait for a P that A's warps make
+// after the epilogue of the item before, so they overwrite no O still in use.
 //
 // Every wait is bounded (about a second); on expiry the kernel sets an error
 // bit, every role skips its remaining work and the CTA exits.
@@ -88,8 +88,7 @@ struct Tile2Cfg {
   static constexpr int B_PFULL = B_SFULL + 2;    // [2] 4 warps
   static constexpr int B_ODONE = B_PFULL + 2;    // [2] O_x += P_x V
   static constexpr int B_SPLIT = B_ODONE + 2;    // 4 warps: B's half of a split item is final
-  static constexpr int B_JOINED = B_SPLIT + 1;   // 4 warps: A has read it
-  static constexpr int B_DRAIN = B_JOINED + 1;
+  static constexpr int B_DRAIN = B_SPLIT + 1;
   static constexpr int NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
@@ -135,7 +134,6 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       mbar_init(bar(C::B_REMPTY + s), C::HELPERS);
     }
     mbar_init(bar(C::B_SPLIT), 4);
-    mbar_init(bar(C::B_JOINED), 4);
     mbar_init(bar(C::B_DRAIN), 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -430,7 +428,6 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
     if (have) c = load_q(r);
     uint32_t n = 0;       // key tiles of this warpgroup
     uint32_t joins = 0;   // split items of both warpgroups
-    bool unread = false;  // B: A may still be reading this O
     while (have) {
       float m = -INFINITY;  // reference maximum, log2 domain
       float l = 0.0f;
@@ -448,11 +445,6 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
           if (!(ok = wait(C::B_ODONE + x, (n - 1) & 1, kErrTimeoutSoftmax))) break;
           tc_fence_after();
           paged_rescale<D>(o_addr, alpha);
-        }
-        if (unread) {
-          // The product that this P allows overwrites O.
-          if (!(ok = wait(C::B_JOINED, (joins - 1) & 1, kErrTimeoutSoftmax))) break;
-          unread = false;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -479,7 +471,6 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
         tc_fence_before();
         mbar_arrive_warp(bar(C::B_SPLIT));
         ++joins;
-        unread = true;
       } else {
         if (!(ok = wait(C::B_SPLIT, joins++ & 1, kErrTimeoutEpilogue))) break;
         tc_fence_after();
@@ -489,11 +480,10 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
         const float fa = ex2_approx(m - ref), fb = ex2_approx(b.x - ref);
         paged_store_row<D, true>(p, now, o_addr, o_addr + C::DP, fa, fb, whole, part, m2,
                                  l * fa + b.y * fb);
-        tc_fence_before();
-        mbar_arrive_warp(bar(C::B_JOINED));
       }
       tc_fence_before();
-      // (The next item's first O product waits for this thread's next P.)
+      // The next item's first O products wait for P of tile A, which its warps
+      // make after this: until then neither O, and no (m, l), is overwritten.
     }
   }
 
