@@ -33,9 +33,8 @@
 // Registers: bf16 384 threads at 168: 224 / 224 / 56; e4m3 512 at 128: 200 /
 // 200 / 56 / 56 (the sums are the launch totals 504 and 512).
 //
-// Tensor memory: S buffers of 128 columns (P, packed in pairs, over the first
-// half), one a tile, or at d = 64 three in turn; then O of A and B.  An S follows
-// O += P V of the S before it in its buffer, in the tensor pipe's order.  The
+// Tensor memory: S of tile x at columns 128 x (P, packed in pairs, over its
+// first half), O at 256 + DP x.  A tile's next S follows its own O += P V.  The
 // products of an item begin with tile A's, and wait for a P that A's warps make
 // after the epilogue of the item before, so they overwrite no O still in use.
 //
@@ -85,26 +84,17 @@ struct Tile2Cfg {
   static constexpr int B_VFIX = B_VEMPTY + NS;   // [NS] the helpers: V is whole and finite
   static constexpr int B_RFULL = B_VFIX + NS;    // [NR] bytes
   static constexpr int B_REMPTY = B_RFULL + NR;  // [NR] the helpers
-  // S buffers.  At d = 64 the O accumulators leave room for three, which the
-  // S products take in turn (the m-th buffer m mod 3), so that a tile's next S
-  // is there while its softmax still works on the last; else tile x has its own.
-  static constexpr bool ROT = DP == 64;
-  static constexpr int NSB = ROT ? 3 : 2;
-  // S is there: by tile, and at d = 64, where a tile may have two, in turn.  (By
-  // buffer, a tile that has had nothing to do would take an older phase for its
-  // own.)
-  static constexpr int B_SFULL = B_REMPTY + NR;             // [2] or [2][2]
-  static constexpr int B_PFULL = B_SFULL + (ROT ? 4 : 2);   // [NSB] 4 warps
-  static constexpr int B_ODONE = B_PFULL + NSB;   // [2] O_x += P_x V
-  static constexpr int B_OFIN = B_ODONE + 2;      // [2] an item's last of them
-  static constexpr int B_SPLIT = B_OFIN + 2;    // 4 warps: B's half of a split item is final
+  static constexpr int B_SFULL = B_REMPTY + NR;  // [2] S of tile x
+  static constexpr int B_PFULL = B_SFULL + 2;    // [2] 4 warps
+  static constexpr int B_ODONE = B_PFULL + 2;    // [2] O_x += P_x V
+  static constexpr int B_SPLIT = B_ODONE + 2;    // 4 warps: B's half of a split item is final
   static constexpr int B_DRAIN = B_SPLIT + 1;
   static constexpr int NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = E4M3 ? 512 : 384;
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t COL_O = ROT ? 384 : 256;
+  static constexpr uint32_t COL_O = 256;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -128,11 +118,10 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(C::B_QFULL + x), 4);
+      mbar_init(bar(C::B_SFULL + x), 1);
+      mbar_init(bar(C::B_PFULL + x), 4);
       mbar_init(bar(C::B_ODONE + x), 1);
-      mbar_init(bar(C::B_OFIN + x), 1);
     }
-    for (int b = C::B_SFULL; b < C::B_PFULL; ++b) mbar_init(bar(b), 1);
-    for (int b = 0; b < C::NSB; ++b) mbar_init(bar(C::B_PFULL + b), 4);
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(bar(C::B_KFULL + s), E4M3 ? C::HELPERS : 1);
       mbar_init(bar(C::B_KEMPTY + s), 1);
@@ -274,18 +263,15 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
         auto wait = [&](int b, uint32_t parity) {
           return mbar_wait(bar(b), parity, abort_flag, p.err, kErrTimeoutMma);
         };
-        // Parities of the next Q of each tile (bits 0, 1), of the next P of each
-        // buffer (bits 2 to 4) and of the number of S of each tile (bits 5, 6); in
-        // registers, as the issuer's own latency lies
-        // between P and O += P V.
+        // Parities of the next Q (bits 0, 1) and P (bits 2, 3) of each tile; in
+        // registers, as the issuer's own latency lies between P and O += P V.
         uint32_t phase = 0;
         // Products S, in order of the key tiles (A before B), run ahead of the
-        // products P V, which follow in the same order: an S may be issued when
-        // O += P V of the S before it in its buffer has been.  Those that wait for
-        // their P: bit 0 tile, bits 1, 2 the item's first and last of the tile, bit
-        // 3 the key tile's last use, bits 4, 5 the buffer, the key tile above.
-        uint32_t job0 = 0, job1 = 0, job2 = 0;
-        int waiting = 0, v_tile = -1, buf = 0;
+        // products P V, which follow in the same order: at most one S a tile is
+        // waiting for its P.  job0 and job1 are those: bit 0 tile, bit 1 the item's
+        // first of the tile, bit 2 the key tile's last use, key tile above.
+        uint32_t job0 = 0, job1 = 0;
+        int waiting = 0, v_tile = -1;
           bool have = true, sp = split(seg);
         int t = seg.t0, x = 0, n = 0;
         bool k_ready = false;
@@ -299,9 +285,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
           if (!k_ready && !wait(C::B_KFULL + st, (n / C::NS) & 1)) return false;
           k_ready = true;
           tc_fence_after();
-          const int b = C::ROT ? buf : x;
-          if (C::ROT) buf = buf == 2 ? 0 : buf + 1;
-          const uint32_t d_tmem = tmem + b * 128;
+          const uint32_t d_tmem = tmem + x * 128;
           const uint64_t qd = desc_add(q_desc, x * C::TILE);
           const uint64_t kd = desc_add(k_desc, st * C::TILE);
           mma_ss_k<ID_S, 0>(d_tmem, qd, kd);
@@ -310,24 +294,15 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
             const uint32_t off = (kk >> 2) * C::BLOCK + (kk & 3) * 32;
             mma_ss_k<ID_S, 1>(d_tmem, desc_add(qd, off), desc_add(kd, off));
           }
-          if (C::ROT) {
-            mma_commit(bar(C::B_SFULL + 2 * x + ((phase >> (5 + x)) & 1)));
-            phase ^= 32u << x;
-          } else {
-            mma_commit(bar(C::B_SFULL + x));
-          }
+          mma_commit(bar(C::B_SFULL + x));
           const bool last = sp || x == 1;
           if (last) mma_commit(bar(C::B_KEMPTY + st));
-          const bool end = t + (sp ? 2 : 1) >= seg.t1;
-          const uint32_t job = (static_cast<uint32_t>(n) << 6) | (static_cast<uint32_t>(b) << 4) |
-                               (last ? 8u : 0u) | (end ? 4u : 0u) | (first ? 2u : 0u) |
-                               static_cast<uint32_t>(x);
+          const uint32_t job = (static_cast<uint32_t>(n) << 3) | (last ? 4u : 0u) |
+                               (first ? 2u : 0u) | static_cast<uint32_t>(x);
           if (waiting == 0)
             job0 = job;
-          else if (waiting == 1)
-            job1 = job;
           else
-            job2 = job;
+            job1 = job;
           ++waiting;
           // The next S: tile B of the same keys, or the next key tile.
           x ^= 1;
@@ -344,29 +319,23 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
         };
         bool ok = true;
         while (true) {
-          // (With three buffers an item's first S, which waits for Q, leaves no two
-          // products waiting: Q may need the epilogue of the first of them.)
-          while (ok && have &&
-                 (C::ROT ? waiting < ((sp ? t - seg.t0 < 2 : t == seg.t0) ? 2 : 3)
-                         : waiting == 0 ||
-                               (waiting == 1 && (job0 & 1) != static_cast<uint32_t>(x))))
+          while (ok && have && (waiting == 0 || (waiting == 1 && (job0 & 1) != static_cast<uint32_t>(x))))
             ok = issue_s();
           if (!ok || waiting == 0) break;
           const uint32_t job = job0;
           job0 = job1;
-          job1 = job2;
           --waiting;
-          const int y = job & 1, b = (job >> 4) & 3, tile = job >> 6, st = tile % C::NS;
+          const int y = job & 1, tile = job >> 3, st = tile % C::NS;
           if (tile != v_tile) {
             ok = (E4M3 || wait(C::B_VFULL + st, (tile / C::NS) & 1)) &&
                  wait(C::B_VFIX + st, (tile / C::NS) & 1);
             v_tile = tile;
           }
-          if (!ok || !(ok = wait(C::B_PFULL + b, (phase >> (2 + b)) & 1))) break;
-          phase ^= 4u << b;
+          if (!ok || !(ok = wait(C::B_PFULL + y, (phase >> (2 + y)) & 1))) break;
+          phase ^= 4u << y;
           tc_fence_after();
           const uint64_t vd = desc_add(v_desc, st * C::TILE);
-          const uint32_t pa = tmem + b * 128;
+          const uint32_t pa = tmem + y * 128;
           const uint32_t od = tmem + C::COL_O + y * C::DP;
           if (job & 2)
             mma_ts_k<ID_O, 0>(od, pa, vd);
@@ -376,8 +345,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
           for (int kk = 1; kk < BN / 16; ++kk)
             mma_ts_k<ID_O, 1>(od, pa + kk * 8, desc_add(vd, kk * 2048));
           mma_commit(bar(C::B_ODONE + y));
-          if (job & 4) mma_commit(bar(C::B_OFIN + y));
-          if (job & 8) mma_commit(bar(C::B_VEMPTY + st));
+          if (job & 4) mma_commit(bar(C::B_VEMPTY + st));
         }
         if (*abort_flag) {
           // Let the MMAs already issued finish before tensor memory is released.
@@ -433,6 +401,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
     const int x = warp >> 2;            // tile of this warpgroup
     const int row = threadIdx.x & 127;  // row within the tile
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_off + x * 128;
     const uint32_t o_addr = tmem + lane_off + C::COL_O + x * C::DP;
     // Waits are made warp-uniform: the TMEM loads and stores are
     // warp-collective, so either every lane goes on or every lane stops.
@@ -441,13 +410,8 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
     };
     // The next item with work for this tile (the one at hand if it has): a
     // split item of one key tile has none for B.
-    uint32_t m0 = 0;  // S products before the item's
-    auto next = [&]() -> bool {
-      m0 += (seg.t1 - seg.t0) * (split(seg) ? 1 : 2);
-      return seg.next(p);
-    };
     auto settle = [&](bool have) {
-      while (have && x == 1 && split(seg) && seg.t1 - seg.t0 == 1) have = next();
+      while (have && x == 1 && split(seg) && seg.t1 - seg.t0 == 1) have = seg.next(p);
       return have;
     };
     auto load_q = [&](PagedRow& r) -> float {
@@ -463,34 +427,28 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
     float c = 0.0f;
     if (have) c = load_q(r);
     uint32_t n = 0;       // key tiles of this warpgroup
-    uint32_t items = 0;   // its items
-    uint32_t joins = 0;   // A: split items joined
+    uint32_t joins = 0;   // split items of both warpgroups
     while (have) {
       float m = -INFINITY;  // reference maximum, log2 domain
       float l = 0.0f;
       const bool sp = split(seg);
       const int t_first = sp ? seg.t0 + x : seg.t0;
       for (int t = t_first; t < seg.t1; t += sp ? 2 : 1, ++n) {
-        // This S: its number among all, and its buffer.
-        const uint32_t number = m0 + (sp ? t - seg.t0 : 2 * (t - seg.t0) + x);
-        const uint32_t b = C::ROT ? number % 3 : x;
-        if (!(ok = wait(C::B_SFULL + (C::ROT ? 2 * x + (n & 1) : x), (C::ROT ? n >> 1 : n) & 1,
-                        kErrTimeoutSoftmax)))
-          break;
+        if (!(ok = wait(C::B_SFULL + x, n & 1, kErrTimeoutSoftmax))) break;
         tc_fence_after();
         bool moved;
-        const float alpha = paged_softmax<BN, E4M3>(tmem + lane_off + b * 128, t * BN + BN - 1 > r.all_see,
+        const float alpha = paged_softmax<BN, E4M3>(s_addr, t * BN + BN - 1 > r.all_see,
                                                     r.last - t * BN, c, m, l, moved);
         if (t > t_first && __any_sync(0xffffffffu, moved)) {
-          // O is final before it is rescaled.  (This S was issued after the
-          // product before the last one, so the barrier is at most a phase behind.)
+          // O is final before it is rescaled (S of this tile was issued after
+          // O += P V of the one before, so this does not wait long).
           if (!(ok = wait(C::B_ODONE + x, (n - 1) & 1, kErrTimeoutSoftmax))) break;
           tc_fence_after();
           paged_rescale<D>(o_addr, alpha);
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive_warp(bar(C::B_PFULL + b));
+        mbar_arrive_warp(bar(C::B_PFULL + x));
       }
       if (!ok) break;
       // ---------------------------------------------------------- end of the item
@@ -502,10 +460,9 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
           static_cast<long long>(cta * 2 + (seg.t0 == 0 ? 1 : 0)) * C::BM + (sp ? 0 : x * 128) + row;
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
         p.notes[cta] = paged_note(p, *reinterpret_cast<const PagedRange*>(scratch), seg);
-      have = settle(next());
+      have = settle(seg.next(p));
       if (have) c = load_q(r);
-      // (With three buffers B_ODONE may be two phases behind here.)
-      if (!(ok = wait(C::B_OFIN + x, items++ & 1, kErrTimeoutEpilogue))) break;
+      if (!(ok = wait(C::B_ODONE + x, (n - 1) & 1, kErrTimeoutEpilogue))) break;
       tc_fence_after();
       if (!both) {
         paged_store_row<D, false>(p, now, o_addr, 0, 1.0f, 0.0f, whole, part, m, l);
@@ -513,6 +470,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
         half_ml[row] = make_float2(m, l);
         tc_fence_before();
         mbar_arrive_warp(bar(C::B_SPLIT));
+        ++joins;
       } else {
         if (!(ok = wait(C::B_SPLIT, joins++ & 1, kErrTimeoutEpilogue))) break;
         tc_fence_after();

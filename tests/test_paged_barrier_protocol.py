@@ -112,36 +112,24 @@ def _loads(mc, tiles, ns, nr, k, v, raw):
     return producer, helper
 
 
-def _two_tiles(items, ns, nr, rng, rot=False, wait_split=True, s_after_pv=True, in_order=True,
-               final=True, early_q=True,
-               own_full=True):
+def _two_tiles(items, ns, nr, rng, wait_split=True, s_after_pv=True, in_order=True):
     """items: (key tiles, split).  A split item's even key tiles go to tile 0, its odd to 1.
-    rot: three S buffers in turn (d = 64) instead of one a tile.  in_order: an item's products
-    begin with tile 0 (A), whose warps store and join the item before.  final: the epilogue waits
-    for a barrier of the item's last product.  early_q: an item's first scores, which wait for its
-    Q, leave no two products waiting whose epilogue that Q might need.  own_full: the barriers of
-    the scores are the tile's own (by buffer, a tile that has had nothing to do would take an
-    older phase for its own)."""
+    in_order: an item's products begin with tile 0 (A), whose warps store and join the item
+    before."""
     mc = _Machine(rng)
     total = sum(n for n, _ in items)
     k, v, raw = [None] * ns, [None] * ns, [None] * max(nr, 1)
-    q, s = [None, None], [None] * 3
+    q, s = [None, None], [None, None]
     o = [[], []]            # (item, key tile) products in each tile's O
     producer, helper = _loads(mc, total, ns, nr, k, v, raw)
     first = (0, 1) if in_order else (1, 0)
-    # (tile, key tile, item, first of the item in the tile, K's last use, buffer, its use, last of
-    # the item in the tile)
-    jobs = []
-    uses = [0, 0, 0]
+    jobs = []               # (tile, key tile, item, first of the item in the tile, K's last use)
     n = 0
     for it, (tiles, split) in enumerate(items):
         for t in range(tiles):
             xs = [t % 2] if split else list(first)
             for x in xs:
-                b = len(jobs) % 3 if rot else x
-                jobs.append((x, n, it, t < 2 if split else t == 0, x == xs[-1], b, uses[b],
-                             t + (2 if split else 1) >= tiles))
-                uses[b] += 1
+                jobs.append((x, n, it, t < 2 if split else t == 0, x == xs[-1]))
             n += 1
 
     def helpers():
@@ -152,16 +140,13 @@ def _two_tiles(items, ns, nr, rng, rot=False, wait_split=True, s_after_pv=True, 
                 n += 1
 
     def issuer():
-        q_phase, waiting, k_ready, v_ready, issued = [0, 0], [], -1, -1, [0, 0]
-        room = 3 if rot else 2
-        if not s_after_pv:
-            room += 1
+        q_phase, p_phase, waiting, k_ready, v_ready = [0, 0], [0, 0], [], -1, -1
         ahead = iter(jobs)
         nxt = next(ahead, None)
         while nxt or waiting:
-            while nxt and len(waiting) < (2 if rot and nxt[3] and early_q else room) and (
-                    rot or not s_after_pv or not waiting or waiting[0][0] != nxt[0]):
-                x, n, it, first, last, b, use, end = nxt
+            while nxt and (not waiting or (len(waiting) == 1 and waiting[0][0] != nxt[0]) or
+                           (not s_after_pv and len(waiting) == 1)):
+                x, n, it, first, last = nxt
                 if first:
                     yield ("QFULL", x), q_phase[x]
                     q_phase[x] ^= 1
@@ -169,34 +154,31 @@ def _two_tiles(items, ns, nr, rng, rot=False, wait_split=True, s_after_pv=True, 
                     yield ("KFULL", n % ns), (n // ns) & 1
                     k_ready = n
 
-                def scores(x=x, n=n, it=it, b=b):
+                def scores(x=x, n=n, it=it):
                     _expect(k[n % ns] == n, "S read another K")
                     _expect(q[x] == it, "S read another Q")
-                    s[b] = ("S", x, n)
+                    s[x] = ("S", n)
                 mc.pipe.append(scores)
-                full = (x, issued[x] % 2) if rot else x
-                issued[x] += 1
-                mc.pipe.append(lambda full=full: mc.arrive(("SFULL", full)))
+                mc.pipe.append(lambda x=x: mc.arrive(("SFULL", x)))
                 if last:
                     mc.pipe.append(lambda n=n: mc.arrive(("KEMPTY", n % ns)))
                 waiting.append(nxt)
                 nxt = next(ahead, None)
-            x, n, it, first, last, b, use, end = waiting.pop(0)
+            x, n, it, first, last = waiting.pop(0)
             if n != v_ready:
                 if not nr:
                     yield ("VFULL", n % ns), (n // ns) & 1
                 yield ("VFIX", n % ns), (n // ns) & 1
                 v_ready = n
-            yield ("PFULL", b), use & 1
+            yield ("PFULL", x), p_phase[x]
+            p_phase[x] ^= 1
 
-            def product(x=x, n=n, it=it, first=first, b=b):
+            def product(x=x, n=n, it=it, first=first):
                 _expect(v[n % ns] == n, "P V read another V")
-                _expect(s[b] == ("P", x, n), "P V read no P of its own")
+                _expect(s[x] == ("P", n), "P V read no P of its own")
                 o[x] = ([] if first else o[x]) + [(it, n)]
             mc.pipe.append(product)
             mc.pipe.append(lambda x=x: mc.arrive(("ODONE", x)))
-            if end:
-                mc.pipe.append(lambda x=x: mc.arrive(("OFIN", x)))
             if last:
                 mc.pipe.append(lambda n=n: mc.arrive(("VEMPTY", n % ns)))
 
@@ -211,27 +193,18 @@ def _two_tiles(items, ns, nr, rng, rot=False, wait_split=True, s_after_pv=True, 
         if todo:
             load(todo[0])
         for at, it in enumerate(todo):
-            for i, (_, n, _it, _f, _l, b, use, _e) in enumerate(mine[it]):
-                if not rot:
-                    yield ("SFULL", x), done & 1
-                elif own_full:
-                    yield ("SFULL", (x, done % 2)), done // 2 & 1
-                else:
-                    yield ("SFULL", (x, 0)), use & 1
-                _expect(s[b] == ("S", x, n), "softmax read other scores")
+            for i, (_, n, *_rest) in enumerate(mine[it]):
+                yield ("SFULL", x), done & 1
+                _expect(s[x] == ("S", n), "softmax read other scores")
                 if i and rng.random() < 0.5:
                     yield ("ODONE", x), (done - 1) & 1
                     _expect(o[x] == [(it, j[1]) for j in mine[it][:i]], "rescale")
-                s[b] = ("P", x, n)
-                mc.arrive(("PFULL", b))
+                s[x] = ("P", n)
+                mc.arrive(("PFULL", x))
                 done += 1
             if at + 1 < len(todo):
                 load(todo[at + 1])
-            if final:
-                yield ("OFIN", x), at & 1
-            else:
-                yield ("ODONE", x), (done - 1) & 1
-            _expect(len(o[x]) and o[x][-1] == (it, mine[it][-1][1]), "O not final")
+            yield ("ODONE", x), (done - 1) & 1
             both = items[it][1] and items[it][0] > 1
             if both and x == 1:
                 mc.arrive("SPLIT")
@@ -347,9 +320,9 @@ def _one_items(rng):
     return [rng.choice((1, 1, 2, 3, 5)) for _ in range(rng.randint(1, 6))]
 
 
-@pytest.mark.parametrize("ns,nr,rot", [(2, 0, False), (2, 2, False), (4, 0, True), (4, 4, True)])
-def test_two_tiles_are_safe_under_any_interleaving(ns, nr, rot):
-    assert _outcomes(_two_tiles, _two_items, ns + nr, 400, ns=ns, nr=nr, rot=rot) == {"ok": 400}
+@pytest.mark.parametrize("ns,nr", [(2, 0), (4, 0), (2, 2), (4, 4)])
+def test_two_tiles_are_safe_under_any_interleaving(ns, nr):
+    assert _outcomes(_two_tiles, _two_items, ns + nr, 400, ns=ns, nr=nr) == {"ok": 400}
 
 
 @pytest.mark.parametrize("nr", [0, 2])
@@ -357,13 +330,9 @@ def test_one_tile_is_safe_under_any_interleaving(nr):
     assert _outcomes(_one_tile, _one_items, nr, 400, ns=2, nr=nr) == {"ok": 400}
 
 
-@pytest.mark.parametrize("left_out,rot", [("wait_split", False), ("s_after_pv", False),
-                                          ("in_order", False), ("wait_split", True),
-                                          ("s_after_pv", True), ("final", True), ("early_q", True),
-                                          ("own_full", True)])
-def test_two_tiles_fail_without(left_out, rot):
-    seen = _outcomes(_two_tiles, _two_items, 7, 400, ns=4 if rot else 2, nr=0, rot=rot,
-                     **{left_out: False})
+@pytest.mark.parametrize("left_out", ["wait_split", "s_after_pv", "in_order"])
+def test_two_tiles_fail_without(left_out):
+    seen = _outcomes(_two_tiles, _two_items, 7, 400, ns=2, nr=0, **{left_out: False})
     assert set(seen) != {"ok"}, seen
 
 
