@@ -321,7 +321,8 @@ fa_status fa_rotary_backward(const fa_rotary_rows* q, const fa_rotary_rows* k, i
  * the sequences: the rows q_start[s] .. q_start[s + 1] - 1 of the step's
  * [T][heads][d] tensors belong to sequence s, whose length INCLUDING them is
  * kv_len[s]; new token i sits at position kv_len - q_len + i.  Lengths, starts
- * and tables are read on the device when the kernels run.
+ * and tables are read on the device when the kernels run.  Sequences may share
+ * pages (a common beginning) that none of them appends to in the step.
  */
 #define FA_CACHE_BF16 0
 #define FA_CACHE_E4M3 1

@@ -135,7 +135,7 @@ def test_append_rejects(lib, kw):
 @pytest.mark.parametrize("kw", [
     dict(q=None), dict(o=None), dict(q=Q), dict(o=Q), dict(lse=F), dict(T=-1), dict(Hq=3),
     dict(Hq=0), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-    dict(scale=float("inf")), dict(causal=2), dict(qt=4), dict(qh=-64), dict(ot=0), dict(oh=0),
+    dict(scale=float("inf")), dict(scale=3e38), dict(causal=2), dict(qt=4), dict(qh=-64), dict(ot=0), dict(oh=0),
     dict(T=2 ** 30, Hq=4),
 ])
 def test_forward_rejects(lib, kw):

@@ -59,7 +59,7 @@ def test_ragged_chunks(d, e4m3, causal):
     run(Step(q, k, 6, 2, d, 32, e4m3, seed=d + causal, pad=1), causal)
 
 
-@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (7, 1), (5, 5), (10, 2), (40, 8), (48, 2)])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (7, 1), (5, 5), (10, 2), (40, 8), (48, 2), (130, 1), (300, 1)])
 def test_head_groups(Hq, Hkv):
     run(Step([1, 4, 30], [90, 260, 31], Hq, Hkv, 128, 16, seed=Hq))
 
@@ -85,6 +85,25 @@ def test_rows_without_keys(causal, q_lens):
     assert torch.all(o[:3] == 0) and torch.all(lse[:3] == -math.inf)
 
 
+def test_shared_pages():
+    """Two sequences with the same beginning, whose pages both read."""
+    step = Step([1, 40], [160, 200], 4, 2, 64, 16, seed=15)
+    shared = 9
+    step.table_cpu[1, :shared] = step.table_cpu[0, :shared]
+    step.table = step.table_cpu.cuda()
+    step.k64[1][:16 * shared] = step.k64[0][:16 * shared]
+    step.v64[1][:16 * shared] = step.v64[0][:16 * shared]
+    run(step)
+
+
+@pytest.mark.parametrize("past", [0, 1, 127, 128, 129, 1000])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_long_chunks(d, past):
+    """Items of every length in one sequence, and rows on both sides of a tile's end."""
+    for n in (127, 128, 129, 700):
+        run(Step([n], [n + past], 2, 1, d, 64, seed=n + past))
+
+
 @pytest.mark.parametrize("bound", [0, 1, 2, 1000])
 def test_wrong_max_q_len_costs_time_only(bound):
     run(Step([1, 20, 90], [50, 40, 300], 4, 1, 64, 16, seed=2), max_q_len=bound)
@@ -102,6 +121,12 @@ def test_many_sequences():
     q = [i % 3 != 1 and 1 or 0 for i in range(n)]
     k = [1 + (i * 37) % 90 if i % 11 == 0 else 1 for i in range(n)]
     run(Step(q, k, 2, 1, 64, 16, seed=6))
+    # ... and with chunks among them
+    for i in (0, 5, 500, 777, 1099):
+        q[i], k[i] = 30 + i % 7, 40 + i % 90
+    run(Step(q, k, 2, 1, 64, 16, seed=6))
+    q = [10 + i % 5 for i in range(40)]
+    run(Step(q, [n + 7 * i for i, n in enumerate(q)], 4, 1, 256, 16, True, seed=6))
 
 
 @pytest.mark.parametrize("k_scale", [30.0, 1e-3])
@@ -336,6 +361,19 @@ def test_append(d, rot, e4m3, interleaved, where):
     for now, was in ((step.k_pages, untouched_k), (step.v_pages, untouched_v)):
         a, b = (x.transpose(1, 2).contiguous().view(torch.uint8)[keep.cuda()] for x in (now, was))
         assert torch.equal(a, b)
+
+
+def test_append_turns_q_in_place():
+    import exact_attention_27_gb300 as fa
+    step = Step([5, 2], [5, 90], 4, 2, 64, 16, seed=3)
+    cache, batch = step.handles()
+    k = torch.randn(7, 2, 64, device="cuda").to(torch.bfloat16)
+    inv = (10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)).float()
+    rotary = fa.Rotary(inv.cuda())
+    want = fa.paged_append(cache, batch, k, k, rotary, q=step.q)
+    fa.fa_paged_append(cache, batch, k, k, rotary, None, step.q, step.q)
+    torch.cuda.synchronize()
+    assert torch.equal(step.q, want)
 
 
 def test_append_without_rotation_copies():
