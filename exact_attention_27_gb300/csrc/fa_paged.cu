@@ -663,7 +663,8 @@ int ctas_for(int sms, int rows, int d, bool e4m3) {
   return sms * (rows == 16 ? rows_occupancy(d, e4m3) : 1);
 }
 
-// Workspace: notes, (m, l), O; each part 256-byte aligned.
+// Workspace: notes, (m, l), O; each part on a 256-byte boundary (parts of O are
+// stored 32 bytes at a time), the first that the caller's 16-byte aligned memory has.
 struct PartLayout {
   size_t ml, o, total;
 };
@@ -672,7 +673,7 @@ PartLayout part_layout(int ctas, int rows, int d) {
   PartLayout l;
   l.ml = up(static_cast<size_t>(ctas) * sizeof(PagedNote));
   l.o = l.ml + up(static_cast<size_t>(ctas) * 2 * rows * sizeof(float2));
-  l.total = l.o + static_cast<size_t>(ctas) * 2 * rows * d * sizeof(float);
+  l.total = l.o + static_cast<size_t>(ctas) * 2 * rows * d * sizeof(float) + 240;
   return l;
 }
 
@@ -781,7 +782,8 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   p.min_units = rows == 16 ? 1 : 4;
   p.scale_log2 = s_eff * kPagedLog2e;
   p.v_scale = cache->v_descale;
-  char* ws = static_cast<char*>(workspace);
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) &
+                                     ~static_cast<uintptr_t>(255));
   p.notes = reinterpret_cast<PagedNote*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   p.part_o = reinterpret_cast<float*>(ws + lay.o);

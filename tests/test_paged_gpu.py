@@ -167,6 +167,23 @@ def test_strided_queries_and_outputs():
     step.check(out[:, 5:], lse, 0.1, True)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("at", [16, 48, 240])
+def test_workspace_on_any_16_bytes(d, at):
+    """The workspace starts on a 16-byte boundary and no larger one; nothing past its end is
+    written."""
+    import exact_attention_27_gb300 as fa
+    step = Step([1, 300], [5000, 400], 4, 2, d, 16, seed=16)
+    cache, batch = step.handles()
+    n = fa.paged_workspace(cache, batch, step.q).nbytes
+    room = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(step.q), torch.empty(step.T, 4, device="cuda")
+    fa.fa_forward_paged(cache, batch, step.q, o, lse, 0.1, True, room[at:at + n])
+    torch.cuda.synchronize()
+    step.check(o, lse, 0.1, True)
+    assert torch.all(room[:at] == 0xA5) and torch.all(room[at + n:] == 0xA5)
+
+
 def test_offsets_past_32_bits():
     """Pages whose elements lie past 2^31."""
     import exact_attention_27_gb300 as fa
