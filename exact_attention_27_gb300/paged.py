@@ -146,8 +146,6 @@ class PagedCache:
         kinds = {torch.bfloat16: (0, 2), torch.float8_e4m3fn: (1, 1)}
         if k_pages.dtype not in kinds or v_pages.dtype is not k_pages.dtype:
             raise ValueError("k_pages and v_pages must both be bf16 or both float8_e4m3fn")
-        if not k_pages.is_cuda or k_pages.get_device() != v_pages.get_device():
-            raise ValueError("k_pages and v_pages must be CUDA tensors of one device")
         dtype, size = kinds[k_pages.dtype]
         n, H, page, d = k_pages.shape
         if d not in (64, 96, 128, 256):
@@ -160,14 +158,15 @@ class PagedCache:
             if t.stride(3) != 1 or t.data_ptr() & 15:
                 raise ValueError("pages must be contiguous along d and start on 16 bytes")
         # the stride of a dimension of one element is free: use the dense one
-        ks, vs = ([t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
+        ks, vs = ([t.stride(i) if t.shape[i] > 1 else d * page * H for i in range(3)]
                   for t in (k_pages, v_pages))
         if ks != vs:
             raise ValueError("k_pages and v_pages must have the same strides")
-        ks = [s or d * page * H for s in ks]
         if any(s * size % 16 or s < d for s in ks):
             raise ValueError(f"page strides {tuple(ks)}: multiples of 16 bytes, at least d, "
                              "are needed")
+        if not k_pages.is_cuda or k_pages.get_device() != v_pages.get_device():
+            raise ValueError("k_pages and v_pages must be CUDA tensors of one device")
         if not (math.isfinite(k_descale) and k_descale > 0 and math.isfinite(v_descale) and
                 v_descale > 0) or (dtype == 0 and (k_descale, v_descale) != (1.0, 1.0)):
             raise ValueError("descales must be finite and > 0, and 1 for bf16 pages")

@@ -172,5 +172,17 @@ def test_handles_check_their_tensors():
         fa.PagedBatch(i, torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("broadcast", [0, 1, 2])
+def test_broadcast_pages_are_refused(dtype, broadcast):
+    """Pages, heads or rows that share their memory: a view with a stride of 0."""
+    shape = [4, 2, 16, 64]
+    one = list(shape)
+    one[broadcast] = 1
+    x = torch.zeros(one, dtype=torch.float32).to(dtype).expand(shape)
+    with pytest.raises(ValueError, match="strides"):
+        fa.PagedCache(x, x)
+
+
 def test_status_of_a_bad_page(lib):
     assert "page" in fa.fa_status_string(fa.FA_ERR_BAD_PAGE)
