@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
               pml[g + 8 * i] = make_float2(M[i], L[i]);
             else if (p.lse)
               p.lse[token * p.Hq + head[i]] =
-                  L[i] > 0.0f ? (M[i] + log2f(L[i])) * kPagedLn2 : -INFINITY;
+                  L[i] == 0.0f ? -INFINITY : (M[i] + log2f(L[i])) * kPagedLn2;
           }
         }
         if (lane == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     *reinterpret_cast<uint2*>(p.o + token * p.o_token + head * p.o_head + 4 * lane) =
         make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     if (lane == 0 && p.lse)
-      p.lse[token * p.Hq + head] = l > 0.0f ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
+      p.lse[token * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kPagedLn2;
   };
   if (parts <= kJoinFew) {
     if (grp < GROUPS)

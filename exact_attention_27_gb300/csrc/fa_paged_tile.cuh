@@ -306,7 +306,7 @@ __device__ __forceinline__ void paged_store_row(const PagedParams& p, const Page
     if (!whole)
       p.part_ml[part_row] = make_float2(m, l);
     else if (p.lse)
-      p.lse[x.token * p.Hq + x.head] = l > 0.0f ? (m + log2f(l)) * kPagedLn2 : -INFINITY;
+      p.lse[x.token * p.Hq + x.head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kPagedLn2;
   }
 }
 

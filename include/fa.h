@@ -385,7 +385,8 @@ fa_status fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* bat
  *          key/value head h / (H_q / H_kv)
  *   lse    [T][H_q] fp32 contiguous, as fa_forward's; NULL: not wanted
  *   causal 1: new token i sees positions <= kv_len - q_len + i; 0: all kv_len.
- *          A token that sees none gets o = 0 and lse = -infinity.
+ *          A token that sees none gets o = 0 and lse = -infinity; a NaN in a row
+ *          of q makes that row's o and lse NaN, and no other's.
  *   workspace  device memory of at least fa_forward_paged_workspace_bytes for
  *          the same H_q, H_kv, d, T and max_q_len, 16-byte aligned; its
  *          contents do not matter before or after.  Calls whose work can

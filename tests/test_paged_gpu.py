@@ -85,6 +85,25 @@ def test_rows_without_keys(causal, q_lens):
     assert torch.all(o[:3] == 0) and torch.all(lse[:3] == -math.inf)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_nan_in_a_query_stays_in_its_row(d, e4m3):
+    """o and lse of the row are NaN (not the -infinity of a row without keys), in items that one
+    CTA finishes and in items that many join; every other row keeps its bits."""
+    for q, k in (([1, 2, 1], [70, 20, 9000]), ([1, 300, 40], [70, 400, 9000])):
+        step = Step(q, k, 4, 2, d, 16, e4m3, seed=18)
+        o, lse = run(step)
+        rows = [(0, 1), (2, 3), (step.T - 1, 0)]
+        for t, h in rows:
+            step.q[t, h, 5] = float("nan")
+        bad_o, bad_lse, _ = attend(step)
+        hit = torch.zeros(step.T, 4, dtype=torch.bool, device="cuda")
+        for t, h in rows:
+            hit[t, h] = True
+        assert torch.isnan(bad_o[hit]).all() and torch.isnan(bad_lse[hit]).all()
+        assert torch.equal(bad_o[~hit], o[~hit]) and torch.equal(bad_lse[~hit], lse[~hit])
+
+
 def test_shared_pages():
     """Two sequences with the same beginning, whose pages both read."""
     step = Step([1, 40], [160, 200], 4, 2, 64, 16, seed=15)
