@@ -375,7 +375,8 @@ fa_status validate_cache(const fa_paged_cache* c, const fa_paged_batch* b, int T
     return FA_ERR_INVALID_ARGUMENT;
   if (c->dtype != FA_CACHE_BF16 && c->dtype != FA_CACHE_E4M3) return FA_ERR_INVALID_ARGUMENT;
   for (float f : {c->k_descale, c->v_descale})
-    if (!std::isfinite(f) || !(f > 0.0f) || (c->dtype == FA_CACHE_BF16 && f != 1.0f))
+    if (!std::isfinite(f) || !(f > 0.0f) || !std::isfinite(1.0f / f) ||
+        (c->dtype == FA_CACHE_BF16 && f != 1.0f))
       return FA_ERR_INVALID_ARGUMENT;
   const int elem = c->dtype == FA_CACHE_BF16 ? 2 : 1;
   // Rows, heads and pages lie apart and start on 16-byte boundaries; a tensor

@@ -338,8 +338,8 @@ typedef struct {
   int H_kv;
   int d;                  /* 64, 96, 128 or 256 */
   int dtype;              /* FA_CACHE_BF16 or FA_CACHE_E4M3 */
-  float k_descale;        /* a stored e4m3 key stands for k * k_descale; finite, > 0; */
-  float v_descale;        /* 1 for bf16 */
+  float k_descale;        /* a stored e4m3 key stands for k * k_descale; finite, > 0, with a */
+  float v_descale;        /* finite 1 / descale; 1 for bf16 */
 } fa_paged_cache;
 
 typedef struct {

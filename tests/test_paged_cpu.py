@@ -122,6 +122,12 @@ def test_bad_batches_are_rejected(lib, call, kw):
     assert call(lib, b=batch(**kw)) == fa.FA_ERR_INVALID_ARGUMENT
 
 
+@pytest.mark.parametrize("call", [append, forward])
+@pytest.mark.parametrize("kw", [dict(k_descale=1e-39), dict(v_descale=2.0 ** -149)])
+def test_descales_without_a_reciprocal_are_rejected(lib, call, kw):
+    assert call(lib, c=cache(dtype=1, **kw)) == fa.FA_ERR_INVALID_ARGUMENT
+
+
 @pytest.mark.parametrize("kw", [
     dict(k=None), dict(v=None), dict(k=Q), dict(v=Q), dict(T=-1), dict(kt=60), dict(vh=-64),
     dict(q=None), dict(o=None), dict(q=Q), dict(o=Q), dict(Hq=0), dict(qt=4), dict(ot=0),
