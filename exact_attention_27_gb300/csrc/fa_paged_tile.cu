@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(384, 1)
         bool ok = issue_s();
         if (ok && more) ok = issue_s();
         int n = 0;
-          do {
+        do {
           for (int t = seg.t0; ok && t < seg.t1; ++t, ++n) {
             const int st = n % C::NS, bf = n % C::NB;
             ok = (E4M3 || wait(C::B_VFULL + st, (n / C::NS) & 1)) &&

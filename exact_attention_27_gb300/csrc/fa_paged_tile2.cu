@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
         // first of the tile, bit 2 the key tile's last use, key tile above.
         uint32_t job0 = 0, job1 = 0;
         int waiting = 0, v_tile = -1;
-          bool have = true, sp = split(seg);
+        bool have = true, sp = split(seg);
         int t = seg.t0, x = 0, n = 0;
         bool k_ready = false;
         auto issue_s = [&]() -> bool {
