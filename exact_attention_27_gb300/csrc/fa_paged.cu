@@ -777,9 +777,12 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   p.n_pages = cache->n_pages;
   p.causal = causal;
   // A CTA starts for one tile of 64 keys (two sequences of a thousand keys: 10.8 us,
-  // 13 to 19 us with 2 to 8 at least), but for four of the tcgen05 kernels, whose
-  // parts are larger (128 rows of 4096 keys: 14.5 us, 21.8 us with one).
-  p.min_units = rows == 16 ? 1 : 4;
+  // 13 to 19 us with 2 to 8 at least), but for more of the tcgen05 kernels, whose
+  // parts are larger: four tiles at d = 256, and otherwise six units, two or three
+  // tiles (128 rows of 4096 keys, d = 128: 15.0 us, 15.7 us with eight; with one
+  // tile it was 21.8 against 14.5 us with four).  Ranges then hold at least three
+  // units, so each CTA between an item's first and last has a tile of it.
+  p.min_units = rows == 16 ? 1 : d == 256 ? 4 : 6;
   p.scale_log2 = s_eff * kPagedLog2e;
   p.v_scale = cache->v_descale;
   char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) &

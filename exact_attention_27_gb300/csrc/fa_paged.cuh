@@ -1,7 +1,7 @@
 // Shared by the kernels of fa_forward_paged: the step's geometry, the division
 // of its key tiles among the CTAs, and the partial results of what is divided.
 //
-// Work is counted in units of about one key tile of one item; an item is a tile of
+// Work is counted in units, one or a few a key tile of an item; an item is a tile of
 // ROWS query rows of one (sequence, key/value head), its rows being the
 // head's tokens x the G query heads that share it (row r: token r / G, head
 // r % G), so that grouped heads read K and V once.  Items stand in order of
@@ -110,10 +110,11 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int s) {
 }
 
 // Items of ROWS rows and key tiles of TK keys.  An item counts for its key
-// tiles and OVER units more, about what starting and ending one costs.
-template <int ROWS_, int TK_, int OVER_>
+// tiles and OVER more, about what starting and ending one costs, at FULL units each,
+// or HALF where its rows fill at most half of ROWS.
+template <int ROWS_, int TK_, int OVER_, int FULL_ = 1, int HALF_ = 1>
 struct PagedWalk {
-  static constexpr int ROWS = ROWS_, TK = TK_, OVER = OVER_;
+  static constexpr int ROWS = ROWS_, TK = TK_, OVER = OVER_, FULL = FULL_, HALF = HALF_;
   int s, h, rt, n_rt;
   PagedSeq g;
 
@@ -132,14 +133,23 @@ struct PagedWalk {
   static __device__ __forceinline__ int tiles(const PagedParams& p, const PagedSeq& g, int rt) {
     return max((keys(p, g, rt) + TK - 1) / TK, 1);
   }
+  // Whether row tile rt has at most half an item's rows.
+  static __device__ __forceinline__ bool half(const PagedParams& p, const PagedSeq& g, int rt) {
+    return g.qlen * p.G - rt * ROWS <= ROWS / 2;
+  }
+  // Units of one of its key tiles.
+  static __device__ __forceinline__ int weight(const PagedParams& p, const PagedSeq& g, int rt) {
+    return FULL == HALF ? FULL : half(p, g, rt) ? HALF : FULL;
+  }
   static __device__ __forceinline__ int units(const PagedParams& p, const PagedSeq& g, int rt) {
-    return tiles(p, g, rt) + OVER;
+    return (tiles(p, g, rt) + OVER) * weight(p, g, rt);
   }
   // Units of one head of the sequence of each lane; the whole warp calls this.
   static __device__ __forceinline__ long long head_units(const PagedParams& p, const PagedSeq& g) {
     constexpr int SHORT = 4;
     const int n = row_tiles(p, g);
-    if (!p.causal) return n == 0 ? 0 : static_cast<long long>(n) * units(p, g, 0);
+    if (!p.causal)  // (all but the last are alike)
+      return n == 0 ? 0 : static_cast<long long>(n - 1) * units(p, g, 0) + units(p, g, n - 1);
     long long u = 0;
     if (n <= SHORT) {
       for (int rt = 0; rt < n; ++rt) u += units(p, g, rt);
@@ -323,12 +333,23 @@ struct PagedSegments {
   Walk w;
   long long unit, end;  // where the item's part of the range begins; the range's end
   int t0, t1, tiles, keys, used;
+  __device__ __forceinline__ int weight(const PagedParams& p) const {
+    return Walk::weight(p, w.g, w.rt);
+  }
   __device__ __forceinline__ void load(const PagedParams& p, int at) {
     tiles = Walk::tiles(p, w.g, w.rt);
     keys = Walk::keys(p, w.g, w.rt);
-    used = static_cast<int>(min(static_cast<long long>(tiles + Walk::OVER - at), end - unit));
-    t0 = min(at, tiles);
-    t1 = min(at + used, tiles);
+    const int wt = weight(p);
+    used = static_cast<int>(
+        min(static_cast<long long>((tiles + Walk::OVER) * wt - at), end - unit));
+    // A tile belongs to the range that holds its first unit.
+    auto tile = [&](int u) {
+      if constexpr (Walk::FULL == 1) return u;
+      return wt == Walk::HALF ? (u + Walk::HALF - 1) / Walk::HALF
+                              : (u + Walk::FULL - 1) / Walk::FULL;
+    };
+    t0 = min(tile(at), tiles);
+    t1 = min(tile(at + used), tiles);
   }
   // False if the range holds no key tile.  The whole warp calls this.
   __device__ __forceinline__ bool start(const PagedParams& p, const PagedRange& r) {
@@ -354,7 +375,7 @@ __device__ __forceinline__ PagedNote paged_note(const PagedParams& p, const Page
                                                 const PagedSegments<Walk>& seg) {
   const Walk& w = seg.w;
   PagedNote n{};
-  n.last = r.owner(seg.unit + seg.tiles - 1);
+  n.last = r.owner(seg.unit + static_cast<long long>(seg.tiles - 1) * seg.weight(p));
   n.q0 = w.g.q0;
   n.rows = w.g.qlen * p.G;
   n.tile0 = w.rt * Walk::ROWS;

@@ -104,7 +104,12 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
                           const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
   using C = Tile2Cfg<D, E4M3>;
   constexpr int BN = C::BN;
-  using Walk = PagedWalk<C::BM, BN, 2>;
+  // A key tile of an item of at most 128 rows (one product pair of half the size)
+  // takes two thirds of another's time: half to nine tenths, by how much of it is
+  // copies and conversion.  24 sequences, 3 chunks among single tokens, 16 / 4
+  // heads, with 1:1, 3:2, 2:1: d = 64 46.4 / 41.0 / 40.0 us, d = 128 57.9 / 53.2 /
+  // 57.6, e4m3 70.1 / 63.5 / 66.0; five e4m3 chunks 166 / 166 to 172 / 184.
+  using Walk = PagedWalk<C::BM, BN, 2, 3, 2>;
   using Seg = PagedSegments<Walk>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
   const uint32_t sR = sbase + C::OFF_RAW;
 
   // Whether the item's rows fill one tile only, and its key tiles go in turn to A and B.
-  auto split = [&](const Seg& s) -> bool { return s.w.g.qlen * p.G - s.w.rt * C::BM <= 128; };
+  auto split = [&](const Seg& s) -> bool { return Walk::half(p, s.w.g, s.w.rt); };
 
   if (warp >= 8) {
     reg_decrease<56>();
