@@ -554,13 +554,16 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
 // Joins the parts of the items that several CTAs share: blocks (c, y) those of
 // the item that starts in CTA c and is not finished there.  A group of D / 4
 // threads runs over parts with a running maximum, four loads in flight.  Few
-// parts: each group has a row of its own.  Many (a long history and few rows):
-// the block's groups share a row's parts and join through shared memory.  Either
-// way the order is that of the CTAs.
+// parts, or rows for more groups than the item's blocks have: each group has a row
+// of its own.  Many parts and few rows (a long history): the block's groups share a
+// row's parts and join through shared memory.  Either way the order is that of the
+// CTAs.  (512 rows of 30,000 keys, d = 64: 27.2 us, 46.4 us when items of all
+// heights of many parts share rows.)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinFew = 12;
+constexpr int kJoinRowsBlocks = 4, kJoinTileBlocks = 16;
 
-template <int D>
+template <int D, bool TILE>
 __global__ void __launch_bounds__(kJoinThreads)
     fa_paged_join_kernel(const PagedParams p, int tile_rows) {
   constexpr int LANES = D / 4;
@@ -622,7 +625,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (lane == 0 && p.lse)
       p.lse[token * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kPagedLn2;
   };
-  if (parts <= kJoinFew) {
+  if (parts <= kJoinFew || (TILE && rows > 2 * kJoinTileBlocks)) {
     if (grp < GROUPS)
       for (int row = blockIdx.y * GROUPS + grp; row < rows; row += gridDim.y * GROUPS) {
         run(row, 0, 1);
@@ -699,13 +702,14 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Page
   return cudaErrorInvalidValue;
 }
 
+template <bool TILE>
 cudaError_t launch_join(const PagedParams& p, int rows, int d, int ctas, cudaStream_t stream) {
-  auto kern = d == 64    ? fa_paged_join_kernel<64>
-              : d == 96  ? fa_paged_join_kernel<96>
-              : d == 128 ? fa_paged_join_kernel<128>
-                         : fa_paged_join_kernel<256>;
-  return launch_dependent(kern, dim3(ctas, rows == 16 ? 4 : 16), dim3(kJoinThreads), 0, stream, p,
-                          rows);
+  auto kern = d == 64    ? fa_paged_join_kernel<64, TILE>
+              : d == 96  ? fa_paged_join_kernel<96, TILE>
+              : d == 128 ? fa_paged_join_kernel<128, TILE>
+                         : fa_paged_join_kernel<256, TILE>;
+  return launch_dependent(kern, dim3(ctas, TILE ? kJoinTileBlocks : kJoinRowsBlocks),
+                          dim3(kJoinThreads), 0, stream, p, rows);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -778,11 +782,12 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
   p.causal = causal;
   // A CTA starts for one tile of 64 keys (two sequences of a thousand keys: 10.8 us,
   // 13 to 19 us with 2 to 8 at least), but for more of the tcgen05 kernels, whose
-  // parts are larger: four tiles at d = 256, and otherwise six units, two or three
-  // tiles (128 rows of 4096 keys, d = 128: 15.0 us, 15.7 us with eight; with one
-  // tile it was 21.8 against 14.5 us with four).  Ranges then hold at least three
-  // units, so each CTA between an item's first and last has a tile of it.
-  p.min_units = rows == 16 ? 1 : d == 256 ? 4 : 6;
+  // parts are larger: two tiles at d = 256 (128 tokens of 32 heads without a
+  // history: 13.0 us, 15.0 with three, 17.3 with four), and otherwise six units, two
+  // or three tiles (128 rows of 4096 keys, d = 128: 15.0 us, 15.7 us with eight).
+  // Ranges then hold at least three units there, so each CTA between an item's first
+  // and last has a tile of it.
+  p.min_units = rows == 16 ? 1 : d == 256 ? 2 : 6;
   p.scale_log2 = s_eff * kPagedLog2e;
   p.v_scale = cache->v_descale;
   char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) &
@@ -800,7 +805,9 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
                                     : launch_paged_tile2(tk, tv, p, d, e4m3, ctas, stream)
                   : e4m3 ? launch_rows<true>(tk, tv, p, d, ctas, stream)
                          : launch_rows<false>(tk, tv, p, d, ctas, stream);
-  if (e == cudaSuccess) e = launch_join(p, rows, d, ctas, stream);
+  if (e == cudaSuccess)
+    e = tile ? launch_join<true>(p, rows, d, ctas, stream)
+             : launch_join<false>(p, rows, d, ctas, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
