@@ -17,8 +17,11 @@
 // heads: a block takes TOK positions, one thread makes one sine and cosine, and
 // a thread then keeps those of its 8 pairs in registers and goes through the
 // heads, kBatch at a time, the first of them loaded before the angles are made.
-// 16384 positions of 32 + 8 heads at d = 128: 55 us, 6.1 TB/s.  (Four heads at a
-// time at this occupancy spill: 76 us.)
+// 16384 positions of 32 + 8 heads at d = 128: 55.8 us, 6.0 TB/s.  (Four heads at a
+// time at this occupancy spill: 76 us; at three blocks an SM 54.2 us, but 8192
+// positions of 16 heads, d = 64, take 9.7 us instead of 8.6 and the append below
+// 39.3.)  Appending 8527 tokens of 32 + 8 + 8 heads, d = 128, to e4m3 pages: 37.5 us,
+// 5.1 TB/s (40.2 us with a thread's k rows before its v rows).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -146,18 +149,35 @@ __global__ void __launch_bounds__(kThreads, 4) fa_turn_kernel(const __grid_const
 
   if (TO != kTurnOnly) {
     // Warp w finds token w (TOK / 8 rounds): its sequence is the number of
-    // starts q_start[1..S] at or below it, counted by all lanes.
+    // starts q_start[1..S] at or below it, counted by all lanes.  Up to 32
+    // sequences, each lane brings its sequence's end and length with that.
     const int lane = tid & 31;
     for (int w = tid >> 5; w < TOK; w += kThreads / 32) {
       const long long tw = t0 + w;
-      int below = 0;
-      for (int i = lane; i < p.S; i += 32) below += p.q_start[i + 1] <= tw;
-      const int s = __reduce_add_sync(0xffffffffu, below);
+      int s, from, to, len;  // the sequence, its first token, its end, its length
+      if (p.S <= 32) {
+        const int end = lane < p.S ? p.q_start[lane + 1] : 0;
+        const int kv = lane < p.S ? p.kv_len[lane] : 0;
+        const int start = p.q_start[0];
+        s = __popc(__ballot_sync(0xffffffffu, lane < p.S && end <= tw));
+        to = __shfl_sync(0xffffffffu, end, s & 31);
+        len = __shfl_sync(0xffffffffu, kv, s & 31);
+        from = __shfl_sync(0xffffffffu, end, (s - 1) & 31);
+        if (s == 0) from = start;
+      } else {
+        int below = 0;
+        for (int i = lane; i < p.S; i += 32) below += p.q_start[i + 1] <= tw;
+        s = __reduce_add_sync(0xffffffffu, below);
+        const int x = min(s, p.S - 1);
+        from = p.q_start[x];
+        to = p.q_start[x + 1];
+        len = p.kv_len[x];
+      }
       if (lane == 0) {
         int pos = INT_MIN;
         long long where = -1;
-        if (tw < p.tokens && s < p.S && tw >= p.q_start[s]) {
-          pos = static_cast<int>(p.kv_len[s] - (p.q_start[s + 1] - tw));
+        if (tw < p.tokens && s < p.S && tw >= from) {
+          pos = static_cast<int>(len - (to - tw));
           const int slot = pos < 0 ? 0 : pos / p.page_size;
           if (pos >= 0 && slot < p.max_pages) {
             const int page = p.table[s * p.table_stride + slot];
@@ -218,38 +238,39 @@ __global__ void __launch_bounds__(kThreads, 4) fa_turn_kernel(const __grid_const
       }
     }
   };
-  // The heads hg, hg + HG, ... of one tensor, the first kBatch in lo and hi; to
-  // bf16 rows at dst, or to e4m3 rows times `scale`.
-  auto rows = [&](const __nv_bfloat16* src, long long step, int heads, auto* dst,
-                  long long dst_step, bool turns, float scale) {
+  // A loaded row to a bf16 row at dst, or to an e4m3 row times `scale`.
+  auto put = [&](const uint4& lo, const uint4& hi, auto* dst, bool turns, float scale) {
+    if (sizeof(*dst) == 2 && !turns) {
+      *reinterpret_cast<uint4*>(dst) = lo;
+      *reinterpret_cast<uint4*>(dst + gap) = hi;
+      return;
+    }
+    float x[8], y[8];
+    unpack8(lo, x);
+    unpack8(hi, y);
+    if (turns) turn(x, y);
+    if constexpr (sizeof(*dst) == 2) {
+      *reinterpret_cast<uint4*>(dst) = pack8(x);
+      *reinterpret_cast<uint4*>(dst + gap) = pack8(y);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] *= scale;
+        y[e] *= scale;
+      }
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]));
+      *reinterpret_cast<uint2*>(dst + gap) =
+          make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
+    }
+  };
+  // The heads hg, hg + HG, ... of one tensor, the first kBatch in lo and hi.
+  auto rows = [&](const __nv_bfloat16* src, long long step, int heads, __nv_bfloat16* dst,
+                  long long dst_step) {
     for (int left = heads - hg; left > 0;) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (i * HG >= left) break;
-        float x[8], y[8];
-        if (sizeof(*dst) == 2 && !turns) {
-          *reinterpret_cast<uint4*>(dst + i * dst_step) = lo[i];
-          *reinterpret_cast<uint4*>(dst + i * dst_step + gap) = hi[i];
-          continue;
-        }
-        unpack8(lo[i], x);
-        unpack8(hi[i], y);
-        if (turns) turn(x, y);
-        if constexpr (sizeof(*dst) == 2) {
-          *reinterpret_cast<uint4*>(dst + i * dst_step) = pack8(x);
-          *reinterpret_cast<uint4*>(dst + i * dst_step + gap) = pack8(y);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] *= scale;
-            y[e] *= scale;
-          }
-          *reinterpret_cast<uint2*>(dst + i * dst_step) =
-              make_uint2(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]));
-          *reinterpret_cast<uint2*>(dst + i * dst_step + gap) =
-              make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
-        }
-      }
+      for (int i = 0; i < kBatch; ++i)
+        if (i * HG < left) put(lo[i], hi[i], dst + i * dst_step, turned, 1.0f);
       src += kBatch * step;
       dst += kBatch * dst_step;
       left -= kBatch * HG;
@@ -257,21 +278,30 @@ __global__ void __launch_bounds__(kThreads, 4) fa_turn_kernel(const __grid_const
     }
   };
   rows(q_in, q_step, p.q.heads,
-       p.q.out + (b * p.q.ob + n * p.q.op + hg * p.q.oh + first), p.q.oh * HG, turned, 1.0f);
-  load(k_in, k_step, p.k.heads - hg);
+       p.q.out + (b * p.q.ob + n * p.q.op + hg * p.q.oh + first), p.q.oh * HG);
   if constexpr (TO == kTurnOnly) {
+    load(k_in, k_step, p.k.heads - hg);
     rows(k_in, k_step, p.k.heads,
-         p.k.out + (b * p.k.ob + n * p.k.op + hg * p.k.oh + first), p.k.oh * HG, turned, 1.0f);
+         p.k.out + (b * p.k.ob + n * p.k.op + hg * p.k.oh + first), p.k.oh * HG);
   } else {
     if (place[tt] < 0) return;
     using Elem = std::conditional_t<TO == kToBf16, __nv_bfloat16, uint8_t>;
     const long long off = place[tt] + hg * p.head_stride + first;
     const __nv_bfloat16* v_in = p.v.in + (n * p.v.ip + hg * p.v.ih + first);
-    rows(k_in, k_step, p.k.heads, static_cast<Elem*>(p.k_pages) + off, p.head_stride * HG, turned,
-         p.k_scale);
-    load(v_in, p.v.ih * HG, p.v.heads - hg);
-    rows(v_in, p.v.ih * HG, p.v.heads, static_cast<Elem*>(p.v_pages) + off, p.head_stride * HG,
-         false, p.v_scale);
+    Elem* k_out = static_cast<Elem*>(p.k_pages) + off;
+    Elem* v_out = static_cast<Elem*>(p.v_pages) + off;
+    for (int h = hg; h < p.k.heads; h += HG) {  // a head's k and v together
+      const uint4 k0 = *reinterpret_cast<const uint4*>(k_in);
+      const uint4 k1 = *reinterpret_cast<const uint4*>(k_in + gap);
+      const uint4 v0 = *reinterpret_cast<const uint4*>(v_in);
+      const uint4 v1 = *reinterpret_cast<const uint4*>(v_in + gap);
+      put(k0, k1, k_out, turned, p.k_scale);
+      put(v0, v1, v_out, false, p.v_scale);
+      k_in += k_step;
+      v_in += p.v.ih * HG;
+      k_out += p.head_stride * HG;
+      v_out += p.head_stride * HG;
+    }
   }
 }
 

@@ -399,6 +399,24 @@ def test_append(d, rot, e4m3, interleaved, where):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("S", [1, 2, 31, 32, 33, 64, 300])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_append_finds_every_sequence(S, pad):
+    """Around the 32 sequences that a warp holds at once, some without tokens; more key heads
+    than a block goes through at a time."""
+    import exact_attention_27_gb300 as fa
+    q = [(5 * i + 2) % 4 for i in range(S)]
+    step = Step(q, [n + (7 * i) % 50 for i, n in enumerate(q)], 24, 24, 64, 16, seed=S, pad=pad)
+    cache, batch = step.handles()
+    k, v = (torch.randn(step.T, 24, 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    fa.fa_paged_append(cache, batch, k, v)
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_error() == 0
+    none = torch.zeros(step.T, 24, 64)
+    check_stored(step.k_pages, step, k.cpu().double(), 1.0, none)
+    check_stored(step.v_pages, step, v.cpu().double(), 1.0, none)
+
+
 def test_append_turns_q_in_place():
     import exact_attention_27_gb300 as fa
     step = Step([5, 2], [5, 90], 4, 2, 64, 16, seed=3)
