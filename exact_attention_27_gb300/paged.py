@@ -12,23 +12,28 @@ rotary_backward, paged_append and paged_attention allocate what they return.
 
 import ctypes
 import math
+import struct
 
 from . import _lib
 from ._lib import FaError, library
 
 _byref = ctypes.byref
+# An fa_rotary_rows as bytes, which a call takes for a pointer (a third of the time of filling a
+# ctypes structure).
+_rows_bytes = struct.Struct("PPqqqqqqi4x").pack
 
 # torch is imported on first use, by the first handle; what every call asks for is then at hand
 # (a server's step makes two calls a layer, and each microsecond of host time counts there).
-_torch = _BF16 = _F32 = _I32 = None
+_torch = _BF16 = _F32 = _I32 = _contiguous = None
 _device = _raw_stream = None
 
 
 def _load_torch():
-    global _torch, _BF16, _F32, _I32, _device, _raw_stream
+    global _torch, _BF16, _F32, _I32, _contiguous, _device, _raw_stream
     if _torch is None:
         import torch
         _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+        _contiguous = torch.contiguous_format
         _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda _: torch.cuda.current_stream().cuda_stream)
@@ -218,8 +223,7 @@ def _rotary_rows(x, out, device, name):
         b = _strides(name + "_out", out, 4, device)
         if any(n > 1 and s == 0 for n, s in zip(shape, b)):
             raise ValueError(f"{name}_out is a broadcast view")
-    return _lib.RotaryRows(x.data_ptr(), out.data_ptr(), a[0], a[1], a[2], b[0], b[1], b[2],
-                           shape[1])
+    return _rows_bytes(x.data_ptr(), out.data_ptr(), a[0], a[1], a[2], b[0], b[1], b[2], shape[1])
 
 
 def _launch_turn(fn, rows_q, rows_k, shape, k, positions, rotary, stream):
@@ -229,7 +233,6 @@ def _launch_turn(fn, rows_q, rows_k, shape, k, positions, rotary, stream):
         Bk, _, Nk, dk = k.shape
         if Bk != B or Nk != N or dk != d:
             raise ValueError("k must be [B, H_kv, N, d] with q's B, N and d")
-        rows_k = _byref(rows_k)
     if device != _device():
         _same_device(device)
     if positions.dim() == 2:
@@ -241,7 +244,7 @@ def _launch_turn(fn, rows_q, rows_k, shape, k, positions, rotary, stream):
     if positions.shape != (rotary.axes, B, N):
         raise ValueError(f"positions have shape {tuple(positions.shape)}, expected "
                          f"{(rotary.axes, B, N)}")
-    status = getattr(library(), fn)(_byref(rows_q), rows_k, B, N, d, positions.data_ptr(), s[0],
+    status = getattr(library(), fn)(rows_q, rows_k, B, N, d, positions.data_ptr(), s[0],
                                     s[1], rotary._ref, _stream(stream, device))
     if status:
         raise FaError(status, fn)
@@ -285,12 +288,10 @@ def _new_rows(x, device, name):
     if x.dtype is not _BF16 or x.get_device() != device or len(a) != 4 or a[3] != 1 or \
             (a[0] | a[1] | a[2]) & 7:
         a = _strides(name, x, 4, device)
-    # (empty_like is the quicker call)
-    out = _torch.empty_like(x) if x.is_contiguous() else \
-        _torch.empty(shape, dtype=_BF16, device=x.device)
+    # (quicker than empty with a type and a device)
+    out = _torch.empty_like(x, memory_format=_contiguous)
     _, H, N, d = shape
-    return out, _lib.RotaryRows(x.data_ptr(), out.data_ptr(), a[0], a[1], a[2], H * N * d, N * d, d,
-                                H)
+    return out, _rows_bytes(x.data_ptr(), out.data_ptr(), a[0], a[1], a[2], H * N * d, N * d, d, H)
 
 
 def _new_turn(fn, q, k, positions, rotary, stream):

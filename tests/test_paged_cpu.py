@@ -190,5 +190,11 @@ def test_broadcast_pages_are_refused(dtype, broadcast):
         fa.PagedCache(x, x)
 
 
+def test_rows_as_bytes_are_the_struct():
+    from exact_attention_27_gb300 import paged
+    values = (1 << 40, 2 << 40, 3, 4, 5 << 33, 6, 7, 8, 9)
+    assert paged._rows_bytes(*values) == bytes(_lib.RotaryRows(*values))
+
+
 def test_status_of_a_bad_page(lib):
     assert "page" in fa.fa_status_string(fa.FA_ERR_BAD_PAGE)
