@@ -18,7 +18,7 @@
 // under a quarter of the rate of the warp-level instruction.  What counts is
 // bytes in flight: two CTAs an SM with about 96 KB of ring each.  64 sequences of
 // 100 to 8000 keys, 8 heads, d = 128: 172 us, 6.5 TB/s; one of 120,000 e4m3
-// keys: 48.5 us, 5.1 TB/s (each tile's conversions and products take as long as
+// keys: 49.0 us, 5.0 TB/s (each tile's conversions and products take as long as
 // its bytes there, and hide behind other warps' in part).
 //
 // bf16 cache: P is rounded to bf16 (2^-8 relative at most) for P V, as in
@@ -70,7 +70,7 @@ struct RowsCfg {
   // in shared memory.
   static constexpr bool QS = D == 256 || OCC == 3;
   static constexpr int QBYTES = QS ? ROWS * D * 2 : 0;
-  static constexpr int FIT = (BUDGET - MERGE - QBYTES - 3072) / STAGE;
+  static constexpr int FIT = (BUDGET - MERGE - QBYTES - 3 * 1024) / STAGE;
   static constexpr int NS = FIT > 8 ? 8 : FIT;
   static constexpr int OFF_MERGE = NS * STAGE;
   static constexpr int OFF_Q = OFF_MERGE + MERGE;               // [D / 16][32 lanes] fragments
@@ -658,7 +658,8 @@ int sm_count() {
 
 // Rows of an item, which says the kernel: sequences of at most 16 rows go to the
 // kernel above, anything longer to the tcgen05 kernels (64 sequences of 100 to
-// 8000 keys, 32 rows each, d = 128: 225 us there, 269 us 32 rows a time here).
+// 8000 keys, 32 rows each, d = 128: 213 us there, 269 us 32 rows a time here;
+// 348 us as two items of 16).
 int rows_for(long long most, int d) { return most <= 16 ? 16 : paged_tile_rows(d); }
 
 // CTAs of a launch with `rows` rows an item.

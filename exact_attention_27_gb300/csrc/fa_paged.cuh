@@ -6,7 +6,7 @@
 // head's tokens x the G query heads that share it (row r: token r / G, head
 // r % G), so that grouped heads read K and V once.  Items stand in order of
 // sequence, head and row tile, and CTA c of C takes the units
-// [c U / C, (c + 1) U / C): every CTA the same number of key tiles, however
+// [c U / C, (c + 1) U / C): every CTA about the same work, however
 // ragged the lengths, and a long sequence of few rows is spread over many.
 // Lengths live on the device, so every CTA works its own range out at its
 // start (one pass over q_start and kv_len by the whole block).
