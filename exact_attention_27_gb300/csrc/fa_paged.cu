@@ -9,8 +9,8 @@
 // and O in registers, so that they meet only at the end of an item:
 //     S = Q K^T;  m' = max(m, max S);  p = 2^(S - m');
 //     l = l 2^(m - m') + sum p;  O = O 2^(m - m') + p V.
-// m moves only when it has grown by more than 8 (log2), which bounds p by 2^8
-// and leaves O / l as it is.  At the end the four key groups join (O, m, l)
+// m moves only when the maximum has grown by more than 8 (log2), which bounds p by
+// 2^8 and leaves O / l as it is.  At the end the four key groups join (O, m, l)
 // through shared memory.
 //
 // Why mma.sync here: 16 rows fill an eighth of a tcgen05 tile, and at 7 TB/s an
@@ -23,10 +23,11 @@
 //
 // bf16 cache: P is rounded to bf16 (2^-8 relative at most) for P V, as in
 // fa_forward; l sums the unrounded fp32 values.  e4m3 cache: K and V convert to
-// fp16 exactly, P is rounded to fp16 (2^-11), and each row of Q is scaled by a power
-// of two to a largest element in [2^7, 2^8), so that its bf16 values fit fp16
-// (what falls below fp16's range is 2^-33 of the row's largest); the power is
-// taken out of the scale of the row's scores.
+// fp16 exactly, P is rounded to fp16 with m held 7 (log2) lower, so that p is at most
+// 2^15 (2^-11 of each p, and 2^-32 of the largest where that is more), and each row of
+// Q is scaled by a power of two to a largest element in [2^7, 2^8), so that its bf16
+// values fit fp16 (what falls below fp16's range is 2^-33 of the row's largest); the
+// power is taken out of the scale of the row's scores.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -44,7 +45,6 @@
 namespace fa {
 namespace {
 
-constexpr float kRescaleThreshold = 8.0f;
 constexpr int kTK = 64;  // keys per tile
 
 // CTAs an SM.  A CTA's four warps each wait for loads, conversions and products
@@ -366,8 +366,9 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
                              fmaxf(s[1][2 * i], s[1][2 * i + 1]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * cs[i];
+            if (E4M3) mx -= kPagedP16;
             alpha[i] = 1.0f;
-            if (mx > m[i] + kRescaleThreshold) {
+            if (mx > m[i] + kPagedRescale) {
               alpha[i] = ex2_approx(m[i] - mx);
               m[i] = mx;
               upd = true;

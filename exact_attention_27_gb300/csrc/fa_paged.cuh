@@ -58,6 +58,16 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 constexpr float kPagedLog2e = 1.4426950408889634f;
 constexpr float kPagedLn2 = 0.6931471805599453f;
 
+// P = 2^(S - m).  The reference m moves only when the maximum has grown by more
+// than kPagedRescale (log2) past what it was set for.  For fp16 P (e4m3 pages) it
+// lies kPagedP16 below that maximum, so that the largest p is 2^7 to 2^15 and uses
+// the range that fp16 (up to 65504) has above 1: fp16 ends at half steps of 2^-25,
+// 2^-32 of the largest p, instead of 2^-25 of it, where many small weights would be
+// lost from O and still count in l.  l, the parts and lse follow, as all are taken
+// relative to m.  bf16 P has fp32's range and needs no such shift.
+constexpr float kPagedRescale = 8.0f;
+constexpr float kPagedP16 = 7.0f;
+
 struct PagedNote {
   int last;   // last CTA with a part of the item that starts here; -1: none
   int q0;     // first token of the sequence

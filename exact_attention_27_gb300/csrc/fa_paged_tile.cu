@@ -30,8 +30,8 @@
 // item by its first product, which waits for a P that the softmax makes after
 // the epilogue of the item before.
 //
-// e4m3 pages: as in fa_paged.cu, K and V as fp16 (exact), P as fp16, Q as fp16
-// with a power of two taken out of each row.
+// e4m3 pages: as in fa_paged.cu, K and V as fp16 (exact), P as fp16 up to 2^15, Q as
+// fp16 with a power of two taken out of each row.
 //
 // Every wait is bounded (about a second); on expiry the kernel sets an error
 // bit, every role skips its remaining work and the CTA exits.

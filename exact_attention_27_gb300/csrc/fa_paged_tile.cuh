@@ -12,8 +12,6 @@
 
 namespace fa {
 
-constexpr float kPagedRescale = 8.0f;  // log2 growth of the maximum that moves it
-
 // Instruction descriptor for kind::f16 with fp16 A and B (format code 0) and
 // an fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
@@ -172,9 +170,9 @@ __device__ __forceinline__ void paged_zero_rows(uint32_t v, int first, int tid) 
 }
 
 // The scores of a row's key tile at TMEM address `s` to P over them, with the
-// running maximum m and sum l (base 2, scores times c).  `see`: the last key of
-// the tile that the row sees, if `mask`.  Returns the factor that O and the old
-// l are due (1 while the maximum has not grown by more than kPagedRescale).
+// running reference m and sum l (base 2, scores times c).  `see`: the last key of
+// the tile that the row sees, if `mask`.  m is the reference that P is relative to
+// (fa_paged.cuh); returns the factor that O and the old l are due (1 while it stays).
 template <int BN, bool F16>
 __device__ __forceinline__ float paged_softmax(uint32_t s_addr, bool mask, int see, float c,
                                                float& m, float& l, bool& moved) {
@@ -203,7 +201,7 @@ __device__ __forceinline__ float paged_softmax(uint32_t s_addr, bool mask, int s
     for (int u = 0; u < 8; ++u) pm[u] = fmax3(pm[u], s[k + u], s[k + u + 8]);
   const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]),
                          fmaxf(fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-  const float m_new = fmaxf(m, mx * c);
+  const float m_new = F16 ? mx * c - kPagedP16 : mx * c;
   float alpha = 1.0f;
   moved = m_new > m + kPagedRescale;
   if (moved) {
