@@ -107,15 +107,24 @@ __device__ __forceinline__ long long paged_div(long long a, long long b) {
   return a / b;
 }
 
+// A sequence: its first row, its rows and its keys.  Its starts may go on past row T;
+// those tokens have no rows here, and under the causal mask no key of theirs is seen,
+// so the sequence then ends before them: its other tokens keep their places, as they
+// do for the append.
 struct PagedSeq {
   int q0, qlen, klen;
 };
 
+__device__ __forceinline__ int paged_room(const PagedParams& p) {
+  return p.max_pages << p.page_shift;
+}
+
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int s) {
   PagedSeq g;
   g.q0 = min(max(p.q_start[s], 0), p.T);
-  g.qlen = min(max(p.q_start[s + 1], g.q0), p.T) - g.q0;
-  g.klen = min(max(p.kv_len[s], 0), p.max_pages << p.page_shift);
+  const int end = max(p.q_start[s + 1], g.q0);
+  g.qlen = min(end, p.T) - g.q0;
+  g.klen = min(max(p.kv_len[s], 0), paged_room(p)) - (p.causal ? max(end - p.T, 0) : 0);
   return g;
 }
 
@@ -263,7 +272,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
     PagedSeq g{0, 0, 0};
     if (s < p.S) {
       g = paged_seq(p, s);
-      if (blockIdx.x == 0 && p.kv_len[s] > g.klen) atomicOr(p.err, kErrBadPage);
+      if (blockIdx.x == 0 && p.kv_len[s] > paged_room(p)) atomicOr(p.err, kErrBadPage);
     }
     return Walk::head_units(p, g) * p.Hkv;
   };

@@ -320,7 +320,9 @@ fa_status fa_rotary_backward(const fa_rotary_rows* q, const fa_rotary_rows* k, i
  * page block_table[s][j / page_size].  A step brings new tokens for some of
  * the sequences: the rows q_start[s] .. q_start[s + 1] - 1 of the step's
  * [T][heads][d] tensors belong to sequence s, whose length INCLUDING them is
- * kv_len[s]; new token i sits at position kv_len - q_len + i.  Lengths, starts
+ * kv_len[s]; new token i sits at position kv_len - q_len + i.  Starts may go on
+ * past T: those tokens have no rows, so they are neither stored nor answered, and
+ * the others keep their positions.  Lengths, starts
  * and tables are read on the device when the kernels run.  Sequences may share
  * pages (a common beginning) that none of them appends to in the step.
  */
@@ -346,7 +348,7 @@ typedef struct {
   const int* block_table;  /* device int32, row s at block_table + s * table_stride; entries */
   long long table_stride;  /* past a sequence's length are not read */
   int max_pages;           /* entries of a row */
-  const int* q_start;      /* device int32 [S + 1], not decreasing */
+  const int* q_start;      /* device int32 [S + 1], >= 0 and not decreasing */
   const int* kv_len;       /* device int32 [S] */
   int S;                   /* sequences, >= 0 */
   int max_q_len;           /* the most new tokens of one sequence: chooses the kernels, and a */
