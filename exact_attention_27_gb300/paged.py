@@ -251,6 +251,8 @@ def _launch_turn(fn, rows_q, rows_k, shape, k, positions, rotary, stream):
 
 
 def _turn(fn, q, q_out, k, k_out, positions, rotary, stream):
+    if (k is None) != (k_out is None):
+        raise ValueError("give k and its output, or neither")
     device = rotary.device
     _launch_turn(fn, _rotary_rows(q, q_out, device, "q"),
                  None if k is None else _rotary_rows(k, k_out, device, "k"), q.shape, k, positions,

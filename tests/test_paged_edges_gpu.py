@@ -58,3 +58,21 @@ def test_starts_past_the_last_row(cut, d, causal, e4m3):
         assert torch.all((o[at:at + rows].cpu().double() - ro).abs() <= ot), s
         assert torch.all((lse[at:at + rows].cpu().double() - rl).abs() <= lt), s
         at += n
+
+
+@pytest.mark.parametrize("fn", ["fa_rotary", "fa_rotary_backward"])
+def test_k_without_its_output_is_refused(fn):
+    """One of k and k_out alone: an output that nothing would write, or a tensor to turn into
+    nothing."""
+    import exact_attention_27_gb300 as fa
+    x = torch.randn(1, 2, 8, 64, device="cuda").to(torch.bfloat16)
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    positions = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    rotary = fa.Rotary(torch.ones(32, device="cuda"))
+    for k, k_out in ((x, None), (None, z)):
+        with pytest.raises(ValueError, match="neither"):
+            getattr(fa, fn)(x, y, k, k_out, positions, rotary)
+    getattr(fa, fn)(x, y, None, None, positions, rotary)
+    getattr(fa, fn)(x, y, x, z, positions, rotary)
+    torch.cuda.synchronize()
+    assert torch.equal(y, z)
