@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "fa_internal.h"
@@ -649,14 +650,6 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return n;
-}
-
 // Rows of an item, which says the kernel: sequences of at most 16 rows go to the
 // kernel above, anything longer to the tcgen05 kernels (64 sequences of 100 to
 // 8000 keys, 32 rows each, d = 128: 213 us there, 269 us 32 rows a time here;
@@ -717,6 +710,18 @@ cudaError_t launch_join(const PagedParams& p, int rows, int d, int ctas, cudaStr
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
+
+int sm_count() {
+  static std::atomic<int> known[64];  // by device; 0: not asked yet
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool slot = dev >= 0 && dev < 64;
+  if (slot && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (slot) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace fa
 
 extern "C" {

@@ -20,6 +20,9 @@ constexpr uint32_t kErrBadPage = 1u << 5;
 // T = 0 or S = 0 needs no pointers.
 fa_status validate_cache(const fa_paged_cache* c, const fa_paged_batch* b, int T);
 
+// Multiprocessors of the current device, 0 if CUDA gives none (fa_paged.cu).
+int sm_count();
+
 // The pages (k or v) of a paged cache as bytes (d, row, head, page), boxes of
 // 128 bytes x box_rows rows, 128-byte swizzle (fa_api.cu).
 bool encode_map_pages(CUtensorMap* m, const fa_paged_cache& c, const void* pages, int box_rows);

@@ -308,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, 4) fa_turn_kernel(const __grid_const
 template <int D, int TO>
 cudaError_t launch_turn_d(const TurnParams& p, cudaStream_t stream) {
   const int heads = p.q.heads + p.k.heads + p.v.heads;
+  const long long sms = sm_count();
+  if (sms < 1) return cudaErrorInvalidDevice;
   // The most positions a block that leave a block for every SM and a thread at
   // most ten heads: the angles' cost is shared, and a short loop ends evenly.
   // Measured with 1 / 4 / 8 / 16: 8192 positions of 16 heads, d = 64: 38 / 14.5 /
@@ -315,7 +317,7 @@ cudaError_t launch_turn_d(const TurnParams& p, cudaStream_t stream) {
   // 96: 6.3 / 4.5 / 4.9 / 7.2; 4 of 48, d = 128: 4.0 / 4.8 / 5.8 / 8.5.
   int tok = 1;
   for (int more : {4, 8, 16})
-    if (p.tokens >= 152LL * more && heads * (D / 16) * more <= 10 * kThreads) tok = more;
+    if (p.tokens >= sms * more && heads * (D / 16) * more <= 10 * kThreads) tok = more;
   const long long grid = (p.tokens + tok - 1) / tok;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kern = tok == 1 ? fa_turn_kernel<D, 1, TO>
