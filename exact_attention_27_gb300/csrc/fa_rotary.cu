@@ -5,12 +5,13 @@
 //     y_i = x_i cos a - x_j sin a,   y_j = x_i sin a + x_j cos a,
 // and the gradient is the turn by -a (the turn is orthogonal).
 //
-// Angle.  Only a mod one turn matters.  f / 2 pi is rounded once to a 64-bit
-// fraction of a turn F (from a double product, off by 2^-53 relative), and
-// position * F wraps modulo 2^64, which is exact: at position 2^20 and f = 1
-// the error is 2^-36 of a turn, where position * f in fp32 would be off by
-// 2^-5 radians.  The top 32 bits, as a signed fraction in [-1/2, 1/2), go to
-// sincospif.
+// Angle.  Only a mod one turn matters.  f / 2 pi becomes a 64-bit fraction of a
+// turn F, from a double product (off by 2^-52 relative), and position * F wraps
+// modulo 2^64, which is exact: at position 2^20 and f = 1 it is off by 2^-34 of a
+// turn, where position * f in fp32 would be off by 2^-5 radians.  The top 32 bits,
+// as a signed fraction in [-1/2, 1/2), go through fp32 to sincospif: 2^-32 of a
+// turn for the cut and 2^-26 for fp32, at any position, which is the larger part
+// up to position 2^28 (the product's is 2^-23.6 at 2^31).
 //
 // Both are bound by memory: they read and write every row once (3 operations
 // for 4 bytes of traffic).  The angles of a position are shared by all its

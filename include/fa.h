@@ -267,8 +267,9 @@ fa_status fa_backward_preprocess(const void* o, const void* dO, float* D, long l
  *     y_i = x_i cos a - x_j sin a,   y_j = x_i sin a + x_j cos a,
  * and values at and past rot_dim are copied.  Text has one axis; images and
  * video have one each for time, height and width, shared out over the pairs
- * by `axis`.  The angle is reduced to a fraction of a turn in 64-bit integers,
- * so far positions lose nothing; products and sums are fp32, and each output
+ * by `axis`.  The angle is reduced to a fraction of a turn in 64-bit integers:
+ * for frequencies up to 1 it is off by 2^-25 of a turn at most at positions up to
+ * 2^28, and by 2^-23 at the farthest.  Products and sums are fp32, and each output
  * is rounded once.
  */
 typedef struct {
