@@ -51,7 +51,7 @@ constexpr int kTK = 64;  // keys per tile
 // CTAs an SM.  A CTA's four warps each wait for loads, conversions and products
 // in turn, so more of them hide more, as registers and shared memory allow; with
 // bytes half as many, e4m3 pages want three (120,000 keys of 8 heads, d = 128: 59
-// us with two).
+// us with two, though d = 128 then spills 60 bytes a thread).
 constexpr int rows_occupancy(int d, bool e4m3) { return d == 256 ? 1 : e4m3 ? 3 : 2; }
 
 template <int D_, bool E4M3_>
@@ -560,7 +560,10 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
 // of its own.  Many parts and few rows (a long history): the block's groups share a
 // row's parts and join through shared memory.  Either way the order is that of the
 // CTAs.  (512 rows of 30,000 keys, d = 64: 27.2 us, 46.4 us when items of all
-// heights of many parts share rows.)
+// heights of many parts share rows.)  The blocks an item are fixed, however few items
+// there are: one item of 256 rows in 152 parts (64 tokens of 4 heads over 100,000 keys
+// of one head, d = 128) keeps 16 blocks busy while the others idle, 63 us in all for
+// 7.6 us of bytes.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinFew = 12;
 constexpr int kJoinRowsBlocks = 4, kJoinTileBlocks = 16;
@@ -653,7 +656,10 @@ __global__ void __launch_bounds__(kJoinThreads)
 // Rows of an item, which says the kernel: sequences of at most 16 rows go to the
 // kernel above, anything longer to the tcgen05 kernels (64 sequences of 100 to
 // 8000 keys, 32 rows each, d = 128: 213 us there, 269 us 32 rows a time here;
-// 348 us as two items of 16).
+// 348 us as two items of 16).  The longest sequence decides for the whole step, so
+// the single tokens of a mixed step fill 128-row tiles: 3 chunks among 21 tokens,
+// 16 / 4 heads, d = 64, take 40.9 us, the chunks on their own 29.9, and single
+// tokens of all 24 sequences in the kernel above 22.1.
 int rows_for(long long most, int d) { return most <= 16 ? 16 : paged_tile_rows(d); }
 
 // CTAs of a launch with `rows` rows an item.

@@ -64,7 +64,7 @@ struct TileCfg {
   static constexpr int KV_BLOCK = BN * 128;
   static constexpr int Q_TILE = SUB * Q_BLOCK;
   static constexpr int KV_TILE = SUB * KV_BLOCK;
-  static constexpr int NQ = 1;                     // Q tiles
+  static constexpr int NQ = 1;                     // Q tiles (shared memory has room for one)
   static constexpr int NS = 2;                     // K and V stages each
   // e4m3 bytes as they come: K and V tiles in turn.
   static constexpr int RSUB = (D + 127) / 128;
