@@ -514,7 +514,8 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
         for (int i = 0; i < 2; ++i) {
           if (!live[i]) continue;
           const long long token = w.g.q0 + tok[i];
-          const float inv = L[i] > 0.0f ? p.v_scale / L[i] : 0.0f;
+          // (v_scale / L could fall below fp32's range where o does not)
+          const float inv = L[i] > 0.0f ? 1.0f / L[i] : 0.0f;
           __nv_bfloat16* dst = p.o + token * p.o_token + head[i] * p.o_head;
           float* pd = po + (g + 8 * i) * D;
 #pragma unroll
@@ -526,7 +527,8 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
               const int col = nt / 2 * 16 + 4 * c;
               if (whole)
                 *reinterpret_cast<uint2*>(dst + col) = make_uint2(
-                    pack_bf16x2(x0 * inv, y0 * inv), pack_bf16x2(x1 * inv, y1 * inv));
+                    pack_bf16x2(x0 * inv * p.v_scale, y0 * inv * p.v_scale),
+                    pack_bf16x2(x1 * inv * p.v_scale, y1 * inv * p.v_scale));
               else
                 *reinterpret_cast<float4*>(pd + col) = make_float4(x0, y0, x1, y1);
             } else {
@@ -624,9 +626,10 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int tok = r / p.G;
     const long long token = note.q0 + tok;
     const int head = note.head * p.G + (r - tok * p.G);
-    const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     *reinterpret_cast<uint2*>(p.o + token * p.o_token + head * p.o_head + 4 * lane) =
-        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        make_uint2(pack_bf16x2(a.x * inv * p.v_scale, a.y * inv * p.v_scale),
+                   pack_bf16x2(a.z * inv * p.v_scale, a.w * inv * p.v_scale));
     if (lane == 0 && p.lse)
       p.lse[token * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kPagedLn2;
   };

@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(384, 1)
       // ---------------------------------------------------------- end of the item
       tc_fence_after();
       const int slot = cta * 2 + (seg.t0 == 0 ? 1 : 0);
-      paged_store_row<D, false>(p, x, tmem + lane_off + C::COL_O, 0, 1.0f, 0.0f,
+      paged_store_row<D, E4M3, false>(p, x, tmem + lane_off + C::COL_O, 0, 1.0f, 0.0f,
                                 seg.t0 == 0 && seg.t1 == seg.tiles,
                                 static_cast<long long>(slot) * C::BM + row, m_used, l);
       if (row == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)

@@ -257,12 +257,13 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t* v) {
 // A row's O out of TMEM (TWO: fa times the one at o_addr plus fb times the one
 // at o_addr2): the result if its item lies whole in this CTA, else its part, at
 // row `part_row` of the parts.
-template <int D, bool TWO>
+template <int D, bool E4M3, bool TWO>
 __device__ __forceinline__ void paged_store_row(const PagedParams& p, const PagedRow& x,
                                                 uint32_t o_addr, uint32_t o_addr2, float fa,
                                                 float fb, bool whole, long long part_row, float m,
                                                 float l) {
-  const float inv = l > 0.0f ? p.v_scale / l : 0.0f;
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float vs = E4M3 ? p.v_scale : 1.0f;  // (vs / l could fall below fp32's range)
   __nv_bfloat16* dst = p.o + x.token * p.o_token + x.head * p.o_head;
   float* part = p.part_o + part_row * D;
   const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
@@ -285,7 +286,8 @@ __device__ __forceinline__ void paged_store_row(const PagedParams& p, const Page
       uint32_t y[16];
 #pragma unroll
       for (int u = 0; u < 16; ++u)
-        y[u] = pack_bf16x2(__uint_as_float(v[2 * u]) * inv, __uint_as_float(v[2 * u + 1]) * inv);
+        y[u] = pack_bf16x2(__uint_as_float(v[2 * u]) * inv * vs,
+                           __uint_as_float(v[2 * u + 1]) * inv * vs);
       if (wide) {
         stg256(dst + q4 * 32, y);
         stg256(dst + q4 * 32 + 16, y + 8);

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
       if (!(ok = wait(C::B_ODONE + x, (n - 1) & 1, kErrTimeoutEpilogue))) break;
       tc_fence_after();
       if (!both) {
-        paged_store_row<D, false>(p, now, o_addr, 0, 1.0f, 0.0f, whole, part, m, l);
+        paged_store_row<D, E4M3, false>(p, now, o_addr, 0, 1.0f, 0.0f, whole, part, m, l);
       } else if (x == 1) {
         half_ml[row] = make_float2(m, l);
         tc_fence_before();
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(Tile2Cfg<D, E4M3>::THREADS, 1)
         const float m2 = fmaxf(m, b.x);
         const float ref = m2 == -INFINITY ? 0.0f : m2;
         const float fa = ex2_approx(m - ref), fb = ex2_approx(b.x - ref);
-        paged_store_row<D, true>(p, now, o_addr, o_addr + C::DP, fa, fb, whole, part, m2,
+        paged_store_row<D, E4M3, true>(p, now, o_addr, o_addr + C::DP, fa, fb, whole, part, m2,
                                  l * fa + b.y * fb);
       }
       tc_fence_before();

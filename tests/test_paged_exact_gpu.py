@@ -105,3 +105,29 @@ def test_long_histories(d, n, e4m3):
     assert fa.fa_last_device_error() == 0
     want = attention64(step.q_cpu.double(), step.k64[0], step.v64[0], scale, True, m - n)
     compare(o, lse, want, d, m * 2.0 ** -32 * step.v64[0].abs().max(), e4m3)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [3000, 200]), ([20, 300], [3000, 400])])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("power", [-126, -60, 110])
+def test_descales_at_the_ends_of_fp32(power, d, q_lens, kv_lens):
+    """A factor of V near the smallest and largest of its range, with many keys of like weight:
+    the factor over the weights' sum lies outside fp32 where the output does not.  o is that of a
+    factor of 1 times the factor, exactly: a power of two."""
+    import exact_attention_27_gb300 as fa
+    step = Step(q_lens, kv_lens, 4, 2, d, 16, True, seed=d, k_scale=0.01)
+    batch = step.handles()[1]
+    outs = []
+    for descale in (1.0, 2.0 ** power):
+        cache = fa.PagedCache(step.k_pages, step.v_pages, step.kd, descale)
+        outs.append(fa.paged_attention(cache, batch, step.q))
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_error() == 0
+    (a, la), (b, lb) = outs
+    assert torch.equal(la, lb)
+    want = a.double() * 2.0 ** power
+    # Below 2^-126 bf16 has steps of 2^-133, half of which is 2^-134; a itself is off by 2^-9 of
+    # what is then below 2^-126, and fp32's steps there are 2^-149: 2^-134 + 2^-135 + 2^-150.
+    # From 2^-126 on both are the same bits, scaled.
+    slack = torch.where(want.abs() < 2.0 ** -126, 2.0 ** -133, 0.0)
+    assert torch.all((b.double() - want).abs() <= slack)
