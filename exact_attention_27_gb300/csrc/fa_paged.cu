@@ -366,12 +366,12 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
             float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]),
                              fmaxf(s[1][2 * i], s[1][2 * i + 1]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * cs[i];
-            if (E4M3) mx -= kPagedP16;
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             alpha[i] = 1.0f;
-            if (mx > m[i] + kPagedRescale) {
-              alpha[i] = ex2_approx(m[i] - mx);
-              m[i] = mx;
+            if (paged_moves<E4M3>(mx, cs[i], m[i])) {
+              const float m_new = paged_reference<E4M3>(mx, cs[i]);
+              alpha[i] = ex2_approx(m[i] - m_new);
+              m[i] = m_new;
               upd = true;
             }
             const float ref = m[i] == -INFINITY ? 0.0f : m[i];

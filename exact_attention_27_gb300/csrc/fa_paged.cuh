@@ -68,6 +68,22 @@ constexpr float kPagedLn2 = 0.6931471805599453f;
 constexpr float kPagedRescale = 8.0f;
 constexpr float kPagedP16 = 7.0f;
 
+// Whether the reference m has to move for scores up to mx (times c).  For fp16 P the
+// largest exponent is worked out as the exponents themselves are, in one rounding, so
+// that none passes 15 unmoved however far the scores are from 0: fp16 has one bit more,
+// where fp32's steps at 2^24 are 2.
+template <bool F16>
+__device__ __forceinline__ bool paged_moves(float mx, float c, float m) {
+  if constexpr (F16) return fmaf(mx, c, -m) > kPagedRescale + kPagedP16;
+  return mx * c > m + kPagedRescale;
+}
+
+// The reference that scores up to mx (times c) want.
+template <bool F16>
+__device__ __forceinline__ float paged_reference(float mx, float c) {
+  return F16 ? fmaf(mx, c, -kPagedP16) : mx * c;
+}
+
 struct PagedNote {
   int last;   // last CTA with a part of the item that starts here; -1: none
   int q0;     // first token of the sequence

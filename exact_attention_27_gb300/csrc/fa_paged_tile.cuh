@@ -201,10 +201,10 @@ __device__ __forceinline__ float paged_softmax(uint32_t s_addr, bool mask, int s
     for (int u = 0; u < 8; ++u) pm[u] = fmax3(pm[u], s[k + u], s[k + u + 8]);
   const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]),
                          fmaxf(fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-  const float m_new = F16 ? mx * c - kPagedP16 : mx * c;
   float alpha = 1.0f;
-  moved = m_new > m + kPagedRescale;
+  moved = paged_moves<F16>(mx, c, m);
   if (moved) {
+    const float m_new = paged_reference<F16>(mx, c);
     alpha = ex2_approx(m - m_new);
     m = m_new;
   }

@@ -131,3 +131,50 @@ def test_descales_at_the_ends_of_fp32(power, d, q_lens, kv_lens):
     # From 2^-126 on both are the same bits, scaled.
     slack = torch.where(want.abs() < 2.0 ** -126, 2.0 ** -133, 0.0)
     assert torch.all((b.double() - want).abs() <= slack)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [1, 20, 130])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("base", [0, 20, 22, 23, 24, 25])
+def test_far_scores_that_climb(base, d, n, e4m3):
+    """Scores of 2^base that climb by a few nats a tile, where fp32's steps at that size (2^base
+    x 2^-23) are no longer small beside them.  With values of 1 o is 1, however the weights come
+    out: their sum, rounded (2^-11 or 2^-8 of each weight), over their sum, and half a step of
+    o.  lse is off by what the scores are: a few steps of their size."""
+    import exact_attention_27_gb300 as fa
+    S, H, m, page = 64, 8, 1500, 64
+    g = torch.Generator().manual_seed(base + d + n)
+    k = torch.zeros(m, H, d)
+    k[:, :, 0] = 16.0 if base else 0.0
+    climb = torch.linspace(-15.0, 15.0, m)[:, None] + 4.0 * torch.rand(m, H, generator=g)
+    k[:, :, 1] = climb.clamp(-16.0, 16.0)
+    kd = 0.0625 if e4m3 else 1.0
+    dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    k = (k / kd).to(dtype)
+    n_pages = -(-m // page)
+    pages = []
+    for x in (k.float(), torch.ones(m, H, d)):
+        room = torch.full((n_pages * page, H, d), float("nan"))
+        room[:m] = x
+        pages.append(room.view(n_pages, page, H, d).transpose(1, 2).contiguous().to(dtype).cuda())
+    cache = fa.PagedCache(pages[0], pages[1], kd, 1.0)
+    # (every sequence reads the same pages)
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda").expand(S, n_pages)
+    starts = torch.arange(0, n * S + 1, n, dtype=torch.int32, device="cuda")
+    batch = fa.PagedBatch(table, starts, torch.full((S,), m, dtype=torch.int32, device="cuda"), n)
+    q = torch.zeros(n * S, H, d)
+    q[..., 0] = 2.0 ** (base - 4)
+    q[..., 1] = 3.0
+    o, lse = fa.paged_attention(cache, batch, q.to(torch.bfloat16).cuda(), False, 1.0)
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_error() == 0
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    # (the weights' rounding 2^-8 or 2^-11, sums of at most m terms in fp32, o's rounding)
+    tol = (F16 if e4m3 else BF16) + BF16 + 2 * m * F32
+    assert (o.float() - 1.0).abs().max().item() <= tol
+    top = 2.0 ** (base - 4) * 16.0 * bool(base)
+    want = top + torch.logsumexp(3.0 * kd * k[:, :, 1].double(), 0)
+    size = top + 3.0 * 16.0
+    err = (lse.cpu().double().view(S, n, H) - want).abs().max().item()
+    assert err <= 2 * ((d + 8) * F32 * 2 * size + 2.0 ** -20) + 2 * F32 * size
