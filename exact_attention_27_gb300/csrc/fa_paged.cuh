@@ -71,7 +71,8 @@ constexpr float kPagedP16 = 7.0f;
 // Whether the reference m has to move for scores up to mx (times c).  For fp16 P the
 // largest exponent is worked out as the exponents themselves are, in one rounding, so
 // that none passes 15 unmoved however far the scores are from 0: fp16 has one bit more,
-// where fp32's steps at 2^24 are 2.
+// where fp32's steps at 2^24 are 2.  (A moved reference is rounded to such a step too:
+// by 8 at most below 2^28, so up to there p stays within 2^15.)
 template <bool F16>
 __device__ __forceinline__ bool paged_moves(float mx, float c, float m) {
   if constexpr (F16) return fmaf(mx, c, -m) > kPagedRescale + kPagedP16;

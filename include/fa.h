@@ -397,7 +397,7 @@ fa_status fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* bat
  * Sums, softmax statistics and the parts of divided rows are fp32.  The weights are
  * rounded before they meet V, but not in their sum: to bf16 for bf16 pages (2^-8 of
  * each), to fp16 for e4m3 pages (2^-11 of each, and 2^-32 of the largest where that
- * is more).
+ * is more; scores, scale times q.k, up to 2^27: fp16 weights may overflow beyond).
  * Positions past a sequence's length are never used, whatever their bits; the
  * values at positions below it must be finite.  Rows of q past q_start[S] get
  * no output.  A length past the table's row is cut to it, and a page outside

@@ -136,7 +136,7 @@ def test_descales_at_the_ends_of_fp32(power, d, q_lens, kv_lens):
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("n", [1, 20, 130])
 @pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("base", [0, 20, 22, 23, 24, 25])
+@pytest.mark.parametrize("base", [0, 20, 22, 23, 24, 25, 26, 27])
 def test_far_scores_that_climb(base, d, n, e4m3):
     """Scores of 2^base that climb by a few nats a tile, where fp32's steps at that size (2^base
     x 2^-23) are no longer small beside them.  With values of 1 o is 1, however the weights come
