@@ -32,7 +32,8 @@ __all__ = [
     "fa_last_device_error", "fa_selftest_wait_timeout", "fa_set_backward_events", "attention_forward", "attention_backward",
     "library", "Rotary", "PagedCache", "PagedBatch", "fa_rotary", "fa_rotary_backward",
     "fa_paged_append", "fa_forward_paged", "paged_workspace", "rotary_forward", "rotary_backward",
-    "paged_append", "paged_attention",
+    "paged_append", "paged_attention", "Scores", "KeySpans", "fa_forward_scores",
+    "fa_backward_scores",
 ]
 
 FA_OK = 0
@@ -233,15 +234,24 @@ def fa_set_backward_events(before, after):
     library().fa_set_backward_events(h(before), h(after))
 
 
-def attention_forward(q, k, v, causal=False, scale=None, q_offset=None, stream=None):
-    """Allocates o and lse on q's device and runs fa_forward (or fa_forward_ex
-    when q and k differ in length or a query offset is given); returns (o, lse)."""
+def attention_forward(q, k, v, causal=False, scale=None, q_offset=None, stream=None, scores=None,
+                      spans=None):
+    """Allocates o and lse on q's device and runs fa_forward (fa_forward_ex
+    when q and k differ in length or a query offset is given; fa_forward_scores
+    with `scores`, a Scores, or `spans`, a KeySpans); returns (o, lse)."""
     import torch
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    if q_offset is None and q.shape[2] == k.shape[2]:
+    if stream is not None and (scores is not None or spans is not None):
+        with _on(stream):
+            o = torch.empty_like(q)
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    else:
+        o = torch.empty_like(q)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    if scores is not None or spans is not None:
+        fa_forward_scores(q, k, v, o, lse, scale, causal, q_offset or 0, scores, spans, stream)
+    elif q_offset is None and q.shape[2] == k.shape[2]:
         fa_forward(q, k, v, o, lse, scale, causal, stream)
     else:
         fa_forward_ex(q, k, v, o, lse, scale, causal, q_offset or 0, stream)
@@ -249,12 +259,22 @@ def attention_forward(q, k, v, causal=False, scale=None, q_offset=None, stream=N
 
 
 def attention_backward(q, k, v, o, lse, do, causal=False, scale=None, deterministic=False,
-                       stream=None):
+                       stream=None, q_offset=None, scores=None, spans=None):
     """Allocates dq, dk, dv on q's device and runs fa_backward (or
-    fa_backward_deterministic); returns them."""
+    fa_backward_deterministic, or with `scores`, `spans` or a query offset
+    fa_backward_scores, whose bits always repeat); returns them."""
     import torch
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
+    if scores is not None or spans is not None or q_offset is not None:
+        if stream is not None:
+            with _on(stream):
+                grads = tuple(torch.empty_like(t) for t in (q, k, v))
+        else:
+            grads = tuple(torch.empty_like(t) for t in (q, k, v))
+        fa_backward_scores(q, k, v, o, lse, do, *grads, scale, causal, q_offset or 0, scores, spans,
+                           stream)
+        return grads
     dq = torch.empty_like(q)
     dk = torch.empty_like(k)
     dv = torch.empty_like(v)
@@ -263,6 +283,7 @@ def attention_backward(q, k, v, o, lse, do, causal=False, scale=None, determinis
     return dq, dk, dv
 
 
-from .paged import (PagedBatch, PagedCache, Rotary, fa_forward_paged, fa_paged_append,  # noqa: E402
+from .paged import (_on, PagedBatch, PagedCache, Rotary, fa_forward_paged, fa_paged_append,  # noqa: E402
                     fa_rotary, fa_rotary_backward, paged_append, paged_attention,
                     paged_workspace, rotary_backward, rotary_forward)
+from .scores import KeySpans, Scores, fa_backward_scores, fa_forward_scores  # noqa: E402

@@ -52,6 +52,18 @@ class PagedBatchStruct(ctypes.Structure):
                 ("kv_len", ctypes.c_void_p), ("S", ctypes.c_int), ("max_q_len", ctypes.c_int)]
 
 
+class ScoreSpec(ctypes.Structure):
+    """fa_score_spec of include/fa.h."""
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int)]
+
+
+class KeySpansStruct(ctypes.Structure):
+    """fa_key_spans of include/fa.h."""
+    _fields_ = [("first", ctypes.c_void_p), ("end", ctypes.c_void_p),
+                ("batch_stride", ctypes.c_longlong)]
+
+
 class FaError(RuntimeError):
     """A non-zero fa_status returned by the CUDA library."""
 
@@ -84,6 +96,11 @@ def _declare(lib):
     lib.fa_backward_noalloc.argtypes = [p, p, p, p, p, p, p, p, p, i, i, i, i, i, f, i, p]
     lib.fa_backward_preprocess.restype = i
     lib.fa_backward_preprocess.argtypes = [p, p, p, ll, i, p]
+    lib.fa_forward_scores.restype = i
+    lib.fa_forward_scores.argtypes = [p, p, p, p, p, i, i, i, i, i, i, f, i, i, p, p, p]
+    lib.fa_backward_scores.restype = i
+    lib.fa_backward_scores.argtypes = [p, p, p, p, p, p, p, p, p, i, i, i, i, i, i, f, i, i, p, p,
+                                       p]
     for name in ("fa_rotary", "fa_rotary_backward"):
         fn = getattr(lib, name)
         fn.restype = i

@@ -191,6 +191,10 @@ bool encode_map_bf16(CUtensorMap* m, const void* ptr, int d, int N, long long pl
   return make_map_bf16(m, ptr, d, N, planes);
 }
 
+bool encode_map_kv_bf16(CUtensorMap* m, const void* ptr, int d, int N, long long planes) {
+  return make_kv_map_bf16(m, ptr, d, N, planes);
+}
+
 bool encode_map_pages(CUtensorMap* m, const fa_paged_cache& c, const void* pages, int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;

@@ -1,0 +1,159 @@
+// Shared by the kernels of fa_forward_scores, fa_backward_scores and
+// fa_forward_paged_scores: what is done to a score between Q K^T and the softmax,
+// and which keys a query row sees.
+//
+//   x = scale q.k;   x = softcap tanh(x / softcap);   x = x - slope_h |pos - j|
+//
+// and row i, at position pos = q_offset + i, sees the keys of one span
+//   [max(first_i, pos - window + 1, 0), min(end_i, pos + 1 if causal, N_kv)),
+// so a row's mask is two integers that its thread keeps in registers, a tile needs
+// no mask at all where every row's span covers it, and tiles outside the union of the
+// rows' spans are never visited.
+//
+// Everything after Q K^T is in the log2 domain (factors of log2(e) are folded in on
+// the host).  The tanh: for |y| <= 0.6, y = x / softcap, as y P(y^2) with P of degree 4,
+// fitted here for the least largest relative error, 7.3e-8 (1.8e-7 with fp32's roundings),
+// eight operations on the FMA pipe in place of the one that scales a score, where one ex2 and
+// one rcp more for each score would take the special-function unit longer than the weights'
+// own exponentials.  (Degree 3 is off by 6e-7 of the cap, which would show in lse.)  A warp
+// with a score beyond goes by tanh y = 1 - 2 / (e^{2y} + 1), which holds everywhere, to 2e-7.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "fa_ptx.cuh"
+#include "fa_scores_host.h"
+
+namespace fa {
+
+constexpr float kScoreLog2e = 1.4426950408889634f;
+constexpr float kScoreLn2 = 0.6931471805599453f;
+
+// tanh(y) = y (c0 + c1 y^2 + ... + c4 y^8) for |y| <= kTanhRange.
+constexpr float kTanhRange = 0.6f;
+constexpr float kTanhC0 = 0.9999999268681676f;
+constexpr float kTanhC1 = -0.3333230997118056f;
+constexpr float kTanhC2 = 0.13310173624961602f;
+constexpr float kTanhC3 = -0.05210147888220161f;
+constexpr float kTanhC4 = 0.01547542595341364f;
+
+struct KeySpan {
+  int lo, hi;  // keys [lo, hi); 0, 0 for a row that sees none
+};
+
+__device__ __forceinline__ KeySpan row_span(const ScoreParams& p, int b, int i) {
+  KeySpan s{0, 0};
+  if (i >= p.Nq) return s;
+  const long long at = b * p.span_batch + i;
+  const int pos = p.q_offset + i;
+  s.hi = p.Nk;
+  if (p.first) s.lo = max(p.first[at], 0);
+  if (p.end) s.hi = min(p.end[at], p.Nk);
+  if (p.window > 0) s.lo = max(s.lo, pos - p.window + 1);
+  if (p.causal) s.hi = min(s.hi, pos + 1);
+  if (s.lo >= s.hi) s.lo = s.hi = 0;
+  return s;
+}
+
+// The union of the spans of the warp's rows, as [lo, hi); lo = INT_MAX, hi = 0 if all are empty.
+__device__ __forceinline__ KeySpan warp_hull(const KeySpan& s) {
+  KeySpan h;
+  h.lo = __reduce_min_sync(0xffffffffu, s.hi > s.lo ? s.lo : INT_MAX);
+  h.hi = __reduce_max_sync(0xffffffffu, s.hi);
+  return h;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// What turns raw products s = q.k of keys kbase + t, t = 0 .. N-1, into exponents of the
+// weights, x (log2 domain), less `sub`:  CAP x = cap2 tanh(s y_scale), else x = s scale2;
+// BIAS then - slope2 |pos - key|.  With GRAD, g gets 1 - tanh^2.  The whole warp calls this.
+template <int N, bool CAP, bool BIAS, bool GRAD>
+__device__ __forceinline__ void shape_scores(const ScoreParams& p, float (&s)[N],
+                                             float (&g)[GRAD ? N : 1], float slope2, float dist0,
+                                             float sub) {
+  if constexpr (CAP) {
+    const uint64_t k2 = f2_pack(p.y_scale, p.y_scale);
+    float big = 0.0f;
+#pragma unroll
+    for (int t = 0; t < N; t += 2) big = fmax3(big, fabsf(s[t]), fabsf(s[t + 1]));
+    // (a NaN takes either way to a NaN)
+    if (__any_sync(0xffffffffu, big * p.y_scale > kTanhRange)) {
+#pragma unroll
+      for (int t = 0; t < N; ++t) {
+        const float r = rcp_approx(ex2_approx(s[t] * (2.0f * kScoreLog2e * p.y_scale)) + 1.0f);
+        s[t] = fmaf(-2.0f * p.cap2, r, p.cap2) - sub;
+        if constexpr (GRAD) g[t] = 4.0f * r * (1.0f - r);
+      }
+    } else {
+      const uint64_t c0 = f2_pack(kTanhC0, kTanhC0), c1 = f2_pack(kTanhC1, kTanhC1);
+      const uint64_t c2 = f2_pack(kTanhC2, kTanhC2), c3 = f2_pack(kTanhC3, kTanhC3);
+      const uint64_t c4 = f2_pack(kTanhC4, kTanhC4);
+      const uint64_t cap = f2_pack(p.cap2, p.cap2), ns = f2_pack(-sub, -sub);
+      const uint64_t one = f2_pack(1.0f, 1.0f), minus = f2_pack(-1.0f, -1.0f);
+#pragma unroll
+      for (int t = 0; t < N; t += 2) {
+        const uint64_t y = f2_mul(f2_pack(s[t], s[t + 1]), k2);
+        const uint64_t y2 = f2_mul(y, y);
+        const uint64_t h = f2_fma(f2_fma(f2_fma(f2_fma(c4, y2, c3), y2, c2), y2, c1), y2, c0);
+        const uint64_t th = f2_mul(y, h);
+        f2_unpack(f2_fma(th, cap, ns), s[t], s[t + 1]);
+        if constexpr (GRAD) f2_unpack(f2_fma(f2_mul(th, minus), th, one), g[t], g[t + 1]);
+      }
+    }
+  } else {
+    const uint64_t c = f2_pack(p.scale2, p.scale2), ns = f2_pack(-sub, -sub);
+#pragma unroll
+    for (int t = 0; t < N; t += 2)
+      f2_unpack(f2_fma(f2_pack(s[t], s[t + 1]), c, ns), s[t], s[t + 1]);
+  }
+  if constexpr (BIAS) {
+    // dist0 = pos - kbase: distances are whole numbers, exact in fp32 up to 2^24
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+      s[t] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(t)), s[t]);
+  }
+}
+
+// Byte offset of 16-byte chunk `ch` of row `r` in a 128-byte-swizzled block of 128-byte rows.
+__device__ __forceinline__ uint32_t sw128(int r, int ch) {
+  return static_cast<uint32_t>(r * 128 + ((ch ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+// First query tile whose rows' spans touch keys [k0, k0 + width), and one past the last, into
+// range[0] and range[1] (INT_MAX and 0 before).  The whole block calls this, a barrier before
+// and after it.
+template <int THREADS>
+__device__ __forceinline__ void seen_by(const int2* tiles, int n, int k0, int width, int* range) {
+  int from = INT_MAX, to = 0;
+  for (int i = threadIdx.x; i < n; i += THREADS) {
+    const int2 t = tiles[i];
+    if (t.y > k0 && t.x < k0 + width) {
+      from = min(from, i);
+      to = i + 1;
+    }
+  }
+  from = __reduce_min_sync(0xffffffffu, from);
+  to = __reduce_max_sync(0xffffffffu, to);
+  if ((threadIdx.x & 31) == 0 && to > 0) {
+    atomicMin(&range[0], from);
+    atomicMax(&range[1], to);
+  }
+}
+
+}  // namespace fa

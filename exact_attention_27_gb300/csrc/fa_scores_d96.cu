@@ -1,0 +1,16 @@
+// The kernels of attention with shaped scores at head dimension 96.
+#include "fa_scores_dq.cuh"
+#include "fa_scores_fwd.cuh"
+#include "fa_scores_dkdv.cuh"
+
+namespace fa {
+
+template cudaError_t launch_scores_forward<96>(const ScoreMaps&, void*, float*, const ScoreParams&,
+                                               int, cudaStream_t);
+template cudaError_t launch_scores_dq<96>(const ScoreMaps&, const float*, float*, void*,
+                                          const ScoreParams&, int, cudaStream_t);
+template cudaError_t launch_scores_dkdv<96>(const ScoreMaps&, const float*, const float*,
+                                            const int2*, void*, void*, const ScoreParams&, int,
+                                            cudaStream_t);
+
+}  // namespace fa

@@ -258,6 +258,61 @@ fa_status fa_backward_noalloc(const void* q, const void* k, const void* v, const
 fa_status fa_backward_preprocess(const void* o, const void* dO, float* D, long long rows, int d,
                                  cudaStream_t stream);
 
+/* ---------------------------------------------------------------- shaped scores
+ *
+ * Attention whose scores are more than scale q.k: capped by a tanh, lowered with the distance
+ * of two positions, and seen through a span of keys for each query.  Query row i sits at
+ * position q_offset + i, key j at position j:
+ *     x = scale q_i.k_j
+ *     x = softcap tanh(x / softcap)              softcap > 0
+ *     x = x - slopes[h] |q_offset + i - j|       slopes given
+ *     row i sees keys first_i <= j < end_i, j <= q_offset + i when causal, and
+ *     j > q_offset + i - window when window > 0
+ *     O = softmax(x) V over the keys seen,  L = ln sum exp(x)
+ * Spans say which keys of a batch a row may see: packed documents (first and end of the
+ * row's document), a prefix that all of it sees (end_i = max(i + 1, prefix), not causal), a
+ * padded batch (end_i = the entry's length).  A row that sees no key gets o = 0, L =
+ * -infinity and no gradients.
+ *
+ * Values of q, k, v and dO must be finite, in masked places too: a weight of 0 times an
+ * infinity or a NaN is a NaN.
+ */
+typedef struct {
+  float softcap;       /* >= 0, finite; 0: scores are not capped */
+  const float* slopes; /* device, [H_q] fp32, or NULL: no distance term.  Finite; no gradient */
+  int window;          /* >= 0; 0: none */
+} fa_score_spec;
+
+typedef struct {
+  const int* first;       /* device int32, row i of batch entry b at first[b * batch_stride + i]; */
+  const int* end;         /* NULL: 0, and N_kv.  Clamped to [0, N_kv] */
+  long long batch_stride; /* 0: all entries share one row of spans */
+} fa_key_spans;
+
+/*
+ * Forward pass with shaped scores: fa_forward_ex with `spec` and `spans` (either may be NULL).
+ * The tanh is off by 2e-7 at most (times softcap in the score).  Returns as fa_forward.
+ */
+fa_status fa_forward_scores(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                            int H_q, int H_kv, int N_q, int N_kv, int d, float scale, int causal,
+                            int q_offset, const fa_score_spec* spec, const fa_key_spans* spans,
+                            cudaStream_t stream);
+
+/*
+ * Its backward pass, with the arguments of that forward:
+ *   P = exp(x - L);  dV = P^T dO;  dS = P o (1 - tanh^2) o (dO V^T - D);
+ *   dQ = dS K scale;  dK = dS^T Q scale
+ * (no 1 - tanh^2 without softcap), dK and dV of a shared head summed over its query heads.
+ * One kernel for dK and dV and one for dQ, without atomics: results repeat to the bit.
+ * Scratch: 4 bytes a query row and 8 for every 128 of them, taken and released stream-ordered
+ * as by fa_backward.
+ */
+fa_status fa_backward_scores(const void* q, const void* k, const void* v, const void* o,
+                             const float* lse, const void* dO, void* dq, void* dk, void* dv, int B,
+                             int H_q, int H_kv, int N_q, int N_kv, int d, float scale, int causal,
+                             int q_offset, const fa_score_spec* spec, const fa_key_spans* spans,
+                             cudaStream_t stream);
+
 /* ---------------------------------------------------------------- rotary positions
  *
  * Rotary positions turn pairs of a head's values by an angle that grows with
