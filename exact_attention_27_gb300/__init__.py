@@ -33,7 +33,8 @@ __all__ = [
     "library", "Rotary", "PagedCache", "PagedBatch", "fa_rotary", "fa_rotary_backward",
     "fa_paged_append", "fa_forward_paged", "paged_workspace", "rotary_forward", "rotary_backward",
     "paged_append", "paged_attention", "Scores", "KeySpans", "fa_forward_scores",
-    "fa_backward_scores",
+    "fa_backward_scores", "HeadNorm", "fa_norm_rotary", "fa_norm_rotary_backward",
+    "norm_rotary_workspace", "norm_rotary_forward", "norm_rotary_backward",
 ]
 
 FA_OK = 0
@@ -283,7 +284,9 @@ def attention_backward(q, k, v, o, lse, do, causal=False, scale=None, determinis
     return dq, dk, dv
 
 
-from .paged import (_on, PagedBatch, PagedCache, Rotary, fa_forward_paged, fa_paged_append,  # noqa: E402
-                    fa_rotary, fa_rotary_backward, paged_append, paged_attention,
-                    paged_workspace, rotary_backward, rotary_forward)
+from .paged import (_on, HeadNorm, PagedBatch, PagedCache, Rotary, fa_forward_paged,  # noqa: E402
+                    fa_norm_rotary, fa_norm_rotary_backward, fa_paged_append, fa_rotary,
+                    fa_rotary_backward, norm_rotary_backward, norm_rotary_forward,
+                    norm_rotary_workspace, paged_append, paged_attention, paged_workspace,
+                    rotary_backward, rotary_forward)
 from .scores import KeySpans, Scores, fa_backward_scores, fa_forward_scores  # noqa: E402

@@ -35,6 +35,12 @@ class RotaryRows(ctypes.Structure):
                 ("heads", ctypes.c_int)]
 
 
+class HeadNormStruct(ctypes.Structure):
+    """fa_head_norm of include/fa.h."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
 class PagedCacheStruct(ctypes.Structure):
     """fa_paged_cache of include/fa.h."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
@@ -105,6 +111,16 @@ def _declare(lib):
         fn = getattr(lib, name)
         fn.restype = i
         fn.argtypes = [p, p, i, i, i, p, ll, ll, p, p]
+    lib.fa_norm_rotary.restype = i
+    lib.fa_norm_rotary.argtypes = [p, p, i, i, i, p, p, ll, ll, p, p]
+    lib.fa_norm_rotary_backward.restype = i
+    lib.fa_norm_rotary_backward.argtypes = [p, p, p, p, i, i, i, p, p, p, p, ll, ll, p, p,
+                                            ctypes.c_size_t, p]
+    lib.fa_norm_rotary_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.fa_norm_rotary_backward_workspace_bytes.argtypes = [i]
+    lib.fa_paged_append_norm.restype = i
+    lib.fa_paged_append_norm.argtypes = [p, p, p, ll, ll, p, ll, ll, i, p, ll, ll, p, ll, ll, i, p,
+                                         p, p, ll, p]
     lib.fa_paged_append.restype = i
     lib.fa_paged_append.argtypes = [p, p, p, ll, ll, p, ll, ll, i, p, ll, ll, p, ll, ll, i, p, p,
                                     ll, p]

@@ -1,13 +1,14 @@
-"""Binding of the rotary-position and paged-cache entry points of include/fa.h.
+"""Binding of the rotary-position, head-norm and paged-cache entry points of include/fa.h.
 
 What a program keeps for many calls is checked once, in a handle that holds its
-tensors and mirrors a struct of the C interface: `Rotary` (of a model),
+tensors and mirrors a struct of the C interface: `Rotary` (of a model), `HeadNorm` and
 `PagedCache` (of a layer) and `PagedBatch` (of a step, shared by its layers).
 The handles hold addresses, not values: a tensor written in place is seen by the
 next call, and a captured graph replays with what the tensors then hold.
 
 The fa_* functions write into the caller's tensors; rotary_forward,
-rotary_backward, paged_append and paged_attention allocate what they return.
+rotary_backward, norm_rotary_forward, norm_rotary_backward, paged_append and
+paged_attention allocate what they return.
 """
 
 import ctypes
@@ -137,6 +138,41 @@ class Rotary:
         self._c = _lib.RotarySpec(inv_freq.data_ptr(), 2 * half, axes, int(bool(interleaved)),
                                   (ctypes.c_ubyte * 128)(*axis_of_pair))
         self._ref = _byref(self._c)
+
+
+class HeadNorm:
+    """Norms of the rows of q and of k of every head, x / sqrt(mean(x^2) + eps) times a weight:
+    q_weight and k_weight [d] fp32 or bf16 on the GPU, both of one type (None: ones)."""
+
+    def __init__(self, q_weight=None, k_weight=None, eps=1e-6, device=None):
+        torch = _load_torch()
+        if not (math.isfinite(eps) and 1e-38 < eps < 1e38):
+            raise ValueError(f"eps {eps}: finite and > 0 is needed")
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
+        given = [(n, w) for n, w in (("q_weight", q_weight), ("k_weight", k_weight))
+                 if w is not None]
+        self.d = self.dtype = None
+        self.device = None if device is None else torch.device(device).index or 0
+        for name, w in given:
+            if w.dtype not in (torch.float32, torch.bfloat16) or not w.is_cuda or w.dim() != 1 or \
+                    not w.is_contiguous() or w.data_ptr() & 15:
+                raise ValueError(f"{name} must be a contiguous fp32 or bf16 CUDA vector that "
+                                 "starts on 16 bytes")
+            if self.d not in (None, w.shape[0]) or self.dtype not in (None, w.dtype) or \
+                    self.device not in (None, w.get_device()):
+                raise ValueError("q_weight and k_weight must have one length, type and device")
+            self.d, self.dtype, self.device = w.shape[0], w.dtype, w.get_device()
+        if self.device is None:
+            self.device = _device()
+        self._c = _lib.HeadNormStruct(
+            q_weight.data_ptr() if q_weight is not None else None,
+            k_weight.data_ptr() if k_weight is not None else None,
+            int(self.dtype is torch.bfloat16), eps)
+        self._ref = _byref(self._c)
+
+    def _check(self, d):
+        if self.d not in (None, d):
+            raise ValueError(f"the norms' weights have {self.d} values, the rows {d}")
 
 
 class PagedCache:
@@ -296,6 +332,150 @@ def _new_rows(x, device, name):
     return out, _rows_bytes(x.data_ptr(), out.data_ptr(), a[0], a[1], a[2], H * N * d, N * d, d, H)
 
 
+def _norm_call(q, k, norm, positions, rotary):
+    """What a call with norms takes of its sizes and positions, after their checks."""
+    B, _, N, d = q.shape
+    device = norm.device
+    norm._check(d)
+    if k is not None and (k.shape[0] != B or k.shape[2] != N or k.shape[3] != d):
+        raise ValueError("k must be [B, H_kv, N, d] with q's B, N and d")
+    if device != _device() or (rotary is not None and rotary.device != device):
+        _same_device(device, rotary)
+    if rotary is None:
+        if positions is not None:
+            raise ValueError("positions without rotary")
+        return B, N, d, norm._ref, None, 0, 0, None
+    if positions is None:
+        raise ValueError("rotary without positions")
+    if positions.dim() == 2:
+        positions = positions[None]
+    _int32("positions", positions, 3, device)
+    if positions.shape != (rotary.axes, B, N):
+        raise ValueError(f"positions have shape {tuple(positions.shape)}, expected "
+                         f"{(rotary.axes, B, N)}")
+    if rotary.rot_dim > d:
+        raise ValueError(f"rotary turns {rotary.rot_dim} values of {d}")
+    s = positions.stride()
+    return B, N, d, norm._ref, positions.data_ptr(), s[0], s[1], rotary._ref
+
+
+def _launch_norm(rows_q, rows_k, call, stream, device):
+    B, N, d, norm, at, axis, batch, ref = call
+    status = library().fa_norm_rotary(rows_q, rows_k, B, N, d, norm, at, axis, batch, ref,
+                                      _stream(stream, device))
+    if status:
+        raise FaError(status, "fa_norm_rotary")
+
+
+def fa_norm_rotary(q, q_out, k, k_out, norm, positions=None, rotary=None, stream=None):
+    """fa_norm_rotary of include/fa.h: fa_rotary of q and k (or None) with their rows normed
+    before; rotary None: normed only."""
+    if (k is None) != (k_out is None):
+        raise ValueError("give k and its output, or neither")
+    device = norm.device
+    call = _norm_call(q, k, norm, positions, rotary)
+    _launch_norm(_rotary_rows(q, q_out, device, "q"),
+                 None if k is None else _rotary_rows(k, k_out, device, "k"), call, stream, device)
+
+
+def norm_rotary_forward(q, k, norm, positions=None, rotary=None, stream=None):
+    """Allocates and returns q and k (None: only q), normed and turned by their positions,
+    contiguous (what attention_forward takes)."""
+    if stream is not None:
+        with _on(stream):
+            return _new_norm(q, k, norm, positions, rotary, stream)
+    return _new_norm(q, k, norm, positions, rotary, None)
+
+
+def _new_norm(q, k, norm, positions, rotary, stream):
+    device = norm.device
+    call = _norm_call(q, k, norm, positions, rotary)
+    q_out, rows_q = _new_rows(q, device, "q")
+    k_out = rows_k = None
+    if k is not None:
+        k_out, rows_k = _new_rows(k, device, "k")
+    _launch_norm(rows_q, rows_k, call, stream, device)
+    return q_out, k_out
+
+
+def _input_rows(x, like, device, name):
+    """The rows of an input alone."""
+    if x.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(like.shape)}")
+    a = _strides(name, x, 4, device)
+    return _rows_bytes(x.data_ptr(), 0, a[0], a[1], a[2], 0, 0, 0, x.shape[1])
+
+
+def norm_rotary_workspace(d, device=None):
+    """A workspace for fa_norm_rotary_backward calls of head dimension d.  Its contents do not
+    matter, and calls on one stream may share it; calls that can overlap may not."""
+    torch = _load_torch()
+    n = library().fa_norm_rotary_backward_workspace_bytes(d)
+    return torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def fa_norm_rotary_backward(dq_out, dq, dk_out, dk, q, k, norm, dq_weight, dk_weight, workspace,
+                            positions=None, rotary=None, stream=None):
+    """fa_norm_rotary_backward of include/fa.h: from the gradients dq_out and dk_out of
+    fa_norm_rotary's outputs and its inputs q and k, writes those of its inputs, dq and dk, and of
+    the weights, fp32 [d] (None: not wanted)."""
+    if not (k is None) == (dk_out is None) == (dk is None):
+        raise ValueError("give k, dk_out and dk, or none of them")
+    if k is None and dk_weight is not None:
+        raise ValueError("dk_weight without k")
+    device = norm.device
+    call = _norm_call(dq_out, dk_out, norm, positions, rotary)
+    rows = (_rotary_rows(dq_out, dq, device, "dq"),
+            None if k is None else _rotary_rows(dk_out, dk, device, "dk"),
+            _input_rows(q, dq_out, device, "q"),
+            None if k is None else _input_rows(k, dk_out, device, "k"))
+    _launch_norm_backward(rows, dq_weight, dk_weight, workspace, call, stream, device)
+
+
+def _launch_norm_backward(rows, dq_weight, dk_weight, workspace, call, stream, device):
+    B, N, d, norm, at, axis, batch, ref = call
+    for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if w is not None and (w.dtype is not _F32 or w.get_device() != device or
+                              w.shape != (d,) or not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous fp32 CUDA vector of {d} values")
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor of the norms' device")
+    status = library().fa_norm_rotary_backward(
+        *rows, B, N, d, norm, None if dq_weight is None else dq_weight.data_ptr(),
+        None if dk_weight is None else dk_weight.data_ptr(), at, axis, batch, ref,
+        workspace.data_ptr(), workspace.nbytes, _stream(stream, device))
+    if status:
+        raise FaError(status, "fa_norm_rotary_backward")
+
+
+def norm_rotary_backward(dq, dk, q, k, norm, positions=None, rotary=None, stream=None):
+    """Gradients of norm_rotary_forward's inputs and of both norms' weights (fp32 [d]), from those
+    of its outputs (for instance what attention_backward returns) and its inputs q and k (dk and k
+    None: of q alone); returns (dq, dk, dq_weight, dk_weight)."""
+    if stream is not None:
+        with _on(stream):
+            return _new_norm_backward(dq, dk, q, k, norm, positions, rotary, stream)
+    return _new_norm_backward(dq, dk, q, k, norm, positions, rotary, None)
+
+
+def _new_norm_backward(dq_out, dk_out, q, k, norm, positions, rotary, stream):
+    if (k is None) != (dk_out is None):
+        raise ValueError("give k and dk, or neither")
+    device = norm.device
+    call = _norm_call(dq_out, dk_out, norm, positions, rotary)
+    d = call[2]
+    dq, rows_q = _new_rows(dq_out, device, "dq")
+    dk = rows_k = in_k = None
+    if k is not None:
+        dk, rows_k = _new_rows(dk_out, device, "dk")
+        in_k = _input_rows(k, dk_out, device, "k")
+    weights = _torch.empty((1 if k is None else 2, d), dtype=_F32, device=dq.device)
+    dk_weight = None if k is None else weights[1]
+    _launch_norm_backward((rows_q, rows_k, _input_rows(q, dq_out, device, "q"), in_k), weights[0],
+                          dk_weight, norm_rotary_workspace(d, dq.device), call, stream, device)
+    return dq, dk, weights[0], dk_weight
+
+
 def _new_turn(fn, q, k, positions, rotary, stream):
     if stream is not None:
         with _on(stream):
@@ -314,10 +494,11 @@ def _new_turn_here(fn, q, k, positions, rotary, stream):
 
 
 def fa_paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, q_out=None,
-                    stream=None):
+                    stream=None, norm=None):
     """fa_paged_append of include/fa.h: stores the step's k and v [T, H_kv, d] (bf16 views) in
     the cache, k turned by `rotary` at `positions` ([axes, T] int32, or [T] for one axis; None:
-    each token's place in its sequence), and writes q [T, H_q, d] turned likewise to q_out."""
+    each token's place in its sequence), and writes q [T, H_q, d] turned likewise to q_out.  With
+    `norm`, a HeadNorm, fa_paged_append_norm: k and q are normed before they are turned."""
     device = cache.device
     ks = _rows3("k", k, device)
     vs = _rows3("v", v, device)
@@ -325,8 +506,11 @@ def fa_paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, q_o
     if v.shape != shape or H != cache.H_kv or d != cache.d:
         raise ValueError(f"k and v must be [T, {cache.H_kv}, {cache.d}]")
     if batch.device != device or device != _device() or \
-            (rotary is not None and rotary.device != device):
-        _same_device(device, batch, rotary)
+            (rotary is not None and rotary.device != device) or \
+            (norm is not None and norm.device != device):
+        _same_device(device, batch, rotary, norm)
+    if norm is not None:
+        norm._check(d)
     qp = op = None
     q_token = q_head = o_token = o_head = Hq = 0
     if q is not None and q_out is not None:
@@ -358,6 +542,14 @@ def fa_paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, q_o
         pp, axis_stride = positions.data_ptr(), s[0]
     if T == 0 or batch.S == 0:
         return
+    if norm is not None:
+        status = library().fa_paged_append_norm(
+            cache._ref, batch._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], T, qp,
+            q_token, q_head, op, o_token, o_head, Hq, norm._ref, ref, pp, axis_stride,
+            _stream(stream, device))
+        if status:
+            raise FaError(status, "fa_paged_append_norm")
+        return
     status = library().fa_paged_append(
         cache._ref, batch._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], T, qp,
         q_token, q_head, op, o_token, o_head, Hq, ref, pp, axis_stride, _stream(stream, device))
@@ -365,7 +557,7 @@ def fa_paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, q_o
         raise FaError(status, "fa_paged_append")
 
 
-def paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, stream=None):
+def paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, stream=None, norm=None):
     """fa_paged_append with a q_out of its own, which it returns (None without q).  Rows past
     the last sequence are left as the allocation has them."""
     q_out = None
@@ -375,7 +567,7 @@ def paged_append(cache, batch, k, v, rotary=None, positions=None, q=None, stream
                 q_out = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
         else:
             q_out = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    fa_paged_append(cache, batch, k, v, rotary, positions, q, q_out, stream)
+    fa_paged_append(cache, batch, k, v, rotary, positions, q, q_out, stream, norm)
     return q_out
 
 

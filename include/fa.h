@@ -369,6 +369,53 @@ fa_status fa_rotary_backward(const fa_rotary_rows* q, const fa_rotary_rows* k, i
                              const int* positions, long long axis_stride, long long batch_stride,
                              const fa_rotary_spec* spec, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- norms of the heads' rows
+ *
+ * Models that norm the queries and keys of each head do so right before the rotation; here both
+ * are one pass.  For a row x of a head, and its weights w,
+ *     u = x / sqrt(mean(x^2) + eps),   y = turn(u o w)
+ * in fp32, each output rounded once.  The squares of a row must sum within fp32's range.
+ */
+#define FA_NORM_F32 0
+#define FA_NORM_BF16 1
+
+typedef struct {
+  const void* q_weight; /* device, [d], 16-byte aligned; NULL: ones */
+  const void* k_weight;
+  int weight_dtype;     /* FA_NORM_F32 or FA_NORM_BF16, of both */
+  float eps;            /* finite, > 0 */
+} fa_head_norm;
+
+/*
+ * fa_rotary of the normed rows, in one launch.  spec NULL: the rows are normed and not turned
+ * (positions are then not read and may be NULL).  Otherwise as fa_rotary.
+ */
+fa_status fa_norm_rotary(const fa_rotary_rows* q, const fa_rotary_rows* k, int B, int N, int d,
+                         const fa_head_norm* norm, const int* positions, long long axis_stride,
+                         long long batch_stride, const fa_rotary_spec* spec, cudaStream_t stream);
+
+/*
+ * Its gradients: with g the gradient of y turned back,
+ *     dx = (g o w - u mean(g o w o u)) / sqrt(mean(x^2) + eps),   dw = sum over rows of g o u
+ *   dq, dk     in = gradients of fa_norm_rotary's outputs, out = gradients of its inputs, which
+ *              may be `in`, or the rows of q and k, with the same strides
+ *   q, k       in = fa_norm_rotary's inputs (out is not used); as many heads
+ *   dq_weight, dk_weight   device fp32 [d], written; NULL: not wanted
+ *   workspace  device memory of at least fa_norm_rotary_backward_workspace_bytes(d), 16-byte
+ *              aligned; its contents do not matter before or after.  Calls whose work can
+ *              overlap (other streams, other captured graphs) need one each.
+ * Sums are fp32 in a fixed order: results repeat to the bit.
+ */
+fa_status fa_norm_rotary_backward(const fa_rotary_rows* dq, const fa_rotary_rows* dk,
+                                  const fa_rotary_rows* q, const fa_rotary_rows* k, int B, int N,
+                                  int d, const fa_head_norm* norm, float* dq_weight,
+                                  float* dk_weight, const int* positions, long long axis_stride,
+                                  long long batch_stride, const fa_rotary_spec* spec,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace for fa_norm_rotary_backward on the current device; 0 for other d. */
+size_t fa_norm_rotary_backward_workspace_bytes(int d);
+
 /* ---------------------------------------------------------------- paged key/value cache
  *
  * The keys and values of many sequences lie in pages of page_size positions,
@@ -434,6 +481,18 @@ fa_status fa_paged_append(const fa_paged_cache* cache, const fa_paged_batch* bat
                           long long q_head, void* q_out, long long qo_token, long long qo_head,
                           int H_q, const fa_rotary_spec* spec, const int* positions,
                           long long axis_stride, cudaStream_t stream);
+
+/*
+ * fa_paged_append with the norms of fa_norm_rotary on the way: k (and q) are normed, turned and
+ * stored, v is stored as it is.  Otherwise as fa_paged_append.
+ */
+fa_status fa_paged_append_norm(const fa_paged_cache* cache, const fa_paged_batch* batch,
+                               const void* k, long long k_token, long long k_head, const void* v,
+                               long long v_token, long long v_head, int T, const void* q,
+                               long long q_token, long long q_head, void* q_out, long long qo_token,
+                               long long qo_head, int H_q, const fa_head_norm* norm,
+                               const fa_rotary_spec* spec, const int* positions,
+                               long long axis_stride, cudaStream_t stream);
 
 /*
  * Attention of the step's new tokens over the cache (which holds them already:
