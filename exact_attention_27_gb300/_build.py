@@ -16,7 +16,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_tile1.cu", "fa_fwd_pair.cu", "fa_bwd.cu", "fa_bwd_d64.cu",
            "fa_bwd_d256.cu", "fa_bwd_dq.cu", "fa_noalloc.cu", "fa_rotary.cu", "fa_norm.cu", "fa_paged.cu",
-           "fa_paged_tile.cu", "fa_paged_tile2.cu", "fa_scores.cu", "fa_scores_d64.cu",
+           "fa_paged_tile.cu", "fa_paged_tile2.cu", "fa_paged_scores.cu", "fa_paged_scores2.cu",
+           "fa_scores.cu", "fa_scores_d64.cu",
            "fa_scores_d96.cu", "fa_scores_d128.cu", "fa_scores_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,

@@ -127,6 +127,9 @@ def _declare(lib):
     lib.fa_forward_paged.restype = i
     lib.fa_forward_paged.argtypes = [p, p, p, ll, ll, p, ll, ll, p, i, i, f, i, p,
                                      ctypes.c_size_t, p]
+    lib.fa_forward_paged_scores.restype = i
+    lib.fa_forward_paged_scores.argtypes = [p, p, p, ll, ll, p, ll, ll, p, i, i, f, i, p, p,
+                                            ctypes.c_size_t, p]
     lib.fa_forward_paged_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_forward_paged_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.fa_status_string.restype = ctypes.c_char_p

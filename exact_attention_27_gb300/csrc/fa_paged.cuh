@@ -110,6 +110,11 @@ struct PagedParams {
   int min_units;           // units that are worth a CTA
   float scale_log2;        // scale * log2(e) * k_descale
   float v_scale;
+  // Shaped scores (fa_score_spec; the SHAPED kernels): softcap log2(e), 0: none; slopes, nullptr:
+  // none; window, 0: none.
+  float cap2;
+  const float* slopes;
+  int window;
   float* part_o;           // [CTA][2][ROWS][D]
   float2* part_ml;         // [CTA][2][ROWS]
   PagedNote* notes;        // [CTA]
@@ -130,6 +135,7 @@ __device__ __forceinline__ long long paged_div(long long a, long long b) {
 // do for the append.
 struct PagedSeq {
   int q0, qlen, klen;
+  int base;  // position of its first row's token
 };
 
 __device__ __forceinline__ int paged_room(const PagedParams& p) {
@@ -141,15 +147,19 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int s) {
   g.q0 = min(max(p.q_start[s], 0), p.T);
   const int end = max(p.q_start[s + 1], g.q0);
   g.qlen = min(end, p.T) - g.q0;
-  g.klen = min(max(p.kv_len[s], 0), paged_room(p)) - (p.causal ? max(end - p.T, 0) : 0);
+  const int len = min(max(p.kv_len[s], 0), paged_room(p));
+  g.klen = len - (p.causal ? max(end - p.T, 0) : 0);
+  g.base = len - (end - g.q0);
   return g;
 }
 
 // Items of ROWS rows and key tiles of TK keys.  An item counts for its key
 // tiles and OVER more, about what starting and ending one costs, at FULL units each,
-// or HALF where its rows fill at most half of ROWS.
-template <int ROWS_, int TK_, int OVER_, int FULL_ = 1, int HALF_ = 1>
+// or HALF where its rows fill at most half of ROWS.  SHAPED: the scores are shaped, and an
+// item's key tiles begin with that of the first key in its first token's window.
+template <int ROWS_, int TK_, int OVER_, bool SHAPED_, int FULL_ = 1, int HALF_ = 1>
 struct PagedWalk {
+  static constexpr bool SHAPED = SHAPED_;
   static constexpr int ROWS = ROWS_, TK = TK_, OVER = OVER_, FULL = FULL_, HALF = HALF_;
   int s, h, rt, n_rt;
   PagedSeq g;
@@ -165,9 +175,16 @@ struct PagedWalk {
                                      static_cast<uint32_t>(p.G)) + 1);
     return max(g.klen - g.qlen + tokens, 0);
   }
+  // First key that any row of row tile rt sees.
+  static __device__ __forceinline__ int first_key(const PagedParams& p, const PagedSeq& g,
+                                                  int rt) {
+    if (!SHAPED || p.window == 0) return 0;
+    const int tok = static_cast<int>(static_cast<uint32_t>(rt * ROWS) / static_cast<uint32_t>(p.G));
+    return max(g.base + tok - p.window + 1, 0);
+  }
   // Its key tiles: one at least, so that rows without keys are written too.
   static __device__ __forceinline__ int tiles(const PagedParams& p, const PagedSeq& g, int rt) {
-    return max((keys(p, g, rt) + TK - 1) / TK, 1);
+    return max((keys(p, g, rt) + TK - 1) / TK - first_key(p, g, rt) / TK, 1);
   }
   // Whether row tile rt has at most half an item's rows.
   static __device__ __forceinline__ bool half(const PagedParams& p, const PagedSeq& g, int rt) {
@@ -184,7 +201,7 @@ struct PagedWalk {
   static __device__ __forceinline__ long long head_units(const PagedParams& p, const PagedSeq& g) {
     constexpr int SHORT = 4;
     const int n = row_tiles(p, g);
-    if (!p.causal)  // (all but the last are alike)
+    if (!p.causal && !(SHAPED && p.window > 0))  // (all but the last are alike)
       return n == 0 ? 0 : static_cast<long long>(n - 1) * units(p, g, 0) + units(p, g, n - 1);
     long long u = 0;
     if (n <= SHORT) {
@@ -198,6 +215,7 @@ struct PagedWalk {
       x.q0 = 0;
       x.qlen = __shfl_sync(0xffffffffu, g.qlen, src);
       x.klen = __shfl_sync(0xffffffffu, g.klen, src);
+      x.base = SHAPED ? __shfl_sync(0xffffffffu, g.base, src) : 0;
       const int m = __shfl_sync(0xffffffffu, n, src);
       long long sum = 0;
       for (int rt = lane; rt < m; rt += 32) sum += units(p, x, rt);
@@ -286,7 +304,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
     return before + x - mine;
   };
   auto units_of = [&](int s) -> long long {
-    PagedSeq g{0, 0, 0};
+    PagedSeq g{0, 0, 0, 0};
     if (s < p.S) {
       g = paged_seq(p, s);
       if (blockIdx.x == 0 && p.kv_len[s] > paged_room(p)) atomicOr(p.err, kErrBadPage);
@@ -362,19 +380,22 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, long lon
 }
 
 // A CTA's segments: the items of its range one after the other, each with the
-// key tiles [t0, t1) that lie in the range.  Every role walks them on its own,
-// from a common start.
+// key tiles [t0, t1) that lie in the range; tile t holds keys (tile0() + t) TK on.
+// Every role walks them on its own, from a common start.
 template <typename Walk>
 struct PagedSegments {
   Walk w;
   long long unit, end;  // where the item's part of the range begins; the range's end
   int t0, t1, tiles, keys, used;
+  int first;  // first key that the item's rows see (a window's; 0 otherwise)
+  __device__ __forceinline__ int tile0() const { return Walk::SHAPED ? first / Walk::TK : 0; }
   __device__ __forceinline__ int weight(const PagedParams& p) const {
     return Walk::weight(p, w.g, w.rt);
   }
   __device__ __forceinline__ void load(const PagedParams& p, int at) {
     tiles = Walk::tiles(p, w.g, w.rt);
     keys = Walk::keys(p, w.g, w.rt);
+    first = Walk::first_key(p, w.g, w.rt);
     const int wt = weight(p);
     used = static_cast<int>(
         min(static_cast<long long>((tiles + Walk::OVER) * wt - at), end - unit));

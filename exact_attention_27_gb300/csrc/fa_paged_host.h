@@ -38,5 +38,15 @@ cudaError_t launch_paged_tile(const CUtensorMap& tk, const CUtensorMap& tv, cons
                               bool e4m3, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_tile2(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
                                int d, bool e4m3, int ctas, cudaStream_t stream);
+// The same kernels for shaped scores (fa_paged_scores.cu).
+cudaError_t launch_paged_rows_shaped(const CUtensorMap& tk, const CUtensorMap& tv,
+                                     const PagedParams& p, int d, bool e4m3, int ctas,
+                                     cudaStream_t stream);
+cudaError_t launch_paged_tile_shaped(const CUtensorMap& tk, const CUtensorMap& tv,
+                                     const PagedParams& p, bool e4m3, int ctas,
+                                     cudaStream_t stream);
+cudaError_t launch_paged_tile2_shaped(const CUtensorMap& tk, const CUtensorMap& tv,
+                                      const PagedParams& p, int d, bool e4m3, int ctas,
+                                      cudaStream_t stream);
 
 }  // namespace fa

@@ -9,6 +9,7 @@
 
 #include "fa_paged.cuh"
 #include "fa_ptx.cuh"
+#include "fa_scores.cuh"
 
 namespace fa {
 
@@ -40,6 +41,10 @@ struct PagedRow {
   int head;        // query head
   int last;        // last key it sees
   int all_see;     // last key that every row of the item sees
+  int first;       // first key it sees, and the last of the item's rows' first ones (0 unless
+  int all_from;    // a window says otherwise)
+  int pos;         // its token's position (shaped scores)
+  float slope2;    // slope log2(e) of its head (shaped scores)
   long long token;
 };
 
@@ -55,6 +60,17 @@ __device__ __forceinline__ PagedRow paged_row(const PagedParams& p, const PagedS
   x.last = p.causal ? base + tok : s.w.g.klen - 1;
   x.all_see = p.causal ? base + s.w.rt * Walk::ROWS / p.G : s.w.g.klen - 1;
   x.token = s.w.g.q0 + tok;
+  x.first = x.all_from = x.pos = 0;
+  x.slope2 = 0.0f;
+  if constexpr (Walk::SHAPED) {
+    x.pos = s.w.g.base + tok;
+    if (p.slopes) x.slope2 = p.slopes[x.head] * kPagedLog2e;
+    if (p.window > 0) {
+      x.first = x.pos - p.window + 1;
+      const int last_row = min(s.w.rt * Walk::ROWS + Walk::ROWS, s.w.g.qlen * p.G) - 1;
+      x.all_from = s.w.g.base + last_row / p.G - p.window + 1;
+    }
+  }
   return x;
 }
 
@@ -127,13 +143,14 @@ __device__ __forceinline__ float paged_load_q(const PagedParams& p, const PagedR
 }
 
 // A tile of BN keys from e4m3 bytes (at `raw`, as the copies leave them) to the
-// fp16 tile at `dst`, rows from `keep` on as zeros; 128 threads.
+// fp16 tile at `dst`, rows before `from` and from `keep` on as zeros; 128 threads.
 template <int D, int BN>
-__device__ __forceinline__ void paged_convert(uint32_t raw, uint32_t dst, int keep, int tid) {
+__device__ __forceinline__ void paged_convert(uint32_t raw, uint32_t dst, int from, int keep,
+                                              int tid) {
   constexpr int PER = 128 / BN;  // threads a row
   constexpr int N = 4;           // chunks of 16 values in flight
   const int r = tid % BN;
-  const bool key = r < keep;
+  const bool key = r >= from && r < keep;
 #pragma unroll
   for (int c0 = 0; c0 < D / 16; c0 += N * PER) {
     uint4 v[N];
@@ -159,11 +176,11 @@ __device__ __forceinline__ void paged_convert(uint32_t raw, uint32_t dst, int ke
   }
 }
 
-// Rows `first`.. of the bf16 tile of BN keys at `v` as zeros; THREADS threads.
+// Rows first .. end - 1 of the bf16 tile at `v` (of BN keys) as zeros; THREADS threads.
 template <int SUB, int BN, int THREADS>
-__device__ __forceinline__ void paged_zero_rows(uint32_t v, int first, int tid) {
+__device__ __forceinline__ void paged_zero_rows(uint32_t v, int first, int end, int tid) {
   constexpr int CHUNKS = SUB * 8;  // 16-byte chunks of a row
-  for (int x = first * CHUNKS + tid; x < BN * CHUNKS; x += THREADS) {
+  for (int x = first * CHUNKS + tid; x < end * CHUNKS; x += THREADS) {
     const int r = x / CHUNKS, c = x % CHUNKS;
     sts128(v + (c >> 3) * (BN * 128) + r * 128 + ((c & 7) << 4), make_uint4(0, 0, 0, 0));
   }
@@ -173,23 +190,36 @@ __device__ __forceinline__ void paged_zero_rows(uint32_t v, int first, int tid) 
 // running reference m and sum l (base 2, scores times c).  `see`: the last key of
 // the tile that the row sees, if `mask`.  m is the reference that P is relative to
 // (fa_paged.cuh); returns the factor that O and the old l are due (1 while it stays).
-template <int BN, bool F16>
-__device__ __forceinline__ float paged_softmax(uint32_t s_addr, bool mask, int see, float c,
+// SHAPED: the scores are capped and lowered first (kbase: the tile's first key), and keys
+// before x.first are not seen either.
+template <int BN, bool F16, bool SHAPED>
+__device__ __forceinline__ float paged_softmax(const PagedParams& p, const PagedRow& x,
+                                               uint32_t s_addr, bool mask, int kbase, float c,
                                                float& m, float& l, bool& moved) {
+  const int see = x.last - kbase;
   float s[BN];
   {
-    uint32_t x[BN];
+    uint32_t raw[BN];
 #pragma unroll
     for (int q4 = 0; q4 < BN / 32; ++q4)
-      tmem_ld32(s_addr + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[q4 * 32]));
+      tmem_ld32(s_addr + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[q4 * 32]));
     tmem_wait_ld();
 #pragma unroll
-    for (int k = 0; k < BN; ++k) s[k] = __uint_as_float(x[k]);
+    for (int k = 0; k < BN; ++k) s[k] = __uint_as_float(raw[k]);
+  }
+  if constexpr (SHAPED) {
+    float none[1];
+    if (p.cap2 > 0.0f)
+      shape_scores<BN, true, false, false>(s, none, c / p.cap2, p.cap2, 0.0f, 0.0f, 0.0f);
+    else
+      shape_scores<BN, false, false, false>(s, none, c, 0.0f, 0.0f, 0.0f, 0.0f);
+    if (p.slopes) lower_scores<BN>(s, x.slope2, static_cast<float>(x.pos - kbase));
+    c = 1.0f;
   }
   if (mask) {
 #pragma unroll
     for (int k = 0; k < BN; ++k)
-      if (k > see) s[k] = -INFINITY;
+      if (k > see || (SHAPED && k < x.first - kbase)) s[k] = -INFINITY;
   }
   // Row maximum over 8 partial maxima, two new values each time.
   float pm[8];

@@ -73,31 +73,39 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// Scores of keys kbase + t less slope2 |pos - key|, dist0 = pos - kbase (distances are whole
+// numbers, exact in fp32 up to 2^24).
+template <int N>
+__device__ __forceinline__ void lower_scores(float (&s)[N], float slope2, float dist0) {
+#pragma unroll
+  for (int t = 0; t < N; ++t) s[t] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(t)), s[t]);
+}
+
 // What turns raw products s = q.k of keys kbase + t, t = 0 .. N-1, into exponents of the
-// weights, x (log2 domain), less `sub`:  CAP x = cap2 tanh(s y_scale), else x = s scale2;
-// BIAS then - slope2 |pos - key|.  With GRAD, g gets 1 - tanh^2.  The whole warp calls this.
+// weights, x (log2 domain), less `sub`:  CAP x = cap2 tanh(s k), else x = s k;
+// BIAS then - slope2 |pos - key|, dist0 = pos - kbase.  With GRAD, g gets 1 - tanh^2.  The
+// whole warp calls this (k may differ between its lanes).
 template <int N, bool CAP, bool BIAS, bool GRAD>
-__device__ __forceinline__ void shape_scores(const ScoreParams& p, float (&s)[N],
-                                             float (&g)[GRAD ? N : 1], float slope2, float dist0,
-                                             float sub) {
+__device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N : 1], float k,
+                                             float cap2, float slope2, float dist0, float sub) {
   if constexpr (CAP) {
-    const uint64_t k2 = f2_pack(p.y_scale, p.y_scale);
+    const uint64_t k2 = f2_pack(k, k);
     float big = 0.0f;
 #pragma unroll
     for (int t = 0; t < N; t += 2) big = fmax3(big, fabsf(s[t]), fabsf(s[t + 1]));
     // (a NaN takes either way to a NaN)
-    if (__any_sync(0xffffffffu, big * p.y_scale > kTanhRange)) {
+    if (__any_sync(0xffffffffu, big * k > kTanhRange)) {
 #pragma unroll
       for (int t = 0; t < N; ++t) {
-        const float r = rcp_approx(ex2_approx(s[t] * (2.0f * kScoreLog2e * p.y_scale)) + 1.0f);
-        s[t] = fmaf(-2.0f * p.cap2, r, p.cap2) - sub;
+        const float r = rcp_approx(ex2_approx(s[t] * (2.0f * kScoreLog2e * k)) + 1.0f);
+        s[t] = fmaf(-2.0f * cap2, r, cap2) - sub;
         if constexpr (GRAD) g[t] = 4.0f * r * (1.0f - r);
       }
     } else {
       const uint64_t c0 = f2_pack(kTanhC0, kTanhC0), c1 = f2_pack(kTanhC1, kTanhC1);
       const uint64_t c2 = f2_pack(kTanhC2, kTanhC2), c3 = f2_pack(kTanhC3, kTanhC3);
       const uint64_t c4 = f2_pack(kTanhC4, kTanhC4);
-      const uint64_t cap = f2_pack(p.cap2, p.cap2), ns = f2_pack(-sub, -sub);
+      const uint64_t cap = f2_pack(cap2, cap2), ns = f2_pack(-sub, -sub);
       const uint64_t one = f2_pack(1.0f, 1.0f), minus = f2_pack(-1.0f, -1.0f);
 #pragma unroll
       for (int t = 0; t < N; t += 2) {
@@ -110,17 +118,12 @@ __device__ __forceinline__ void shape_scores(const ScoreParams& p, float (&s)[N]
       }
     }
   } else {
-    const uint64_t c = f2_pack(p.scale2, p.scale2), ns = f2_pack(-sub, -sub);
+    const uint64_t c = f2_pack(k, k), ns = f2_pack(-sub, -sub);
 #pragma unroll
     for (int t = 0; t < N; t += 2)
       f2_unpack(f2_fma(f2_pack(s[t], s[t + 1]), c, ns), s[t], s[t + 1]);
   }
-  if constexpr (BIAS) {
-    // dist0 = pos - kbase: distances are whole numbers, exact in fp32 up to 2^24
-#pragma unroll
-    for (int t = 0; t < N; ++t)
-      s[t] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(t)), s[t]);
-  }
+  if constexpr (BIAS) lower_scores<N>(s, slope2, dist0);
 }
 
 // Byte offset of 16-byte chunk `ch` of row `r` in a 128-byte-swizzled block of 128-byte rows.

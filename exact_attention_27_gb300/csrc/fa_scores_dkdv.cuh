@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(320, 1)
         for (int t = 0; t < 64; ++t) w[t] = __uint_as_float(sv[t]);
       }
       shape_scores<64, CAP, BIAS, CAP>(
-          p.s, w, gr, slope2, static_cast<float>(p.s.q_offset + it * C::BQ + row - kbase), L2);
+          w, gr, p.s.factor(CAP), p.s.cap2, slope2,
+          static_cast<float>(p.s.q_offset + it * C::BQ + row - kbase), L2);
 #pragma unroll
       for (int t = 0; t < 64; ++t) w[t] = ex2_approx(w[t]);
       if (masked) {

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(320, 1)
       const int kbase = key_tile(j) * C::BN + KH * g;
       const bool need_mask = __any_sync(0xffffffffu, span.lo > kbase || span.hi < kbase + KH);
       float gr[CAP ? KH : 1];
-      shape_scores<KH, CAP, BIAS, CAP>(p.s, s, gr, slope2,
+      shape_scores<KH, CAP, BIAS, CAP>(s, gr, p.s.factor(CAP), p.s.cap2, slope2,
                                        static_cast<float>(p.s.q_offset + qi - kbase), L2);
       if (j < n_sum) {
         // D = sum of P dP, of both halves of the row's keys.

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(192, 1)
       const bool need_mask =
           __any_sync(0xffffffffu, span.lo > kbase || span.hi < kbase + C::BN);
       float none[1];
-      shape_scores<C::BN, CAP, BIAS, false>(p.s, s, none, slope2,
+      shape_scores<C::BN, CAP, BIAS, false>(s, none, p.s.factor(CAP), p.s.cap2, slope2,
                                             static_cast<float>(pos - kbase),
                                             FIXED ? m_used : 0.0f);
       if (need_mask) {

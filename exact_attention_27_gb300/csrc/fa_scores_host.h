@@ -16,6 +16,8 @@ struct ScoreParams {
   float scale2;   // scale log2(e)
   float y_scale;  // scale / softcap
   float cap2;     // softcap log2(e); 0: none
+  // The factor of q.k that the kernels take.
+  __host__ __device__ float factor(bool cap) const { return cap ? y_scale : scale2; }
   const float* slopes;  // [Hq], nullptr: none
   const int* first;
   const int* end;

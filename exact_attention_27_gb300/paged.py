@@ -582,9 +582,10 @@ def paged_workspace(cache, batch, q):
     return _torch.empty(n, dtype=_torch.uint8, device=q.device)
 
 
-def fa_forward_paged(cache, batch, q, o, lse, scale, causal, workspace, stream=None):
+def fa_forward_paged(cache, batch, q, o, lse, scale, causal, workspace, stream=None, scores=None):
     """fa_forward_paged of include/fa.h: the step's q [T, H_q, d] (a bf16 view) against the
-    cache; writes o (like q) and lse [T, H_q] fp32 (None: not wanted)."""
+    cache; writes o (like q) and lse [T, H_q] fp32 (None: not wanted).  With `scores`, a Scores,
+    fa_forward_paged_scores: capped, lowered with the distance, seen through a window."""
     device = cache.device
     q_token, q_head, _ = _rows3("q", q, device)
     o_token, o_head, _ = _rows3("o", o, device)
@@ -602,7 +603,17 @@ def fa_forward_paged(cache, batch, q, o, lse, scale, causal, workspace, stream=N
         lp = lse.data_ptr()
     if workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor of the cache's device")
+    if scores is not None:
+        scores._check(Hq, device)
     if T == 0 or batch.S == 0:
+        return
+    if scores is not None:
+        status = library().fa_forward_paged_scores(
+            cache._ref, batch._ref, q.data_ptr(), q_token, q_head, o.data_ptr(), o_token, o_head,
+            lp, T, Hq, scale, 1 if causal else 0, scores._ref, workspace.data_ptr(),
+            workspace.nbytes, _stream(stream, device))
+        if status:
+            raise FaError(status, "fa_forward_paged_scores")
         return
     status = library().fa_forward_paged(
         cache._ref, batch._ref, q.data_ptr(), q_token, q_head, o.data_ptr(), o_token, o_head, lp,
@@ -612,20 +623,21 @@ def fa_forward_paged(cache, batch, q, o, lse, scale, causal, workspace, stream=N
         raise FaError(status, "fa_forward_paged")
 
 
-def paged_attention(cache, batch, q, causal=True, scale=None, stream=None):
-    """Allocates o, lse and the workspace and runs fa_forward_paged; returns (o, lse).  Rows
-    past the last sequence are left as the allocations have them."""
+def paged_attention(cache, batch, q, causal=True, scale=None, stream=None, scores=None):
+    """Allocates o, lse and the workspace and runs fa_forward_paged (fa_forward_paged_scores with
+    `scores`); returns (o, lse).  Rows past the last sequence are left as the allocations have
+    them."""
     if stream is not None:
         with _on(stream):
-            return _paged_attention(cache, batch, q, causal, scale, stream)
-    return _paged_attention(cache, batch, q, causal, scale, stream)
+            return _paged_attention(cache, batch, q, causal, scale, stream, scores)
+    return _paged_attention(cache, batch, q, causal, scale, stream, scores)
 
 
-def _paged_attention(cache, batch, q, causal, scale, stream):
+def _paged_attention(cache, batch, q, causal, scale, stream, scores):
     if scale is None:
         scale = 1.0 / math.sqrt(cache.d)
     o = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
     lse = _torch.empty(q.shape[:2], dtype=_F32, device=q.device)
     fa_forward_paged(cache, batch, q, o, lse, scale, causal, paged_workspace(cache, batch, q),
-                     stream)
+                     stream, scores)
     return o, lse

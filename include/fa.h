@@ -523,6 +523,20 @@ fa_status fa_forward_paged(const fa_paged_cache* cache, const fa_paged_batch* ba
                            long long o_head, float* lse, int T, int H_q, float scale, int causal,
                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * fa_forward_paged with shaped scores (fa_score_spec, NULL: none): scores are capped, lowered
+ * with the distance of the token's position (kv_len - q_len + i) from the key's, and seen
+ * through the window.  Pages that lie wholly before the windows of all of a sequence's new tokens
+ * are not read, nor are their entries of the block table, so a server may have given them up;
+ * within the first page read, the values before the windows are not used, whatever their bits.
+ * Otherwise as fa_forward_paged, with its workspace.
+ */
+fa_status fa_forward_paged_scores(const fa_paged_cache* cache, const fa_paged_batch* batch,
+                                  const void* q, long long q_token, long long q_head, void* o,
+                                  long long o_token, long long o_head, float* lse, int T, int H_q,
+                                  float scale, int causal, const fa_score_spec* spec,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Bytes of workspace for fa_forward_paged on the current device; 0 for sizes it rejects. */
 size_t fa_forward_paged_workspace_bytes(int H_q, int H_kv, int d, int T, int max_q_len);
 

@@ -178,3 +178,34 @@ def test_bounds_notice_mistakes(mistake):
         # (a causal row's scores all fall by the slope: lse alone shows it)
         assert off_by(got["lse"], val["lse"], tol["lse"]) > 3
     assert worst > 3, worst
+
+
+# ------------------------------------------------------------------ over a paged cache
+
+def paged(lib, s, c=None, **kw):
+    from test_paged_cpu import batch, cache
+    a = dict(q=P, qt=256, qh=64, o=P, ot=256, oh=64, lse=P, T=2, Hq=4, scale=0.125, causal=1, ws=P,
+             bytes=2 ** 40)
+    a.update(kw)
+    ref = ctypes.byref
+    return lib.fa_forward_paged_scores(
+        ref(c or cache()), ref(batch()), a["q"], a["qt"], a["qh"], a["o"], a["ot"], a["oh"],
+        a["lse"], a["T"], a["Hq"], ctypes.c_float(a["scale"]), a["causal"],
+        None if s is None else ref(s), a["ws"], a["bytes"], None)
+
+
+@pytest.mark.parametrize("s", [spec(-1.0), spec(float("nan")), spec(float("inf")), spec(1e-40),
+                               spec(3e38), spec(slopes=F), spec(window=-1)])
+def test_paged_rejects_bad_scores(lib, s):
+    assert paged(lib, s) == fa.FA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("kw", [dict(q=None), dict(o=Q), dict(lse=F), dict(T=-1), dict(Hq=3),
+                                dict(scale=0.0), dict(causal=2), dict(qt=4), dict(ot=0)])
+def test_paged_rejects(lib, kw):
+    assert paged(lib, spec(10.0), **kw) == fa.FA_ERR_INVALID_ARGUMENT
+
+
+def test_paged_with_nothing_to_do_needs_no_gpu(lib):
+    assert paged(lib, spec(10.0), T=0, q=None, o=None, ws=None) == fa.FA_OK
+    assert paged(lib, None, T=0, q=None, o=None, ws=None) == fa.FA_OK
