@@ -67,6 +67,13 @@ __device__ __forceinline__ KeySpan warp_hull(const KeySpan& s) {
   return h;
 }
 
+// Largest magnitude of three.
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -90,9 +97,16 @@ __device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N 
                                              float cap2, float slope2, float dist0, float sub) {
   if constexpr (CAP) {
     const uint64_t k2 = f2_pack(k, k);
-    float big = 0.0f;
+    constexpr int CHAINS = N < 16 ? 1 : 4;  // independent maxima
+    float part[CHAINS];
 #pragma unroll
-    for (int t = 0; t < N; t += 2) big = fmax3(big, fabsf(s[t]), fabsf(s[t + 1]));
+    for (int u = 0; u < CHAINS; ++u) part[u] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < N; t += 2)
+      part[t / 2 % CHAINS] = fmax3_abs(part[t / 2 % CHAINS], s[t], s[t + 1]);
+    float big = part[0];
+#pragma unroll
+    for (int u = 1; u < CHAINS; ++u) big = fmaxf(big, part[u]);
     // (a NaN takes either way to a NaN)
     if (__any_sync(0xffffffffu, big * k > kTanhRange)) {
 #pragma unroll
@@ -124,6 +138,16 @@ __device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N 
       f2_unpack(f2_fma(f2_pack(s[t], s[t + 1]), c, ns), s[t], s[t + 1]);
   }
   if constexpr (BIAS) lower_scores<N>(s, slope2, dist0);
+}
+
+// TMEM -> registers, 16 or 32 consecutive columns.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 16 || N == 32, "columns");
+  if constexpr (N == 16)
+    tmem_ld16(taddr, r);
+  else
+    tmem_ld32(taddr, r);
 }
 
 // Byte offset of 16-byte chunk `ch` of row `r` in a 128-byte-swizzled block of 128-byte rows.

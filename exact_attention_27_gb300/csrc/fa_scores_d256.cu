@@ -1,7 +1,7 @@
 // The kernels of attention with shaped scores at head dimension 256.
 #include "fa_scores_dq.cuh"
-#include "fa_scores_fwd.cuh"
 #include "fa_scores_kv256.cuh"
+#include "fa_scores_launch.cuh"
 
 namespace fa {
 

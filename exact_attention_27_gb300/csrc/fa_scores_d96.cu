@@ -1,7 +1,7 @@
 // The kernels of attention with shaped scores at head dimension 96.
-#include "fa_scores_dq.cuh"
-#include "fa_scores_fwd.cuh"
 #include "fa_scores_dkdv.cuh"
+#include "fa_scores_dq.cuh"
+#include "fa_scores_launch.cuh"
 
 namespace fa {
 

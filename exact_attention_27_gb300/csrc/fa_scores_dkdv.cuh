@@ -65,7 +65,8 @@ struct ScoreDkdvCfg {
   static constexpr int NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // tmem slot, abort word, range
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
-  static constexpr int THREADS = 320;
+  static constexpr int WARPS = 16;                   // row warps; then TMA and MMA
+  static constexpr int THREADS = 32 * WARPS + 64;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DV = 256, COL_DK = 256 + DP;
   static_assert(COL_DK + DP <= TMEM_COLS, "tensor memory");
@@ -83,7 +84,7 @@ struct ScoreDkdvParams {
 };
 
 template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
     fa_scores_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV,
@@ -116,13 +117,13 @@ __global__ void __launch_bounds__(320, 1)
   const uint32_t sDS = sbase + C::OFF_DS;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NBAR; ++i) mbar_init(bar(i), i == C::B_P || i == C::B_DS ? 8 : 1);
+    for (int i = 0; i < C::NBAR; ++i) mbar_init(bar(i), i == C::B_P || i == C::B_DS ? C::WARPS : 1);
     *abort_flag = 0;
     range[0] = INT_MAX;
     range[1] = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == C::WARPS + 1) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(320, 1)
     bhq = bh0 + g;
   };
 
-  if (warp == 8) {
+  if (warp == C::WARPS) {
     // ------------------------------------------------------------ TMA producer
     if (n_steps > 0 && elect_one()) {
       tma_prefetch_desc(&tmQ);
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(320, 1)
           mbar_wait_timed(bar(C::B_DOFULL + s % C::NDO), (s / C::NDO) & 1);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == C::WARPS + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (n_steps > 0 && elect_one()) {
       constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, false, false);  // S, dP
@@ -267,87 +268,100 @@ __global__ void __launch_bounds__(320, 1)
     const int wq = warp & 3, g = warp >> 2;
     const int row = wq * 32 + static_cast<int>(threadIdx.x & 31);
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-    const int kbase = jt * C::BK + 64 * g;  // first key of this warp's half of the tile
-    // L, D and the span of this thread's row at step s, loaded one step ahead.
-    auto load_row = [&](int s, float& l, float& dd, KeySpan& span) {
-      int bhq, it;
-      step_coords(s, bhq, it);
+    const int kbase = jt * C::BK + 32 * g;  // first key of this warp's part of the tile
+    // L, D and the span of this thread's row, loaded one step ahead; steps go through the query
+    // tiles i0 .. i1 - 1 of one head after the other.
+    const int i1 = i0 + per_head;
+    const float* lse = p.lse + static_cast<size_t>(bh0) * p.s.Nq;  // of the next step's head
+    const float* dvec = p.Dvec + static_cast<size_t>(bh0) * p.s.Nq;
+    auto load_row = [&](int it, float& l, float& dd, KeySpan& span) {
       const int q = it * C::BQ + row;
       span = row_span(p.s, b, q);
-      const size_t idx = static_cast<size_t>(bhq) * p.s.Nq + min(q, p.s.Nq - 1);
-      l = p.lse[idx];
-      dd = p.Dvec[idx];
+      const int at = min(q, p.s.Nq - 1);
+      l = lse[at];
+      dd = dvec[at];
     };
     float l_cur = 0.0f, d_cur = 0.0f;
     KeySpan span_cur{0, 0};
-    if (n_steps > 0) load_row(0, l_cur, d_cur, span_cur);
+    if (n_steps > 0) load_row(i0, l_cur, d_cur, span_cur);
+    int it = i0, head = bh0 - b * p.s.Hq;
+    float slope2 = BIAS && p.s.slopes ? p.s.slopes[head] * kScoreLog2e : 0.0f;
     bool ok = true;
     for (int s = 0; s < n_steps; ++s) {
-      int bhq, it;
-      step_coords(s, bhq, it);
       const KeySpan span = span_cur;
       const bool sees = span.hi > 0;
       const float L2 = sees ? l_cur * kScoreLog2e : INFINITY;  // no key seen: P = 0
       const float nd = sees ? -d_cur : 0.0f;
-      const float slope2 =
-          BIAS && p.s.slopes ? p.s.slopes[bhq - b * p.s.Hq] * kScoreLog2e : 0.0f;
-      if (s + 1 < n_steps) load_row(s + 1, l_cur, d_cur, span_cur);  // used at the next step
-      const bool masked = __any_sync(0xffffffffu, span.lo > kbase || span.hi < kbase + 64);
+      const float dist0 = static_cast<float>(p.s.q_offset + it * C::BQ + row - kbase);
+      const float slope_now = slope2;
+      if (s + 1 < n_steps) {  // used at the next step
+        if (++it == i1) {
+          it = i0;
+          lse += p.s.Nq;
+          dvec += p.s.Nq;
+          if (BIAS && p.s.slopes) slope2 = p.s.slopes[++head] * kScoreLog2e;
+        }
+        load_row(it, l_cur, d_cur, span_cur);
+      }
+      const bool masked = __any_sync(0xffffffffu, span.lo > kbase || span.hi < kbase + 32);
       const unsigned from = static_cast<unsigned>(span.lo - kbase);
       const unsigned len = static_cast<unsigned>(span.hi - span.lo);
       ok = __all_sync(0xffffffffu,
                       mbar_wait(bar(C::B_S), s & 1, abort_flag, err, kErrTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
-      float w[64], gr[CAP ? 64 : 1];
+      float w[32];  // scores, then P, and at last what dP - D is multiplied by
       {
-        uint32_t sv[64];
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          tmem_ld32(tmem + lane_off + C::COL_S + 64 * g + 32 * c,
-                    *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+        uint32_t sv[32];
+        tmem_ld32(tmem + lane_off + C::COL_S + 32 * g, sv);
         tmem_wait_ld();
 #pragma unroll
-        for (int t = 0; t < 64; ++t) w[t] = __uint_as_float(sv[t]);
+        for (int t = 0; t < 32; ++t) w[t] = __uint_as_float(sv[t]);
       }
-      shape_scores<64, CAP, BIAS, CAP>(
-          w, gr, p.s.factor(CAP), p.s.cap2, slope2,
-          static_cast<float>(p.s.q_offset + it * C::BQ + row - kbase), L2);
+      // CH columns at a time: all, or half of them where the tanh's derivative takes registers
+      // too (96 a thread).
+      constexpr int CH = CAP ? 16 : 32;
+      uint32_t pk[16];
 #pragma unroll
-      for (int t = 0; t < 64; ++t) w[t] = ex2_approx(w[t]);
-      if (masked) {
+      for (int c0 = 0; c0 < 32; c0 += CH) {
+        float(&x)[CH] = *reinterpret_cast<float(*)[CH]>(&w[c0]);
+        float gr[CAP ? CH : 1];
+        shape_scores<CH, CAP, BIAS, CAP>(
+            x, gr, p.s.factor(CAP), p.s.cap2, slope_now, dist0 - c0, L2);
 #pragma unroll
-        for (int t = 0; t < 64; ++t)
-          if (static_cast<unsigned>(t) - from >= len) w[t] = 0.0f;
+        for (int t = 0; t < CH; ++t) x[t] = ex2_approx(x[t]);
+        if (masked) {
+#pragma unroll
+          for (int t = 0; t < CH; ++t)
+            if (static_cast<unsigned>(c0 + t) - from >= len) x[t] = 0.0f;
+        }
+#pragma unroll
+        for (int t = 0; t < CH; t += 2) {
+          pk[(c0 + t) / 2] = pack_bf16x2(x[t], x[t + 1]);
+          if constexpr (CAP)
+            f2_unpack(f2_mul(f2_pack(x[t], x[t + 1]), f2_pack(gr[t], gr[t + 1])), x[t], x[t + 1]);
+        }
       }
-      // P as bf16 to its row in the block of this warp's 64 keys.
+      // P as bf16 to its row in the block of 64 keys: four of its eight 16-byte chunks.
+      const uint32_t blk = (g >> 1) * C::BLOCK;
+      const int ch = (g & 1) * 4;
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        st_shared_v4(sP + g * C::BLOCK + sw128(row, c), pack_bf16x2(w[8 * c], w[8 * c + 1]),
-                     pack_bf16x2(w[8 * c + 2], w[8 * c + 3]),
-                     pack_bf16x2(w[8 * c + 4], w[8 * c + 5]),
-                     pack_bf16x2(w[8 * c + 6], w[8 * c + 7]));
+      for (int c = 0; c < 4; ++c)
+        st_shared_v4(sP + blk + sw128(row, ch + c), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2],
+                     pk[4 * c + 3]);
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive_warp(bar(C::B_P));
-      if constexpr (CAP) {
-#pragma unroll
-        for (int t = 0; t < 64; t += 2)
-          f2_unpack(f2_mul(f2_pack(w[t], w[t + 1]), f2_pack(gr[t], gr[t + 1])), w[t], w[t + 1]);
-      }
       ok = __all_sync(0xffffffffu,
                       mbar_wait(bar(C::B_DP), s & 1, abort_flag, err, kErrTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
       const uint64_t nd2 = f2_pack(nd, nd);
-      uint32_t dpv[64];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        tmem_ld32(tmem + lane_off + C::COL_DP + 64 * g + 32 * c,
-                  *reinterpret_cast<uint32_t(*)[32]>(&dpv[32 * c]));
+      uint32_t dpv[32];
+      tmem_ld32(tmem + lane_off + C::COL_DP + 32 * g, dpv);
       tmem_wait_ld();
 #pragma unroll
-      for (int t = 0; t < 64; t += 2)
+      for (int t = 0; t < 32; t += 2)
         f2_unpack(f2_mul(f2_pack(w[t], w[t + 1]),
                          f2_add(f2_pack(__uint_as_float(dpv[t]), __uint_as_float(dpv[t + 1])),
                                 nd2)),
@@ -356,12 +370,12 @@ __global__ void __launch_bounds__(320, 1)
         // (0 x NaN where a row that sees nothing holds anything; a row of one key has dP = D)
         const unsigned len_ds = len > 1 ? len : 0u;
 #pragma unroll
-        for (int t = 0; t < 64; ++t)
+        for (int t = 0; t < 32; ++t)
           if (static_cast<unsigned>(t) - from >= len_ds) w[t] = 0.0f;
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        st_shared_v4(sDS + g * C::BLOCK + sw128(row, c), pack_bf16x2(w[8 * c], w[8 * c + 1]),
+      for (int c = 0; c < 4; ++c)
+        st_shared_v4(sDS + blk + sw128(row, ch + c), pack_bf16x2(w[8 * c], w[8 * c + 1]),
                      pack_bf16x2(w[8 * c + 2], w[8 * c + 3]),
                      pack_bf16x2(w[8 * c + 4], w[8 * c + 5]),
                      pack_bf16x2(w[8 * c + 6], w[8 * c + 7]));
@@ -369,21 +383,22 @@ __global__ void __launch_bounds__(320, 1)
       tc_fence_before();
       mbar_arrive_warp(bar(C::B_DS));
     }
-    // ---- epilogue, once every product has completed: warps 0-3 write dV, warps 4-7 dK
-    // (times scale); lane l of warp w holds key 32 (w % 4) + l.
+    // ---- epilogue, once every product has completed: column groups 0 and 1 write dV, 2 and 3
+    // dK (times scale), every other 32 columns each; lane l of warp w holds key 32 (w % 4) + l.
     if (ok && n_steps > 0)
       ok = __all_sync(0xffffffffu,
                       mbar_wait(bar(C::B_FINAL), 0, abort_flag, err, kErrTimeoutEpilogue));
     if (ok) {
       tc_fence_after();
-      const float mul = g == 0 ? 1.0f : p.s.scale;
-      const uint32_t col0 = g == 0 ? C::COL_DV : C::COL_DK;
+      const bool is_dv = g < 2;
+      const float mul = is_dv ? 1.0f : p.s.scale;
+      const uint32_t col0 = is_dv ? C::COL_DV : C::COL_DK;
       const int key = jt * C::BK + row;
       const bool live = key < p.s.Nk;
-      __nv_bfloat16* out = (g == 0 ? p.dv : p.dk) +
+      __nv_bfloat16* out = (is_dv ? p.dv : p.dk) +
                            (static_cast<size_t>(kvz) * p.s.Nk + (live ? key : 0)) * D;
 #pragma unroll 1
-      for (int q4 = 0; q4 < D / 32; ++q4) {
+      for (int q4 = g & 1; q4 < D / 32; q4 += 2) {
         uint32_t r[32];
         if (n_steps > 0) {
           tmem_ld32(tmem + lane_off + col0 + q4 * 32, r);
@@ -411,7 +426,7 @@ __global__ void __launch_bounds__(320, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::WARPS + 1) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);

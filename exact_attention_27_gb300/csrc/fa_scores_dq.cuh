@@ -47,7 +47,9 @@ struct ScoreDqCfg {
   static constexpr int BM = 128;                 // query rows per CTA
   static constexpr int BN = (D == 256) ? 64 : 128;  // keys per tile
   static constexpr int EXACT_TILES = 3 * 128 / BN;
-  static constexpr int KH = BN / 2;              // key columns per row warp
+  static constexpr int KH = 32;                  // key columns per row warp
+  static constexpr int GROUPS = BN / KH;         // row warps that share a row
+  static constexpr int WARPS = 4 * GROUPS;       // row warps; then TMA and MMA
   static constexpr int SUB = DP / 64;
   static constexpr int QSUB = 128 * 128;         // 128 query rows x 64 bf16
   static constexpr int KSUB = BN * 128;          // BN key rows x 64 bf16
@@ -74,13 +76,13 @@ struct ScoreDqCfg {
   static constexpr int B_DPFREE = B_DPFULL + 1;    // dP_j read by every row warp (8 arrivals)
   static constexpr int B_DSREADY = B_DPFREE + 1;   // [2] dS_j in S buffer j % 2 (8 arrivals)
   static constexpr int B_DQDONE = B_DSREADY + 2;   // every dQ MMA done (completes once)
-  static constexpr int B_DSUM = B_DQDONE + 1;      // both halves' sums of P dP (8 arrivals, once)
+  static constexpr int B_DSUM = B_DQDONE + 1;      // the parts' sums of P dP (every row warp, twice)
   static constexpr int B_DRAIN = B_DSUM + 1;
   static constexpr int NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int OFF_SUM = OFF_MISC + 8 + 32;    // [2][BM] sums of P dP
   static constexpr int SMEM_BYTES = OFF_SUM + 2 * BM * 4 + 1024;
-  static constexpr int THREADS = 320;
+  static constexpr int THREADS = 32 * WARPS + 64;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_S = 0, COL_DP = 2 * BN;  // S buffer b at COL_S + BN b
   static constexpr uint32_t COL_DQ = (D == 256) ? 256 : 384;
@@ -97,7 +99,7 @@ struct ScoreDqParams {
 };
 
 template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
     fa_scores_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV,
@@ -138,24 +140,24 @@ __global__ void __launch_bounds__(320, 1)
     }
     for (int b2 = 0; b2 < 2; ++b2) {
       mbar_init(bar(C::B_SFULL + b2), 1);
-      mbar_init(bar(C::B_DSREADY + b2), 8);
+      mbar_init(bar(C::B_DSREADY + b2), C::WARPS);
     }
     mbar_init(bar(C::B_DPFULL), 1);
-    mbar_init(bar(C::B_DPFREE), 8);
+    mbar_init(bar(C::B_DPFREE), C::WARPS);
     mbar_init(bar(C::B_DQDONE), 1);
-    mbar_init(bar(C::B_DSUM), 8);
+    mbar_init(bar(C::B_DSUM), C::WARPS);
     mbar_init(bar(C::B_DRAIN), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == C::WARPS + 1) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
   grid_dependency_wait();
   grid_launch_dependents();
   KeySpan span{0, 0};
-  if (warp < 8) {
+  if (warp < C::WARPS) {
     span = row_span(p.s, b, qt * C::BM + (warp & 3) * 32 + static_cast<int>(threadIdx.x & 31));
     const KeySpan h = warp_hull(span);
     if (warp < 4 && (threadIdx.x & 31) == 0) hulls[warp] = h;
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(320, 1)
   const uint32_t sK = sbase + C::OFF_K;
   const uint32_t sV = sbase + C::OFF_V;
 
-  if (warp == 8) {
+  if (warp == C::WARPS) {
     // ------------------------------------------------------------ TMA producer
     if (n_kv > 0 && elect_one()) {
       tma_prefetch_desc(&tmQ);
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(320, 1)
           mbar_wait_timed(bar(C::B_VFULL + j % C::NSV), (j / C::NSV) & 1);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == C::WARPS + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (n_kv > 0 && elect_one()) {
       constexpr uint32_t ID_S = idesc_bf16_f32(128, C::BN, false, false);  // S, dP
@@ -339,42 +341,80 @@ __global__ void __launch_bounds__(320, 1)
       tc_fence_after();
       const uint32_t scol = C::COL_S + C::BN * (j & 1) + C::KH * g;
       constexpr int KH = C::KH;
-      float s[KH];
-      uint32_t dpv[KH];
-      {
-        uint32_t sv[KH];
-#pragma unroll
-        for (int c = 0; c < KH / 32; ++c) {
-          tmem_ld32(tmem + lane_off + scol + 32 * c,
-                    *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
-          tmem_ld32(tmem + lane_off + C::COL_DP + KH * g + 32 * c,
-                    *reinterpret_cast<uint32_t(*)[32]>(&dpv[32 * c]));
-        }
-        tmem_wait_ld();
-#pragma unroll
-        for (int t = 0; t < KH; ++t) s[t] = __uint_as_float(sv[t]);
-      }
-      tc_fence_before();
-      mbar_arrive_warp(bar(C::B_DPFREE));
       const int kbase = key_tile(j) * C::BN + KH * g;
       const bool need_mask = __any_sync(0xffffffffu, span.lo > kbase || span.hi < kbase + KH);
-      float gr[CAP ? KH : 1];
-      shape_scores<KH, CAP, BIAS, CAP>(s, gr, p.s.factor(CAP), p.s.cap2, slope2,
-                                       static_cast<float>(p.s.q_offset + qi - kbase), L2);
-      if (j < n_sum) {
-        // D = sum of P dP, of both halves of the row's keys.
-        const unsigned at = static_cast<unsigned>(span.lo - kbase);
-        const unsigned seen = static_cast<unsigned>(span.hi - span.lo);
+      const unsigned from = static_cast<unsigned>(span.lo - kbase);
+      const int n_seen = span.hi - span.lo;
+      const float dist0 = static_cast<float>(p.s.q_offset + qi - kbase);
+      // CH columns at a time: all, or half of them where the tanh's derivative takes registers
+      // too (96 a thread).
+      constexpr int CH = CAP ? KH / 2 : KH;
+      // (a row of one key: P = 1 and dP = D, so dS = 0)
+      const unsigned seen = static_cast<unsigned>(n_seen);
+      const unsigned len = n_seen > 1 ? seen : 0u;
+      uint32_t pk[KH / 2];
 #pragma unroll
-        for (int t = 0; t < KH; ++t)
-          if (static_cast<unsigned>(t) - at < seen)
-            Drow = fmaf(ex2_approx(s[t]), __uint_as_float(dpv[t]), Drow);
+      for (int c0 = 0; c0 < KH; c0 += CH) {
+        float s[CH];
+        uint32_t dpv[CH];
+        {
+          uint32_t sv[CH];
+          tmem_ld<CH>(tmem + lane_off + scol + c0, sv);
+          tmem_ld<CH>(tmem + lane_off + C::COL_DP + KH * g + c0, dpv);
+          tmem_wait_ld();
+#pragma unroll
+          for (int t = 0; t < CH; ++t) s[t] = __uint_as_float(sv[t]);
+        }
+        if (c0 + CH == KH) {
+          tc_fence_before();
+          mbar_arrive_warp(bar(C::B_DPFREE));
+        }
+        float gr[CAP ? CH : 1];
+        shape_scores<CH, CAP, BIAS, CAP>(s, gr, p.s.factor(CAP), p.s.cap2, slope2, dist0 - c0, L2);
+        if (j < n_sum) {
+          // D = sum of P dP, over all parts of the row's keys.
+#pragma unroll
+          for (int t = 0; t < CH; ++t)
+            if (static_cast<unsigned>(c0 + t) - from < seen)
+              Drow = fmaf(ex2_approx(s[t]), __uint_as_float(dpv[t]), Drow);
+          continue;
+        }
+        // One copy of the loop with the (warp-uniform) mask and one without: a branch inside
+        // the unrolled loop would split it into blocks scheduled one by one.
+        auto ds_pass = [&](auto masked_t) {
+#pragma unroll
+          for (int u = 0; u < CH / 2; ++u) {
+            uint64_t w = f2_pack(ex2_approx(s[2 * u]), ex2_approx(s[2 * u + 1]));
+            if constexpr (CAP) w = f2_mul(w, f2_pack(gr[2 * u], gr[2 * u + 1]));
+            const uint64_t dd =
+                f2_add(f2_pack(__uint_as_float(dpv[2 * u]), __uint_as_float(dpv[2 * u + 1])), nd2);
+            float d0, d1;
+            f2_unpack(f2_mul(w, dd), d0, d1);
+            if constexpr (decltype(masked_t)::value) {
+              if (static_cast<unsigned>(c0 + 2 * u) - from >= len) d0 = 0.0f;
+              if (static_cast<unsigned>(c0 + 2 * u + 1) - from >= len) d1 = 0.0f;
+            }
+            pk[c0 / 2 + u] = pack_bf16x2(d0, d1);
+          }
+        };
+        if (need_mask)
+          ds_pass(std::true_type{});
+        else
+          ds_pass(std::false_type{});
+      }
+      if (j < n_sum) {
         tc_fence_before();
         mbar_arrive_warp(bar(C::B_DSREADY + (j & 1)));
         if (j == n_sum - 1) {
-          sums[g * C::BM + row] = Drow;
+          // The row's parts join: groups 2 and 3 hand theirs to 0 and 1, which all then add.
+          if (g >= 2) sums[(g - 2) * C::BM + row] = Drow;
           mbar_arrive_warp(bar(C::B_DSUM));
           ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_DSUM), 0, abort_flag, err,
+                                                 kErrTimeoutSoftmax));
+          if (!ok) break;
+          if (g < 2) sums[g * C::BM + row] = Drow + (C::GROUPS > 2 ? sums[g * C::BM + row] : 0.0f);
+          mbar_arrive_warp(bar(C::B_DSUM));
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_DSUM), 1, abort_flag, err,
                                                  kErrTimeoutSoftmax));
           if (!ok) break;
           Drow = sums[row] + sums[C::BM + row];
@@ -383,38 +423,8 @@ __global__ void __launch_bounds__(320, 1)
         }
         continue;
       }
-      uint32_t pk[KH / 2];
-      // One copy of the loop with the (warp-uniform) mask and one without: a branch inside
-      // the unrolled loop would split it into blocks scheduled one by one.
-      const unsigned from = static_cast<unsigned>(span.lo - kbase);
-      // (a row of one key: P = 1 and dP = D, so dS = 0)
-      const int n_seen = span.hi - span.lo;
-      const unsigned len = n_seen > 1 ? static_cast<unsigned>(n_seen) : 0u;
-      auto ds_pass = [&](auto masked_t) {
-#pragma unroll
-        for (int u = 0; u < KH / 2; ++u) {
-          uint64_t w = f2_pack(ex2_approx(s[2 * u]), ex2_approx(s[2 * u + 1]));
-          if constexpr (CAP) w = f2_mul(w, f2_pack(gr[2 * u], gr[2 * u + 1]));
-          const uint64_t dd =
-              f2_add(f2_pack(__uint_as_float(dpv[2 * u]), __uint_as_float(dpv[2 * u + 1])), nd2);
-          float d0, d1;
-          f2_unpack(f2_mul(w, dd), d0, d1);
-          if constexpr (decltype(masked_t)::value) {
-            if (static_cast<unsigned>(2 * u) - from >= len) d0 = 0.0f;
-            if (static_cast<unsigned>(2 * u + 1) - from >= len) d1 = 0.0f;
-          }
-          pk[u] = pack_bf16x2(d0, d1);
-        }
-      };
-      if (need_mask)
-        ds_pass(std::true_type{});
-      else
-        ds_pass(std::false_type{});
       // dS (bf16 pairs) over S columns this warp has already read.
-      if constexpr (KH == 64)
-        tmem_st32(tmem + lane_off + scol, pk);
-      else
-        tmem_st16(tmem + lane_off + scol, pk);
+      tmem_st16(tmem + lane_off + scol, pk);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive_warp(bar(C::B_DSREADY + (j & 1)));
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(320, 1)
       tc_fence_after();
       __nv_bfloat16* qrow = p.dq + ridx * D;
 #pragma unroll 1
-      for (int q4 = g; q4 < D / 32; q4 += 2) {
+      for (int q4 = g; q4 < D / 32; q4 += C::GROUPS) {
         uint32_t r[32];
         if (n_kv > 0) {
           tmem_ld32(tmem + lane_off + C::COL_DQ + q4 * 32, r);
@@ -457,7 +467,7 @@ __global__ void __launch_bounds__(320, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::WARPS + 1) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);

@@ -10,6 +10,7 @@
 // online softmax subtracts is fixed, at half the cap's exponent, as long as all weights then
 // stay within fp32's (and bf16's) exponents: no running maximum and no rescaling of O.  For
 // softcap log2(e) <= kFixedCap the weights lie in [2^-(1.5 kFixedCap), 2^(kFixedCap / 2)].
+#pragma once
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -25,12 +26,15 @@ namespace {
 
 constexpr float kRescaleThreshold = 8.0f;
 
-template <int D_>
+template <int D_, bool FIXED>
 struct ScoreFwdCfg {
   static constexpr int D = D_;
   static constexpr int DP = (D + 63) / 64 * 64;  // tiles are whole 128-byte swizzle atoms wide
   static constexpr int BM = 128;
   static constexpr int BN = D == 256 ? 64 : 128;
+  static constexpr int KH = FIXED ? 32 : BN;     // key columns of a softmax warp
+  static constexpr int GROUPS = BN / KH;         // softmax warps that share a row
+  static constexpr int WARPS = 4 * GROUPS;       // softmax warps; then TMA and MMA
   static constexpr int SUB = DP / 64;
   static constexpr int Q_BLOCK = BM * 128;
   static constexpr int KV_BLOCK = BN * 128;
@@ -48,14 +52,16 @@ struct ScoreFwdCfg {
   static constexpr int B_VEMPTY = B_VFULL + NS;
   static constexpr int NB = 3;                   // S/P buffers
   static constexpr int B_SFULL = B_VEMPTY + NS;  // [NB] S_j in buffer j % NB
-  static constexpr int B_PFULL = B_SFULL + NB;   // [NB] P_j there (4 warp arrivals)
+  static constexpr int B_PFULL = B_SFULL + NB;   // [NB] P_j there (every softmax warp)
   static constexpr int B_ODONE = B_PFULL + NB;   // O += P_j V_j completed
   static constexpr int B_FINAL = B_ODONE + 1;    // every product completed (once)
-  static constexpr int B_DRAIN = B_FINAL + 1;
+  static constexpr int B_SUM = B_FINAL + 1;      // the parts of l in shared memory (once)
+  static constexpr int B_DRAIN = B_SUM + 1;
   static constexpr int NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;  // tmem slot, abort word, 4 warps' hulls
-  static constexpr int SMEM_BYTES = OFF_MISC + 8 + 32 + 1024;
-  static constexpr int THREADS = 192;
+  static constexpr int OFF_SUM = OFF_MISC + 8 + 32;    // [GROUPS][BM] parts of l
+  static constexpr int SMEM_BYTES = OFF_SUM + (GROUPS > 1 ? GROUPS * BM * 4 : 0) + 1024;
+  static constexpr int THREADS = 32 * WARPS + 64;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_O = 512 - DP;
   static_assert(NB * BN <= 512 - DP, "tensor memory");
@@ -69,14 +75,150 @@ struct ScoreFwdParams {
   int n_qtiles, n_heads, heads_per_group;
 };
 
+// The scores of a row's key tile (BN keys from kbase on) at TMEM address `s_addr` to P over
+// them, with the running reference m and sum l (log2 domain); keys outside `span` get 0 where
+// `mask`.  Returns the factor that O and the old l are due (1 unless `moved`).  FIXED: m is
+// the reference, cap2 / 2, and stays.  The whole warp calls this.
+template <int BN, bool CAP, bool BIAS, bool FIXED>
+__device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr, bool mask,
+                                           const KeySpan& span, int kbase, int pos, float slope2,
+                                           float& m, float& l, bool& moved) {
+  const unsigned from = static_cast<unsigned>(span.lo - kbase);
+  const unsigned len = static_cast<unsigned>(span.hi - span.lo);
+  uint64_t ps2[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) ps2[u] = 0ull;
+  float alpha = 1.0f;
+  if constexpr (FIXED) {
+    float x[BN], none[1];
+    {
+      uint32_t r[BN];
+      tmem_ld<BN>(s_addr, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int t = 0; t < BN; ++t) x[t] = __uint_as_float(r[t]);
+    }
+    shape_scores<BN, CAP, BIAS, false>(x, none, p.factor(CAP), p.cap2, slope2,
+                                       static_cast<float>(pos - kbase), m);
+    if (mask) {
+#pragma unroll
+      for (int t = 0; t < BN; ++t)
+        if (static_cast<unsigned>(t) - from >= len) x[t] = -INFINITY;
+    }
+    uint32_t pk[BN / 2];
+#pragma unroll
+    for (int t = 0; t < BN / 2; ++t) {
+      const float p0 = ex2_approx(x[2 * t]);
+      const float p1 = ex2_approx(x[2 * t + 1]);
+      ps2[t & 3] = f2_add(ps2[t & 3], f2_pack(p0, p1));
+      pk[t] = pack_bf16x2(p0, p1);
+    }
+    static_assert(!FIXED || BN == 32, "columns of a part");
+    tmem_st16(s_addr, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
+  } else {
+    float s[BN], none[1];
+    {
+      uint32_t r[BN];
+#pragma unroll
+      for (int q4 = 0; q4 < BN / 32; ++q4)
+        tmem_ld32(s_addr + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[q4 * 32]));
+      tmem_wait_ld();
+#pragma unroll
+      for (int t = 0; t < BN; ++t) s[t] = __uint_as_float(r[t]);
+    }
+    // Without a tanh or a distance the scale waits for the exponents' multiply-add.
+    constexpr bool RAW = !CAP && !BIAS;
+    if constexpr (!RAW)
+      shape_scores<BN, CAP, BIAS, false>(s, none, p.factor(CAP), p.cap2, slope2,
+                                         static_cast<float>(pos - kbase), 0.0f);
+    if (mask) {
+#pragma unroll
+      for (int t = 0; t < BN; ++t)
+        if (static_cast<unsigned>(t) - from >= len) s[t] = -INFINITY;
+    }
+    // Row max over 8 independent partial maxima, two values a three-input max.
+    float pm[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) pm[u] = fmaxf(s[u], s[u + 8]);
+#pragma unroll
+    for (int t = 16; t < BN; t += 16)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) pm[u] = fmax3(pm[u], s[t + u], s[t + u + 8]);
+    const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]),
+                           fmaxf(fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+    const float c = RAW ? p.scale2 : 1.0f;
+    const float m_new = fmaxf(m, mx * c);
+    // The reference moves only when the maximum has grown by more than the threshold.
+    moved = m_new > m + kRescaleThreshold;
+    if (moved) {
+      alpha = ex2_approx(m - m_new);
+      m = m_new;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+    const uint64_t nm2 = f2_pack(-ref, -ref), c2 = f2_pack(c, c);
+    uint32_t pk[BN / 2];
+#pragma unroll
+    for (int t = 0; t < BN / 2; ++t) {
+      float x0, x1;
+      const uint64_t x = f2_pack(s[2 * t], s[2 * t + 1]);
+      f2_unpack(RAW ? f2_fma(x, c2, nm2) : f2_add(x, nm2), x0, x1);
+      const float p0 = ex2_approx(x0);
+      const float p1 = ex2_approx(x1);
+      ps2[t & 3] = f2_add(ps2[t & 3], f2_pack(p0, p1));
+      pk[t] = pack_bf16x2(p0, p1);
+    }
+#pragma unroll
+    for (int q4 = 0; q4 < BN / 64; ++q4)
+      tmem_st32(s_addr + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[q4 * 32]));
+  }
+  float sum, sum_hi;
+  f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), sum, sum_hi);
+  l = l * alpha + (sum + sum_hi);
+  return alpha;
+}
+
+// A row's O out of TMEM at `col_o` (any: there is one) over l, and its lse; zeros and
+// -infinity for a row that sees no key.  Every GROUPS-th part of 32 columns, from the g-th on.
+// The whole warp calls this.
+template <int D, int GROUPS>
+__device__ __forceinline__ void store_row(const ScoreFwdParams& p, int bh, int qi, uint32_t col_o,
+                                          int g, bool any, bool empty, float m, float l) {
+  const float inv_l = 1.0f / l;
+  const bool live = qi < p.s.Nq;
+  __nv_bfloat16* orow = p.o + (static_cast<size_t>(bh) * p.s.Nq + (live ? qi : 0)) * D;
+#pragma unroll 1
+  for (int q4 = g; q4 < D / 32; q4 += GROUPS) {
+    uint32_t r[32];
+    if (any) {
+      tmem_ld32(col_o + q4 * 32, r);
+      tmem_wait_ld();
+    }
+    uint32_t pk[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+      pk[t] = empty || !any ? 0u
+                            : pack_bf16x2(__uint_as_float(r[2 * t]) * inv_l,
+                                          __uint_as_float(r[2 * t + 1]) * inv_l);
+    if (live) {
+      uint4* dst = reinterpret_cast<uint4*>(orow + q4 * 32);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        dst[t] = make_uint4(pk[4 * t], pk[4 * t + 1], pk[4 * t + 2], pk[4 * t + 3]);
+    }
+  }
+  if (live && g == 0)
+    p.lse[static_cast<size_t>(bh) * p.s.Nq + qi] =
+        empty ? -INFINITY : (m + log2f(l)) * kScoreLn2;
+}
+
 // FIXED: the softmax reference is p.s.cap2 / 2.
 template <int D, bool CAP, bool BIAS, bool FIXED>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__((ScoreFwdCfg<D, FIXED>::THREADS), 1)
     fa_scores_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ ScoreFwdParams p) {
-  using C = ScoreFwdCfg<D>;
+  using C = ScoreFwdCfg<D, FIXED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -103,21 +245,24 @@ __global__ void __launch_bounds__(192, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBAR; ++i)
-      mbar_init(bar(i), i >= C::B_PFULL && i < C::B_PFULL + C::NB ? 4 : 1);
+      mbar_init(bar(i),
+                (i >= C::B_PFULL && i < C::B_PFULL + C::NB) || i == C::B_SUM ? C::WARPS : 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (warp == C::WARPS + 1) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
   grid_dependency_wait();
   grid_launch_dependents();
   KeySpan span{0, 0};
-  if (warp < 4) {
-    span = row_span(p.s, b, qt * C::BM + static_cast<int>(threadIdx.x));
-    const KeySpan h = warp_hull(span);
-    if ((threadIdx.x & 31) == 0) hulls[warp] = h;
+  if (warp < C::WARPS) {
+    span = row_span(p.s, b, qt * C::BM + static_cast<int>(threadIdx.x & 127));
+    if (warp < 4) {
+      const KeySpan h = warp_hull(span);
+      if ((threadIdx.x & 31) == 0) hulls[warp] = h;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -132,7 +277,7 @@ __global__ void __launch_bounds__(192, 1)
   const uint32_t sK = sbase + C::OFF_K;
   const uint32_t sV = sbase + C::OFF_V;
 
-  if (warp == 4) {
+  if (warp == C::WARPS) {
     // ------------------------------------------------------------ TMA producer
     if (n_kv > 0 && elect_one()) {
       tma_prefetch_desc(&tmQ);
@@ -173,7 +318,7 @@ __global__ void __launch_bounds__(192, 1)
           mbar_wait_timed(bar(C::B_VFULL + j % C::NS), (j / C::NS) & 1);
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == C::WARPS + 1) {
     // ------------------------------------------------------------ MMA issuer
     if (n_kv > 0 && elect_one()) {
       constexpr uint32_t ID_S = idesc_bf16_f32(128, C::BN, false, false);
@@ -207,7 +352,8 @@ __global__ void __launch_bounds__(192, 1)
         if (!mbar_wait(bar(C::B_PFULL + bf), (j / C::NB) & 1, abort_flag, err, kErrTimeoutMma))
           break;
         tc_fence_after();
-        // O += P_j V_j: P packed in the first columns of buffer bf, 16 keys a step.
+        // O += P_j V_j: P of keys KH g.. packed at columns KH g.. of buffer bf, 16 keys a step.
+        constexpr int KPW = C::KH / 16;
         const uint64_t vd = desc_add(v_desc, st * C::KV_TILE);
         const uint32_t pa = tmem + bf * C::BN;
         if (j == 0)
@@ -216,7 +362,8 @@ __global__ void __launch_bounds__(192, 1)
           mma_ts_k<ID_O, 1>(tmem + C::COL_O, pa, vd);
 #pragma unroll
         for (int kk = 1; kk < C::BN / 16; ++kk)
-          mma_ts_k<ID_O, 1>(tmem + C::COL_O, pa + kk * 8, desc_add(vd, kk * 2048));
+          mma_ts_k<ID_O, 1>(tmem + C::COL_O, pa + kk / KPW * C::KH + kk % KPW * 8,
+                            desc_add(vd, kk * 2048));
         mma_commit(bar(C::B_ODONE));
         mma_commit(bar(C::B_VEMPTY + st));
         // Once, after the last product: at its epilogue the softmax may be two phases behind
@@ -232,8 +379,9 @@ __global__ void __launch_bounds__(192, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax (rows)
-    const int row = threadIdx.x;
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    // Warp w: rows 32 (w % 4).., key columns KH (w / 4)...
+    const int row = threadIdx.x & 127, g = warp >> 2;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int qi = qt * C::BM + row;
     const float slope2 = BIAS && p.s.slopes ? p.s.slopes[hq] * kScoreLog2e : 0.0f;
     const int pos = p.s.q_offset + qi;
@@ -242,86 +390,19 @@ __global__ void __launch_bounds__(192, 1)
     bool ok = true;
     for (int j = 0; j < n_kv; ++j) {
       const int bf = j % C::NB;
-      const uint32_t col_s = bf * C::BN;
       // Waits are made warp-uniform: the TMEM loads and stores below are
       // warp-collective, so either every lane goes on or every lane stops.
       ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_SFULL + bf), (j / C::NB) & 1, abort_flag,
                                              err, kErrTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
-      float s[C::BN];
-      {
-        uint32_t r[C::BN];
-#pragma unroll
-        for (int q4 = 0; q4 < C::BN / 32; ++q4)
-          tmem_ld32(tmem + lane_off + col_s + q4 * 32,
-                    *reinterpret_cast<uint32_t(*)[32]>(&r[q4 * 32]));
-        tmem_wait_ld();
-#pragma unroll
-        for (int t = 0; t < C::BN; ++t) s[t] = __uint_as_float(r[t]);
-      }
-      const int kbase = (j0 + j) * C::BN;
-      const bool need_mask =
-          __any_sync(0xffffffffu, span.lo > kbase || span.hi < kbase + C::BN);
-      float none[1];
-      shape_scores<C::BN, CAP, BIAS, false>(s, none, p.s.factor(CAP), p.s.cap2, slope2,
-                                            static_cast<float>(pos - kbase),
-                                            FIXED ? m_used : 0.0f);
-      if (need_mask) {
-        const unsigned from = static_cast<unsigned>(span.lo - kbase);
-        const unsigned len = static_cast<unsigned>(span.hi - span.lo);
-#pragma unroll
-        for (int t = 0; t < C::BN; ++t)
-          if (static_cast<unsigned>(t) - from >= len) s[t] = -INFINITY;
-      }
-      float alpha = 1.0f, m_ref = 0.0f;
+      const int kbase = (j0 + j) * C::BN + C::KH * g;
+      const bool need_mask = __any_sync(0xffffffffu, span.lo > kbase || span.hi < kbase + C::KH);
       bool upd = false;
-      if constexpr (!FIXED) {
-        // Row max over 8 independent partial maxima, two values a three-input max.
-        float pm[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) pm[u] = fmaxf(s[u], s[u + 8]);
-#pragma unroll
-        for (int t = 16; t < C::BN; t += 16)
-#pragma unroll
-          for (int u = 0; u < 8; ++u) pm[u] = fmax3(pm[u], s[t + u], s[t + u + 8]);
-        const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]),
-                               fmaxf(fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-        const float m_new = fmaxf(m_used, mx);
-        // The reference moves only when the maximum has grown by more than the threshold.
-        upd = m_new > m_used + kRescaleThreshold;
-        if (upd) {
-          alpha = ex2_approx(m_used - m_new);
-          m_used = m_new;
-        }
-        m_ref = (m_used == -INFINITY) ? 0.0f : m_used;
-      }
-      const uint64_t nm2 = f2_pack(-m_ref, -m_ref);
-      uint64_t ps2[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) ps2[u] = 0ull;
-      {
-        uint32_t pk[C::BN / 2];
-#pragma unroll
-        for (int t = 0; t < C::BN / 2; ++t) {
-          float x0 = s[2 * t], x1 = s[2 * t + 1];
-          if constexpr (!FIXED) f2_unpack(f2_add(f2_pack(x0, x1), nm2), x0, x1);
-          const float p0 = ex2_approx(x0);
-          const float p1 = ex2_approx(x1);
-          ps2[t & 3] = f2_add(ps2[t & 3], f2_pack(p0, p1));
-          pk[t] = pack_bf16x2(p0, p1);
-        }
-        // P over the S columns just read.
-#pragma unroll
-        for (int q4 = 0; q4 < C::BN / 64; ++q4)
-          tmem_st32(tmem + lane_off + col_s + q4 * 32,
-                    *reinterpret_cast<uint32_t(*)[32]>(&pk[q4 * 32]));
-      }
-      float sum, sum_hi;
-      f2_unpack(f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3])), sum, sum_hi);
-      sum += sum_hi;
-      l = l * alpha + sum;
-      if (j > 0 && __any_sync(0xffffffffu, upd)) {
+      const float alpha =
+          score_row<C::KH, CAP, BIAS, FIXED>(p.s, tmem + lane_off + bf * C::BN + C::KH * g,
+                                             need_mask, span, kbase, pos, slope2, m_used, l, upd);
+      if (!FIXED && j > 0 && __any_sync(0xffffffffu, upd)) {
         // O must be final before it is rescaled.  S_j being ready implies O += P_{j-2}
         // V_{j-2} is done, so the per-tile barrier is at most one phase behind.
         ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_ODONE), (j - 1) & 1, abort_flag, err,
@@ -343,38 +424,23 @@ __global__ void __launch_bounds__(192, 1)
       mbar_arrive_warp(bar(C::B_PFULL + bf));
     }
     // ------------------------------------------------------------ epilogue
+    if constexpr (C::GROUPS > 1) {
+      float* sums = reinterpret_cast<float*>(smem + C::OFF_SUM);
+      sums[g * C::BM + row] = l;
+      mbar_arrive_warp(bar(C::B_SUM));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(C::B_SUM), 0, abort_flag, err,
+                                                   kErrTimeoutEpilogue));
+      l = 0.0f;
+#pragma unroll
+      for (int k = 0; k < C::GROUPS; ++k) l += sums[k * C::BM + row];
+    }
     if (ok && n_kv > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_FINAL), 0, abort_flag, err,
                                              kErrTimeoutEpilogue));
     if (ok) {
       tc_fence_after();
-      const bool empty = span.hi == 0;  // sees no key: zeros and -infinity
-      const float inv_l = 1.0f / l;
-      const bool live = qi < p.s.Nq;
-      __nv_bfloat16* orow = p.o + (static_cast<size_t>(bh) * p.s.Nq + (live ? qi : 0)) * C::D;
-#pragma unroll 1
-      for (int q4 = 0; q4 < C::D / 32; ++q4) {
-        uint32_t r[32];
-        if (n_kv > 0) {
-          tmem_ld32(tmem + lane_off + C::COL_O + q4 * 32, r);
-          tmem_wait_ld();
-        }
-        uint32_t pk[16];
-#pragma unroll
-        for (int t = 0; t < 16; ++t)
-          pk[t] = empty || n_kv == 0 ? 0u
-                                     : pack_bf16x2(__uint_as_float(r[2 * t]) * inv_l,
-                                                   __uint_as_float(r[2 * t + 1]) * inv_l);
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + q4 * 32);
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            dst[t] = make_uint4(pk[4 * t], pk[4 * t + 1], pk[4 * t + 2], pk[4 * t + 3]);
-        }
-      }
-      if (live)
-        p.lse[static_cast<size_t>(bh) * p.s.Nq + qi] =
-            empty ? -INFINITY : (m_used + log2f(l)) * kScoreLn2;
+      store_row<D, C::GROUPS>(p, bh, qi, tmem + lane_off + C::COL_O, g, n_kv > 0, span.hi == 0,
+                              m_used, l);
     }
   }
 
@@ -383,51 +449,12 @@ __global__ void __launch_bounds__(192, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == C::WARPS + 1) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
-// Caps up to here (log2 domain; 55 in scores) have a fixed reference: weights down to
-// 2^-120 and up to 2^40.
-constexpr float kFixedCap = 80.0f;
-
-template <int D, bool CAP, bool BIAS, bool FIXED>
-cudaError_t launch_scores_fwd_t(const ScoreMaps& m, void* o, float* lse, const ScoreParams& s,
-                                cudaStream_t stream) {
-  using C = ScoreFwdCfg<D>;
-  auto kern = fa_scores_fwd_kernel<D, CAP, BIAS, FIXED>;
-  cudaError_t e = set_smem_limit_once<fa_scores_fwd_kernel<D, CAP, BIAS, FIXED>>(C::SMEM_BYTES);
-  if (e != cudaSuccess) return e;
-  ScoreFwdParams p;
-  p.s = s;
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.n_qtiles = (s.Nq + C::BM - 1) / C::BM;
-  p.n_heads = s.B * s.Hq;
-  p.heads_per_group = static_cast<int>(heads_per_group(s.Nk, D, 2.0, s.G, p.n_heads));
-  const long long grid = static_cast<long long>(p.n_heads) * p.n_qtiles;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS),
-                          C::SMEM_BYTES, stream, m.q, m.k, m.v, p);
-}
-
 }  // namespace
-
-template <int D>
-cudaError_t launch_scores_forward(const ScoreMaps& m, void* o, float* lse, const ScoreParams& p,
-                                  int mode, cudaStream_t stream) {
-  switch (mode) {
-    case kScorePlain: return launch_scores_fwd_t<D, false, false, false>(m, o, lse, p, stream);
-    case kScoreBias: return launch_scores_fwd_t<D, false, true, false>(m, o, lse, p, stream);
-    case kScoreCap:
-      if (p.cap2 <= kFixedCap)
-        return launch_scores_fwd_t<D, true, false, true>(m, o, lse, p, stream);
-      [[fallthrough]];  // (no slopes: a slope of 0)
-    default: return launch_scores_fwd_t<D, true, true, false>(m, o, lse, p, stream);
-  }
-}
-
 }  // namespace fa

@@ -1,0 +1,66 @@
+// Launches of the forward with shaped scores: the kernel by its mode, one query tile a CTA or two.
+#pragma once
+
+#include "fa_scores_fwd.cuh"
+#include "fa_scores_fwd2.cuh"
+
+namespace fa {
+namespace {
+
+// Caps up to here (log2 domain; 55 in scores) have a fixed reference: weights down to
+// 2^-120 and up to 2^40.
+constexpr float kFixedCap = 80.0f;
+
+bool two_tiles(const ScoreFwdParams& p) { return getenv("FA_ONE") == nullptr; }
+
+template <int D, bool CAP, bool BIAS, bool FIXED>
+cudaError_t launch_scores_fwd_t(const ScoreMaps& m, void* o, float* lse, const ScoreParams& s,
+                                cudaStream_t stream) {
+  ScoreFwdParams p;
+  p.s = s;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.n_qtiles = (s.Nq + 127) / 128;
+  p.n_heads = s.B * s.Hq;
+  p.heads_per_group = static_cast<int>(heads_per_group(s.Nk, D, 2.0, s.G, p.n_heads));
+  if constexpr (D <= 128 && !FIXED) {
+    if (two_tiles(p)) {
+      using C = ScoreFwd2Cfg<D>;
+      const cudaError_t e =
+          set_smem_limit_once<fa_scores_fwd2_kernel<D, CAP, BIAS, FIXED>>(C::SMEM_BYTES);
+      if (e != cudaSuccess) return e;
+      const long long grid = static_cast<long long>(p.n_heads) * ((p.n_qtiles + 1) / 2);
+      if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+      return launch_dependent(fa_scores_fwd2_kernel<D, CAP, BIAS, FIXED>,
+                              dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), C::SMEM_BYTES,
+                              stream, m.q, m.k, m.v, p);
+    }
+  }
+  using C = ScoreFwdCfg<D, FIXED>;
+  const cudaError_t e =
+      set_smem_limit_once<fa_scores_fwd_kernel<D, CAP, BIAS, FIXED>>(C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const long long grid = static_cast<long long>(p.n_heads) * p.n_qtiles;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_dependent(fa_scores_fwd_kernel<D, CAP, BIAS, FIXED>,
+                          dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), C::SMEM_BYTES,
+                          stream, m.q, m.k, m.v, p);
+}
+
+}  // namespace
+
+template <int D>
+cudaError_t launch_scores_forward(const ScoreMaps& m, void* o, float* lse, const ScoreParams& p,
+                                  int mode, cudaStream_t stream) {
+  switch (mode) {
+    case kScorePlain: return launch_scores_fwd_t<D, false, false, false>(m, o, lse, p, stream);
+    case kScoreBias: return launch_scores_fwd_t<D, false, true, false>(m, o, lse, p, stream);
+    case kScoreCap:
+      if (p.cap2 <= kFixedCap)
+        return launch_scores_fwd_t<D, true, false, true>(m, o, lse, p, stream);
+      [[fallthrough]];  // (no slopes: a slope of 0)
+    default: return launch_scores_fwd_t<D, true, true, false>(m, o, lse, p, stream);
+  }
+}
+
+}  // namespace fa
