@@ -189,7 +189,7 @@ fa_status forward_paged(const fa_paged_cache* cache, const fa_paged_batch* batch
   if (!std::isfinite(s_eff * kPagedLog2e) || !(s_eff > 0.0f)) return FA_ERR_INVALID_ARGUMENT;
   ScoreParams shape;
   if (put_scores(&shape, spec, s_eff) != FA_OK) return FA_ERR_INVALID_ARGUMENT;
-  const bool shaped = shape.cap2 > 0.0f || shape.slopes || shape.window > 0;
+  const bool shaped = shape.f.cap2 > 0.0f || shape.slopes || shape.window > 0;
   if (static_cast<long long>(T) * H_q >= 0x7fffff00LL) return FA_ERR_INVALID_ARGUMENT;
   if (T == 0 || batch->S == 0) return FA_OK;
   if (!q || !o || !aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u))
@@ -239,7 +239,7 @@ fa_status forward_paged(const fa_paged_cache* cache, const fa_paged_batch* batch
   p.min_units = rows == 16 ? 1 : d == 256 ? 2 : 6;
   p.scale_log2 = s_eff * kPagedLog2e;
   p.v_scale = cache->v_descale;
-  p.cap2 = shape.cap2;
+  p.cap2 = shape.f.cap2;
   p.slopes = shape.slopes;
   p.window = shape.window;
   char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) &

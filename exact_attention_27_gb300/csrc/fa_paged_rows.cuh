@@ -119,17 +119,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // Scores of two 8-key tiles (keys key + 8 i + (x & 1); rows by x >> 1) to exponents: products
-// times c capped and lowered (fa_scores.cuh; the tanh as there).  The whole warp calls this.
+// capped (f) and lowered (fa_scores.cuh; the tanh as there).  The whole warp calls this.
 __device__ __forceinline__ void shape_rows(const PagedParams& p, float (&s)[2][4],
-                                           const float (&c)[2], const float (&slope2)[2],
+                                           const ScoreFactors (&f)[2], const float (&slope2)[2],
                                            const float (&pos)[2], int key) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float v[4] = {s[0][2 * h], s[0][2 * h + 1], s[1][2 * h], s[1][2 * h + 1]}, none[1];
     if (p.cap2 > 0.0f)
-      shape_scores<4, true, false, false>(v, none, c[h] / p.cap2, p.cap2, 0.0f, 0.0f, 0.0f);
+      shape_scores<4, true, false, false>(v, none, f[h], 0.0f, 0.0f, 0.0f);
     else
-      shape_scores<4, false, false, false>(v, none, c[h], 0.0f, 0.0f, 0.0f, 0.0f);
+      shape_scores<4, false, false, false>(v, none, f[h], 0.0f, 0.0f, 0.0f);
     if (p.slopes) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -316,6 +316,12 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
           }
         }
       }
+      ScoreFactors factors[2];
+      if constexpr (SHAPED) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          factors[i] = score_factors(p.cap2 > 0.0f ? cs[i] / p.cap2 : cs[i], p.cap2);
+      }
       if constexpr (C::QS) {
         if (kg == 0) {
 #pragma unroll
@@ -388,7 +394,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
               mma16816<false>(s[1], a, b[2], b[3]);
             }
           }
-          if constexpr (SHAPED) shape_rows(p, s, cs, slope2, pos, key0 + 2 * c);
+          if constexpr (SHAPED) shape_rows(p, s, factors, slope2, pos, key0 + 2 * c);
           if (key0 + 15 > all_see || (SHAPED && key0 < from_all)) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)

@@ -210,9 +210,10 @@ __device__ __forceinline__ float paged_softmax(const PagedParams& p, const Paged
   if constexpr (SHAPED) {
     float none[1];
     if (p.cap2 > 0.0f)
-      shape_scores<BN, true, false, false>(s, none, c / p.cap2, p.cap2, 0.0f, 0.0f, 0.0f);
+      shape_scores<BN, true, false, false>(s, none, score_factors(c / p.cap2, p.cap2), 0.0f, 0.0f,
+                                           0.0f);
     else
-      shape_scores<BN, false, false, false>(s, none, c, 0.0f, 0.0f, 0.0f, 0.0f);
+      shape_scores<BN, false, false, false>(s, none, score_factors(c, 0.0f), 0.0f, 0.0f, 0.0f);
     if (p.slopes) lower_scores<BN>(s, x.slope2, static_cast<float>(x.pos - kbase));
     c = 1.0f;
   }

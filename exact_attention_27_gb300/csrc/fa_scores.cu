@@ -37,22 +37,20 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 fa_status put_scores(ScoreParams* p, const fa_score_spec* spec, float scale) {
   p->scale = scale;
-  p->scale2 = scale * kScoreLog2e;
-  p->y_scale = 0.0f;
-  p->cap2 = 0.0f;
+  p->f = score_factors(scale * kScoreLog2e, 0.0f);
   p->slopes = nullptr;
   p->window = 0;
-  if (!std::isfinite(p->scale2) || !(p->scale2 > 0.0f)) return FA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(p->f.k) || !(p->f.k > 0.0f)) return FA_ERR_INVALID_ARGUMENT;
   if (!spec) return FA_OK;
   if (!std::isfinite(spec->softcap) || spec->softcap < 0.0f || spec->window < 0)
     return FA_ERR_INVALID_ARGUMENT;
   if (spec->softcap > 0.0f) {
-    p->y_scale = scale / spec->softcap;
-    p->cap2 = spec->softcap * kScoreLog2e;
-    // (the tanh takes 2 log2(e) y_scale)
-    if (!std::isfinite(3.0f * p->y_scale) || !(p->y_scale >= 1.2e-38f) ||
-        !std::isfinite(2.0f * p->cap2) || !(p->cap2 >= 1.2e-38f))
+    const float k = scale / spec->softcap, cap2 = spec->softcap * kScoreLog2e;
+    // (the tanh takes 2 log2(e) k)
+    if (!std::isfinite(3.0f * k) || !(k >= 1.2e-38f) || !std::isfinite(2.0f * cap2) ||
+        !(cap2 >= 1.2e-38f))
       return FA_ERR_INVALID_ARGUMENT;
+    p->f = score_factors(k, cap2);
   }
   if (!aligned(spec->slopes, 4)) return FA_ERR_INVALID_ARGUMENT;
   p->slopes = spec->slopes;
@@ -61,7 +59,7 @@ fa_status put_scores(ScoreParams* p, const fa_score_spec* spec, float scale) {
 }
 
 int score_mode(const ScoreParams& p) {
-  return (p.cap2 > 0.0f ? kScoreCap : 0) + (p.slopes ? kScoreBias : 0);
+  return (p.f.cap2 > 0.0f ? kScoreCap : 0) + (p.slopes ? kScoreBias : 0);
 }
 
 namespace {

@@ -12,10 +12,11 @@
 //
 // Everything after Q K^T is in the log2 domain (factors of log2(e) are folded in on
 // the host).  The tanh: for |y| <= 0.6, y = x / softcap, as y P(y^2) with P of degree 4,
-// fitted here for the least largest relative error, 7.3e-8 (1.8e-7 with fp32's roundings),
-// eight operations on the FMA pipe in place of the one that scales a score, where one ex2 and
-// one rcp more for each score would take the special-function unit longer than the weights'
-// own exponentials.  (Degree 3 is off by 6e-7 of the cap, which would show in lse.)  A warp
+// fitted here for the least largest relative error, 7.3e-8 (1.8e-7 with fp32's roundings).
+// Its coefficients take in scale / softcap and softcap log2(e) (score_factors), which leaves six
+// operations on the FMA pipe in place of the one that scales a score, where one ex2 and one rcp
+// more for each score would take the special-function unit longer than the weights' own
+// exponentials.  (Degree 3 is off by 6e-7 of the cap, which would show in lse.)  A warp
 // with a score beyond goes by tanh y = 1 - 2 / (e^{2y} + 1), which holds everywhere, to 2e-7.
 #pragma once
 
@@ -32,14 +33,6 @@ namespace fa {
 
 constexpr float kScoreLog2e = 1.4426950408889634f;
 constexpr float kScoreLn2 = 0.6931471805599453f;
-
-// tanh(y) = y (c0 + c1 y^2 + ... + c4 y^8) for |y| <= kTanhRange.
-constexpr float kTanhRange = 0.6f;
-constexpr float kTanhC0 = 0.9999999268681676f;
-constexpr float kTanhC1 = -0.3333230997118056f;
-constexpr float kTanhC2 = 0.13310173624961602f;
-constexpr float kTanhC3 = -0.05210147888220161f;
-constexpr float kTanhC4 = 0.01547542595341364f;
 
 struct KeySpan {
   int lo, hi;  // keys [lo, hi); 0, 0 for a row that sees none
@@ -89,14 +82,14 @@ __device__ __forceinline__ void lower_scores(float (&s)[N], float slope2, float 
 }
 
 // What turns raw products s = q.k of keys kbase + t, t = 0 .. N-1, into exponents of the
-// weights, x (log2 domain), less `sub`:  CAP x = cap2 tanh(s k), else x = s k;
+// weights, x (log2 domain), less `sub`:  CAP x = cap tanh(s k) (in f), else x = s f.k;
 // BIAS then - slope2 |pos - key|, dist0 = pos - kbase.  With GRAD, g gets 1 - tanh^2.  The
-// whole warp calls this (k may differ between its lanes).
+// whole warp calls this (f may differ between its lanes).
 template <int N, bool CAP, bool BIAS, bool GRAD>
-__device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N : 1], float k,
-                                             float cap2, float slope2, float dist0, float sub) {
+__device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N : 1],
+                                             const ScoreFactors& f, float slope2, float dist0,
+                                             float sub) {
   if constexpr (CAP) {
-    const uint64_t k2 = f2_pack(k, k);
     constexpr int CHAINS = N < 16 ? 1 : 4;  // independent maxima
     float part[CHAINS];
 #pragma unroll
@@ -108,31 +101,35 @@ __device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N 
 #pragma unroll
     for (int u = 1; u < CHAINS; ++u) big = fmaxf(big, part[u]);
     // (a NaN takes either way to a NaN)
-    if (__any_sync(0xffffffffu, big * k > kTanhRange)) {
+    if (__any_sync(0xffffffffu, big > f.range)) {
 #pragma unroll
       for (int t = 0; t < N; ++t) {
-        const float r = rcp_approx(ex2_approx(s[t] * (2.0f * kScoreLog2e * k)) + 1.0f);
-        s[t] = fmaf(-2.0f * cap2, r, cap2) - sub;
+        const float r = rcp_approx(ex2_approx(s[t] * (2.0f * kScoreLog2e * f.k)) + 1.0f);
+        s[t] = fmaf(-2.0f * f.cap2, r, f.cap2) - sub;
         if constexpr (GRAD) g[t] = 4.0f * r * (1.0f - r);
       }
     } else {
-      const uint64_t c0 = f2_pack(kTanhC0, kTanhC0), c1 = f2_pack(kTanhC1, kTanhC1);
-      const uint64_t c2 = f2_pack(kTanhC2, kTanhC2), c3 = f2_pack(kTanhC3, kTanhC3);
-      const uint64_t c4 = f2_pack(kTanhC4, kTanhC4);
-      const uint64_t cap = f2_pack(cap2, cap2), ns = f2_pack(-sub, -sub);
-      const uint64_t one = f2_pack(1.0f, 1.0f), minus = f2_pack(-1.0f, -1.0f);
+      const uint64_t a0 = f2_pack(f.a[0], f.a[0]), a1 = f2_pack(f.a[1], f.a[1]);
+      const uint64_t a2 = f2_pack(f.a[2], f.a[2]), a3 = f2_pack(f.a[3], f.a[3]);
+      const uint64_t a4 = f2_pack(f.a[4], f.a[4]), ns = f2_pack(-sub, -sub);
+      const uint64_t one = f2_pack(1.0f, 1.0f), nz = f2_pack(f.neg_inv_cap_sq, f.neg_inv_cap_sq);
 #pragma unroll
       for (int t = 0; t < N; t += 2) {
-        const uint64_t y = f2_mul(f2_pack(s[t], s[t + 1]), k2);
-        const uint64_t y2 = f2_mul(y, y);
-        const uint64_t h = f2_fma(f2_fma(f2_fma(f2_fma(c4, y2, c3), y2, c2), y2, c1), y2, c0);
-        const uint64_t th = f2_mul(y, h);
-        f2_unpack(f2_fma(th, cap, ns), s[t], s[t + 1]);
-        if constexpr (GRAD) f2_unpack(f2_fma(f2_mul(th, minus), th, one), g[t], g[t + 1]);
+        const uint64_t v = f2_pack(s[t], s[t + 1]);
+        const uint64_t v2 = f2_mul(v, v);
+        const uint64_t h =
+            f2_fma(f2_fma(f2_fma(f2_fma(a4, v2, a3), v2, a2), v2, a1), v2, a0);
+        if constexpr (GRAD) {
+          const uint64_t x = f2_mul(v, h);
+          f2_unpack(f2_add(x, ns), s[t], s[t + 1]);
+          f2_unpack(f2_fma(f2_mul(x, x), nz, one), g[t], g[t + 1]);
+        } else {
+          f2_unpack(f2_fma(v, h, ns), s[t], s[t + 1]);
+        }
       }
     }
   } else {
-    const uint64_t c = f2_pack(k, k), ns = f2_pack(-sub, -sub);
+    const uint64_t c = f2_pack(f.k, f.k), ns = f2_pack(-sub, -sub);
 #pragma unroll
     for (int t = 0; t < N; t += 2)
       f2_unpack(f2_fma(f2_pack(s[t], s[t + 1]), c, ns), s[t], s[t + 1]);

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
         float(&x)[CH] = *reinterpret_cast<float(*)[CH]>(&w[c0]);
         float gr[CAP ? CH : 1];
         shape_scores<CH, CAP, BIAS, CAP>(
-            x, gr, p.s.factor(CAP), p.s.cap2, slope_now, dist0 - c0, L2);
+            x, gr, p.s.f, slope_now, dist0 - c0, L2);
 #pragma unroll
         for (int t = 0; t < CH; ++t) x[t] = ex2_approx(x[t]);
         if (masked) {

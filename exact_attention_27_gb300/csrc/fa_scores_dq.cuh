@@ -28,8 +28,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <type_traits>
-
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 #include "fa_scores.cuh"
@@ -334,9 +332,6 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
     for (int j = 0; j < n_kv; ++j) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_SFULL + (j & 1)), (j >> 1) & 1, abort_flag,
                                              err, kErrTimeoutSoftmax));
-      if (ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_DPFULL), j & 1, abort_flag, err,
-                                               kErrTimeoutSoftmax));
       if (!ok) break;
       tc_fence_after();
       const uint32_t scol = C::COL_S + C::BN * (j & 1) + C::KH * g;
@@ -346,64 +341,49 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
       const unsigned from = static_cast<unsigned>(span.lo - kbase);
       const int n_seen = span.hi - span.lo;
       const float dist0 = static_cast<float>(p.s.q_offset + qi - kbase);
+      // A row of one key has P = 1 and dP = D, so dS = 0.
+      const unsigned len = n_seen > 1 || j < n_sum ? static_cast<unsigned>(n_seen) : 0u;
+      // What dP - D is multiplied by (dP where D is summed), from S alone: dP is asked for last,
+      // so that it is there, and its columns are handed back at once.
+      float w[KH];
+      {
+        uint32_t sv[KH];
+        tmem_ld32(tmem + lane_off + scol, sv);
+        tmem_wait_ld();
+#pragma unroll
+        for (int t = 0; t < KH; ++t) w[t] = __uint_as_float(sv[t]);
+      }
       // CH columns at a time: all, or half of them where the tanh's derivative takes registers
       // too (96 a thread).
       constexpr int CH = CAP ? KH / 2 : KH;
-      // (a row of one key: P = 1 and dP = D, so dS = 0)
-      const unsigned seen = static_cast<unsigned>(n_seen);
-      const unsigned len = n_seen > 1 ? seen : 0u;
-      uint32_t pk[KH / 2];
 #pragma unroll
       for (int c0 = 0; c0 < KH; c0 += CH) {
-        float s[CH];
-        uint32_t dpv[CH];
-        {
-          uint32_t sv[CH];
-          tmem_ld<CH>(tmem + lane_off + scol + c0, sv);
-          tmem_ld<CH>(tmem + lane_off + C::COL_DP + KH * g + c0, dpv);
-          tmem_wait_ld();
-#pragma unroll
-          for (int t = 0; t < CH; ++t) s[t] = __uint_as_float(sv[t]);
-        }
-        if (c0 + CH == KH) {
-          tc_fence_before();
-          mbar_arrive_warp(bar(C::B_DPFREE));
-        }
+        float(&x)[CH] = *reinterpret_cast<float(*)[CH]>(&w[c0]);
         float gr[CAP ? CH : 1];
-        shape_scores<CH, CAP, BIAS, CAP>(s, gr, p.s.factor(CAP), p.s.cap2, slope2, dist0 - c0, L2);
-        if (j < n_sum) {
-          // D = sum of P dP, over all parts of the row's keys.
+        shape_scores<CH, CAP, BIAS, CAP>(x, gr, p.s.f, slope2, dist0 - c0, L2);
 #pragma unroll
-          for (int t = 0; t < CH; ++t)
-            if (static_cast<unsigned>(c0 + t) - from < seen)
-              Drow = fmaf(ex2_approx(s[t]), __uint_as_float(dpv[t]), Drow);
-          continue;
+        for (int t = 0; t < CH; t += 2) {
+          uint64_t v = f2_pack(ex2_approx(x[t]), ex2_approx(x[t + 1]));
+          if constexpr (CAP)
+            if (j >= n_sum) v = f2_mul(v, f2_pack(gr[t], gr[t + 1]));
+          f2_unpack(v, x[t], x[t + 1]);
         }
-        // One copy of the loop with the (warp-uniform) mask and one without: a branch inside
-        // the unrolled loop would split it into blocks scheduled one by one.
-        auto ds_pass = [&](auto masked_t) {
-#pragma unroll
-          for (int u = 0; u < CH / 2; ++u) {
-            uint64_t w = f2_pack(ex2_approx(s[2 * u]), ex2_approx(s[2 * u + 1]));
-            if constexpr (CAP) w = f2_mul(w, f2_pack(gr[2 * u], gr[2 * u + 1]));
-            const uint64_t dd =
-                f2_add(f2_pack(__uint_as_float(dpv[2 * u]), __uint_as_float(dpv[2 * u + 1])), nd2);
-            float d0, d1;
-            f2_unpack(f2_mul(w, dd), d0, d1);
-            if constexpr (decltype(masked_t)::value) {
-              if (static_cast<unsigned>(c0 + 2 * u) - from >= len) d0 = 0.0f;
-              if (static_cast<unsigned>(c0 + 2 * u + 1) - from >= len) d1 = 0.0f;
-            }
-            pk[c0 / 2 + u] = pack_bf16x2(d0, d1);
-          }
-        };
-        if (need_mask)
-          ds_pass(std::true_type{});
-        else
-          ds_pass(std::false_type{});
       }
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_DPFULL), j & 1, abort_flag, err,
+                                             kErrTimeoutSoftmax));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t dpv[KH];
+      tmem_ld32(tmem + lane_off + C::COL_DP + KH * g, dpv);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive_warp(bar(C::B_DPFREE));
       if (j < n_sum) {
-        tc_fence_before();
+        // D = sum of P dP, over all parts of the row's keys.
+#pragma unroll
+        for (int t = 0; t < KH; ++t)
+          if (static_cast<unsigned>(t) - from < len)
+            Drow = fmaf(w[t], __uint_as_float(dpv[t]), Drow);
         mbar_arrive_warp(bar(C::B_DSREADY + (j & 1)));
         if (j == n_sum - 1) {
           // The row's parts join: groups 2 and 3 hand theirs to 0 and 1, which all then add.
@@ -423,6 +403,20 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
         }
         continue;
       }
+#pragma unroll
+      for (int t = 0; t < KH; t += 2)
+        f2_unpack(f2_mul(f2_pack(w[t], w[t + 1]),
+                         f2_add(f2_pack(__uint_as_float(dpv[t]), __uint_as_float(dpv[t + 1])),
+                                nd2)),
+                  w[t], w[t + 1]);
+      if (need_mask) {
+#pragma unroll
+        for (int t = 0; t < KH; ++t)
+          if (static_cast<unsigned>(t) - from >= len) w[t] = 0.0f;
+      }
+      uint32_t pk[KH / 2];
+#pragma unroll
+      for (int u = 0; u < KH / 2; ++u) pk[u] = pack_bf16x2(w[2 * u], w[2 * u + 1]);
       // dS (bf16 pairs) over S columns this warp has already read.
       tmem_st16(tmem + lane_off + scol, pk);
       tmem_wait_st();

@@ -98,7 +98,7 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
 #pragma unroll
       for (int t = 0; t < BN; ++t) x[t] = __uint_as_float(r[t]);
     }
-    shape_scores<BN, CAP, BIAS, false>(x, none, p.factor(CAP), p.cap2, slope2,
+    shape_scores<BN, CAP, BIAS, false>(x, none, p.f, slope2,
                                        static_cast<float>(pos - kbase), m);
     if (mask) {
 #pragma unroll
@@ -129,7 +129,7 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
     // Without a tanh or a distance the scale waits for the exponents' multiply-add.
     constexpr bool RAW = !CAP && !BIAS;
     if constexpr (!RAW)
-      shape_scores<BN, CAP, BIAS, false>(s, none, p.factor(CAP), p.cap2, slope2,
+      shape_scores<BN, CAP, BIAS, false>(s, none, p.f, slope2,
                                          static_cast<float>(pos - kbase), 0.0f);
     if (mask) {
 #pragma unroll
@@ -146,7 +146,7 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
       for (int u = 0; u < 8; ++u) pm[u] = fmax3(pm[u], s[t + u], s[t + u + 8]);
     const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]),
                            fmaxf(fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-    const float c = RAW ? p.scale2 : 1.0f;
+    const float c = RAW ? p.f.k : 1.0f;
     const float m_new = fmaxf(m, mx * c);
     // The reference moves only when the maximum has grown by more than the threshold.
     moved = m_new > m + kRescaleThreshold;
@@ -211,7 +211,7 @@ __device__ __forceinline__ void store_row(const ScoreFwdParams& p, int bh, int q
         empty ? -INFINITY : (m + log2f(l)) * kScoreLn2;
 }
 
-// FIXED: the softmax reference is p.s.cap2 / 2.
+// FIXED: the softmax reference is p.s.f.cap2 / 2.
 template <int D, bool CAP, bool BIAS, bool FIXED>
 __global__ void __launch_bounds__((ScoreFwdCfg<D, FIXED>::THREADS), 1)
     fa_scores_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__((ScoreFwdCfg<D, FIXED>::THREADS), 1)
     const int qi = qt * C::BM + row;
     const float slope2 = BIAS && p.s.slopes ? p.s.slopes[hq] * kScoreLog2e : 0.0f;
     const int pos = p.s.q_offset + qi;
-    float m_used = FIXED ? 0.5f * p.s.cap2 : -INFINITY;  // reference, log2 domain
+    float m_used = FIXED ? 0.5f * p.s.f.cap2 : -INFINITY;  // reference, log2 domain
     float l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n_kv; ++j) {

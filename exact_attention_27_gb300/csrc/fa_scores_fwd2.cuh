@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(384, 1)
     const int j1 = x == 0 ? a1 : b1;
     const float slope2 = BIAS && p.s.slopes ? p.s.slopes[hq] * kScoreLog2e : 0.0f;
     const int pos = p.s.q_offset + qi;
-    float m_used = FIXED ? 0.5f * p.s.cap2 : -INFINITY;  // reference, log2 domain
+    float m_used = FIXED ? 0.5f * p.s.f.cap2 : -INFINITY;  // reference, log2 domain
     float l = 0.0f;
     bool ok = true;
     for (int j = j0; j < j1; ++j) {

@@ -10,14 +10,45 @@
 
 namespace fa {
 
+// What a score is multiplied by, and its tanh.
+struct ScoreFactors {
+  float k;      // CAP: the tanh's factor of q.k, scale / softcap; otherwise scale log2(e)
+  float cap2;   // softcap log2(e); 0: none
+  // cap2 tanh(s k) = s (a0 + a1 s^2 + ... + a4 s^8) for |s| <= range (0: never)
+  float a[5];
+  float range;
+  float neg_inv_cap_sq;  // -1 / cap2^2
+};
+
+// tanh(y) = y (c0 + c1 y^2 + ... + c4 y^8) for |y| <= kTanhRange (fa_scores.cuh).
+constexpr float kTanhRange = 0.6f;
+constexpr float kTanhC0 = 0.9999999268681676f;
+constexpr float kTanhC1 = -0.3333230997118056f;
+constexpr float kTanhC2 = 0.13310173624961602f;
+constexpr float kTanhC3 = -0.05210147888220161f;
+constexpr float kTanhC4 = 0.01547542595341364f;
+
+__host__ __device__ inline ScoreFactors score_factors(float k, float cap2) {
+  ScoreFactors f;
+  f.k = k;
+  f.cap2 = cap2;
+  const float k2 = k * k;
+  f.a[0] = kTanhC0 * cap2 * k;
+  f.a[1] = kTanhC1 * cap2 * k * k2;
+  f.a[2] = kTanhC2 * cap2 * k * k2 * k2;
+  f.a[3] = kTanhC3 * cap2 * k * k2 * k2 * k2;
+  f.a[4] = kTanhC4 * cap2 * k * k2 * k2 * k2 * k2;
+  // (where a coefficient leaves fp32's range, the other way always)
+  const float last = f.a[4] < 0.0f ? -f.a[4] : f.a[4];
+  f.range = k2 > 1e-18f && k2 < 1e12f && last > 1e-30f && last < 1e30f ? kTanhRange / k : -1.0f;
+  f.neg_inv_cap_sq = cap2 > 0.0f ? -1.0f / (cap2 * cap2) : 0.0f;
+  return f;
+}
+
 // What the kernels get of fa_score_spec, fa_key_spans and the call's sizes.
 struct ScoreParams {
   float scale;    // of Q K^T
-  float scale2;   // scale log2(e)
-  float y_scale;  // scale / softcap
-  float cap2;     // softcap log2(e); 0: none
-  // The factor of q.k that the kernels take.
-  __host__ __device__ float factor(bool cap) const { return cap ? y_scale : scale2; }
+  ScoreFactors f;
   const float* slopes;  // [Hq], nullptr: none
   const int* first;
   const int* end;

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
       for (int e = 0; e < 32; ++e) pv[e] = __uint_as_float(sv[e]);
       shape_scores<32, CAP, BIAS, CAP>(
-          pv, gr, p.s.factor(CAP), p.s.cap2, slope2,
+          pv, gr, p.s.f, slope2,
           static_cast<float>(p.s.q_offset + it * C::BQ + row - kbase), L2);
 #pragma unroll
       for (int e = 0; e < 32; ++e) pv[e] = ex2_approx(pv[e]);

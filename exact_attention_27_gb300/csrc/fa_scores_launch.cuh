@@ -56,7 +56,7 @@ cudaError_t launch_scores_forward(const ScoreMaps& m, void* o, float* lse, const
     case kScorePlain: return launch_scores_fwd_t<D, false, false, false>(m, o, lse, p, stream);
     case kScoreBias: return launch_scores_fwd_t<D, false, true, false>(m, o, lse, p, stream);
     case kScoreCap:
-      if (p.cap2 <= kFixedCap)
+      if (p.f.cap2 <= kFixedCap)
         return launch_scores_fwd_t<D, true, false, true>(m, o, lse, p, stream);
       [[fallthrough]];  // (no slopes: a slope of 0)
     default: return launch_scores_fwd_t<D, true, true, false>(m, o, lse, p, stream);
