@@ -126,10 +126,13 @@ __device__ __forceinline__ void shape_rows(const PagedParams& p, float (&s)[2][4
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float v[4] = {s[0][2 * h], s[0][2 * h + 1], s[1][2 * h], s[1][2 * h + 1]}, none[1];
+    auto again = [&](float (&y)[4]) {
+      y[0] = s[0][2 * h], y[1] = s[0][2 * h + 1], y[2] = s[1][2 * h], y[3] = s[1][2 * h + 1];
+    };
     if (p.cap2 > 0.0f)
-      shape_scores<4, true, false, false>(v, none, f[h], 0.0f, 0.0f, 0.0f);
+      shape_scores<4, true, false, false>(v, none, f[h], 0.0f, 0.0f, 0.0f, again);
     else
-      shape_scores<4, false, false, false>(v, none, f[h], 0.0f, 0.0f, 0.0f);
+      shape_scores<4, false, false, false>(v, none, f[h], 0.0f, 0.0f, 0.0f, again);
     if (p.slopes) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {

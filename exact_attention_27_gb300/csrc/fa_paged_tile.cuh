@@ -198,22 +198,24 @@ __device__ __forceinline__ float paged_softmax(const PagedParams& p, const Paged
                                                float& m, float& l, bool& moved) {
   const int see = x.last - kbase;
   float s[BN];
-  {
+  auto load = [&](float (&y)[BN]) {
     uint32_t raw[BN];
 #pragma unroll
     for (int q4 = 0; q4 < BN / 32; ++q4)
       tmem_ld32(s_addr + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[q4 * 32]));
     tmem_wait_ld();
 #pragma unroll
-    for (int k = 0; k < BN; ++k) s[k] = __uint_as_float(raw[k]);
-  }
+    for (int k = 0; k < BN; ++k) y[k] = __uint_as_float(raw[k]);
+  };
+  load(s);
   if constexpr (SHAPED) {
     float none[1];
     if (p.cap2 > 0.0f)
       shape_scores<BN, true, false, false>(s, none, score_factors(c / p.cap2, p.cap2), 0.0f, 0.0f,
-                                           0.0f);
+                                           0.0f, load);
     else
-      shape_scores<BN, false, false, false>(s, none, score_factors(c, 0.0f), 0.0f, 0.0f, 0.0f);
+      shape_scores<BN, false, false, false>(s, none, score_factors(c, 0.0f), 0.0f, 0.0f, 0.0f,
+                                            load);
     if (p.slopes) lower_scores<BN>(s, x.slope2, static_cast<float>(x.pos - kbase));
     c = 1.0f;
   }

@@ -11,13 +11,13 @@
 // rows' spans are never visited.
 //
 // Everything after Q K^T is in the log2 domain (factors of log2(e) are folded in on
-// the host).  The tanh: for |y| <= 0.6, y = x / softcap, as y P(y^2) with P of degree 4,
-// fitted here for the least largest relative error, 7.3e-8 (1.8e-7 with fp32's roundings).
-// Its coefficients take in scale / softcap and softcap log2(e) (score_factors), which leaves six
+// the host).  The tanh: for |y| <= 0.4, y = x / softcap, as y P(y^2) with P of degree 3,
+// fitted here for the least largest relative error, 9.8e-8 (2.0e-7 with fp32's roundings).
+// Its coefficients take in scale / softcap and softcap log2(e) (score_factors), which leaves five
 // operations on the FMA pipe in place of the one that scales a score, where one ex2 and one rcp
 // more for each score would take the special-function unit longer than the weights' own
-// exponentials.  (Degree 3 is off by 6e-7 of the cap, which would show in lse.)  A warp
-// with a score beyond goes by tanh y = 1 - 2 / (e^{2y} + 1), which holds everywhere, to 2e-7.
+// exponentials.  A warp with a score beyond goes by tanh y = 1 - 2 / (e^{2y} + 1), which holds
+// everywhere, to 2e-7.  (16 heads of 8192, d = 64, causal: dQ takes 381 us if all go that way.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -84,48 +84,47 @@ __device__ __forceinline__ void lower_scores(float (&s)[N], float slope2, float 
 // What turns raw products s = q.k of keys kbase + t, t = 0 .. N-1, into exponents of the
 // weights, x (log2 domain), less `sub`:  CAP x = cap tanh(s k) (in f), else x = s f.k;
 // BIAS then - slope2 |pos - key|, dist0 = pos - kbase.  With GRAD, g gets 1 - tanh^2.  The
-// whole warp calls this (f may differ between its lanes).
-template <int N, bool CAP, bool BIAS, bool GRAD>
+// whole warp calls this (f may differ between its lanes).  `again` puts the products into s
+// once more, for the warp that finds only after the polynomial that it did not hold (to look
+// first would have all of the arithmetic wait for all of the maxima: 5 % of dQ).
+template <int N, bool CAP, bool BIAS, bool GRAD, typename Again>
 __device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N : 1],
                                              const ScoreFactors& f, float slope2, float dist0,
-                                             float sub) {
+                                             float sub, Again&& again) {
   if constexpr (CAP) {
-    constexpr int CHAINS = N < 16 ? 1 : 4;  // independent maxima
+    constexpr int CHAINS = N < 16 ? 1 : 2;  // independent maxima
     float part[CHAINS];
 #pragma unroll
     for (int u = 0; u < CHAINS; ++u) part[u] = 0.0f;
+    const uint64_t a0 = f2_pack(f.a[0], f.a[0]), a1 = f2_pack(f.a[1], f.a[1]);
+    const uint64_t a2 = f2_pack(f.a[2], f.a[2]), a3 = f2_pack(f.a[3], f.a[3]);
+    const uint64_t ns = f2_pack(-sub, -sub);
+    const uint64_t one = f2_pack(1.0f, 1.0f), nz = f2_pack(f.neg_inv_cap_sq, f.neg_inv_cap_sq);
 #pragma unroll
-    for (int t = 0; t < N; t += 2)
+    for (int t = 0; t < N; t += 2) {
       part[t / 2 % CHAINS] = fmax3_abs(part[t / 2 % CHAINS], s[t], s[t + 1]);
+      const uint64_t v = f2_pack(s[t], s[t + 1]);
+      const uint64_t v2 = f2_mul(v, v);
+      const uint64_t h = f2_fma(f2_fma(f2_fma(a3, v2, a2), v2, a1), v2, a0);
+      if constexpr (GRAD) {
+        const uint64_t x = f2_mul(v, h);
+        f2_unpack(f2_add(x, ns), s[t], s[t + 1]);
+        f2_unpack(f2_fma(f2_mul(x, x), nz, one), g[t], g[t + 1]);
+      } else {
+        f2_unpack(f2_fma(v, h, ns), s[t], s[t + 1]);
+      }
+    }
     float big = part[0];
 #pragma unroll
     for (int u = 1; u < CHAINS; ++u) big = fmaxf(big, part[u]);
     // (a NaN takes either way to a NaN)
     if (__any_sync(0xffffffffu, big > f.range)) {
+      again(s);
 #pragma unroll
       for (int t = 0; t < N; ++t) {
         const float r = rcp_approx(ex2_approx(s[t] * (2.0f * kScoreLog2e * f.k)) + 1.0f);
         s[t] = fmaf(-2.0f * f.cap2, r, f.cap2) - sub;
         if constexpr (GRAD) g[t] = 4.0f * r * (1.0f - r);
-      }
-    } else {
-      const uint64_t a0 = f2_pack(f.a[0], f.a[0]), a1 = f2_pack(f.a[1], f.a[1]);
-      const uint64_t a2 = f2_pack(f.a[2], f.a[2]), a3 = f2_pack(f.a[3], f.a[3]);
-      const uint64_t a4 = f2_pack(f.a[4], f.a[4]), ns = f2_pack(-sub, -sub);
-      const uint64_t one = f2_pack(1.0f, 1.0f), nz = f2_pack(f.neg_inv_cap_sq, f.neg_inv_cap_sq);
-#pragma unroll
-      for (int t = 0; t < N; t += 2) {
-        const uint64_t v = f2_pack(s[t], s[t + 1]);
-        const uint64_t v2 = f2_mul(v, v);
-        const uint64_t h =
-            f2_fma(f2_fma(f2_fma(f2_fma(a4, v2, a3), v2, a2), v2, a1), v2, a0);
-        if constexpr (GRAD) {
-          const uint64_t x = f2_mul(v, h);
-          f2_unpack(f2_add(x, ns), s[t], s[t + 1]);
-          f2_unpack(f2_fma(f2_mul(x, x), nz, one), g[t], g[t + 1]);
-        } else {
-          f2_unpack(f2_fma(v, h, ns), s[t], s[t + 1]);
-        }
       }
     }
   } else {
@@ -145,6 +144,16 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
     tmem_ld16(taddr, r);
   else
     tmem_ld32(taddr, r);
+}
+
+// N products out of TMEM; the whole warp calls this.
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[N]) {
+  uint32_t r[N];
+  tmem_ld<N>(taddr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int t = 0; t < N; ++t) s[t] = __uint_as_float(r[t]);
 }
 
 // Byte offset of 16-byte chunk `ch` of row `r` in a 128-byte-swizzled block of 128-byte rows.

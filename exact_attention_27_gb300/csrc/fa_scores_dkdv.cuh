@@ -311,13 +311,7 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       float w[32];  // scores, then P, and at last what dP - D is multiplied by
-      {
-        uint32_t sv[32];
-        tmem_ld32(tmem + lane_off + C::COL_S + 32 * g, sv);
-        tmem_wait_ld();
-#pragma unroll
-        for (int t = 0; t < 32; ++t) w[t] = __uint_as_float(sv[t]);
-      }
+      load_scores(tmem + lane_off + C::COL_S + 32 * g, w);
       // CH columns at a time: all, or half of them where the tanh's derivative takes registers
       // too (96 a thread).
       constexpr int CH = CAP ? 16 : 32;
@@ -327,7 +321,9 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
         float(&x)[CH] = *reinterpret_cast<float(*)[CH]>(&w[c0]);
         float gr[CAP ? CH : 1];
         shape_scores<CH, CAP, BIAS, CAP>(
-            x, gr, p.s.f, slope_now, dist0 - c0, L2);
+            x, gr, p.s.f, slope_now, dist0 - c0, L2, [&](float (&y)[CH]) {
+              load_scores(tmem + lane_off + C::COL_S + 32 * g + c0, y);
+            });
 #pragma unroll
         for (int t = 0; t < CH; ++t) x[t] = ex2_approx(x[t]);
         if (masked) {

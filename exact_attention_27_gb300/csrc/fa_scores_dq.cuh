@@ -346,13 +346,7 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
       // What dP - D is multiplied by (dP where D is summed), from S alone: dP is asked for last,
       // so that it is there, and its columns are handed back at once.
       float w[KH];
-      {
-        uint32_t sv[KH];
-        tmem_ld32(tmem + lane_off + scol, sv);
-        tmem_wait_ld();
-#pragma unroll
-        for (int t = 0; t < KH; ++t) w[t] = __uint_as_float(sv[t]);
-      }
+      load_scores(tmem + lane_off + scol, w);
       // CH columns at a time: all, or half of them where the tanh's derivative takes registers
       // too (96 a thread).
       constexpr int CH = CAP ? KH / 2 : KH;
@@ -360,7 +354,9 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
       for (int c0 = 0; c0 < KH; c0 += CH) {
         float(&x)[CH] = *reinterpret_cast<float(*)[CH]>(&w[c0]);
         float gr[CAP ? CH : 1];
-        shape_scores<CH, CAP, BIAS, CAP>(x, gr, p.s.f, slope2, dist0 - c0, L2);
+        shape_scores<CH, CAP, BIAS, CAP>(x, gr, p.s.f, slope2, dist0 - c0, L2, [&](float (&y)[CH]) {
+          load_scores(tmem + lane_off + scol + c0, y);
+        });
 #pragma unroll
         for (int t = 0; t < CH; t += 2) {
           uint64_t v = f2_pack(ex2_approx(x[t]), ex2_approx(x[t + 1]));

@@ -89,17 +89,20 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
 #pragma unroll
   for (int u = 0; u < 4; ++u) ps2[u] = 0ull;
   float alpha = 1.0f;
+  auto load = [&](float (&x)[BN]) {
+    uint32_t r[BN];
+#pragma unroll
+    for (int c = 0; c < BN / 32; ++c)
+      tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
+    tmem_wait_ld();
+#pragma unroll
+    for (int t = 0; t < BN; ++t) x[t] = __uint_as_float(r[t]);
+  };
   if constexpr (FIXED) {
     float x[BN], none[1];
-    {
-      uint32_t r[BN];
-      tmem_ld<BN>(s_addr, r);
-      tmem_wait_ld();
-#pragma unroll
-      for (int t = 0; t < BN; ++t) x[t] = __uint_as_float(r[t]);
-    }
+    load(x);
     shape_scores<BN, CAP, BIAS, false>(x, none, p.f, slope2,
-                                       static_cast<float>(pos - kbase), m);
+                                       static_cast<float>(pos - kbase), m, load);
     if (mask) {
 #pragma unroll
       for (int t = 0; t < BN; ++t)
@@ -117,20 +120,12 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
     tmem_st16(s_addr, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
   } else {
     float s[BN], none[1];
-    {
-      uint32_t r[BN];
-#pragma unroll
-      for (int q4 = 0; q4 < BN / 32; ++q4)
-        tmem_ld32(s_addr + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[q4 * 32]));
-      tmem_wait_ld();
-#pragma unroll
-      for (int t = 0; t < BN; ++t) s[t] = __uint_as_float(r[t]);
-    }
+    load(s);
     // Without a tanh or a distance the scale waits for the exponents' multiply-add.
     constexpr bool RAW = !CAP && !BIAS;
     if constexpr (!RAW)
       shape_scores<BN, CAP, BIAS, false>(s, none, p.f, slope2,
-                                         static_cast<float>(pos - kbase), 0.0f);
+                                         static_cast<float>(pos - kbase), 0.0f, load);
     if (mask) {
 #pragma unroll
       for (int t = 0; t < BN; ++t)

@@ -14,19 +14,18 @@ namespace fa {
 struct ScoreFactors {
   float k;      // CAP: the tanh's factor of q.k, scale / softcap; otherwise scale log2(e)
   float cap2;   // softcap log2(e); 0: none
-  // cap2 tanh(s k) = s (a0 + a1 s^2 + ... + a4 s^8) for |s| <= range (0: never)
-  float a[5];
+  // cap2 tanh(s k) = s (a0 + a1 s^2 + a2 s^4 + a3 s^6) for |s| <= range (below 0: never)
+  float a[4];
   float range;
   float neg_inv_cap_sq;  // -1 / cap2^2
 };
 
-// tanh(y) = y (c0 + c1 y^2 + ... + c4 y^8) for |y| <= kTanhRange (fa_scores.cuh).
-constexpr float kTanhRange = 0.6f;
-constexpr float kTanhC0 = 0.9999999268681676f;
-constexpr float kTanhC1 = -0.3333230997118056f;
-constexpr float kTanhC2 = 0.13310173624961602f;
-constexpr float kTanhC3 = -0.05210147888220161f;
-constexpr float kTanhC4 = 0.01547542595341364f;
+// tanh(y) = y (c0 + c1 y^2 + c2 y^4 + c3 y^6) for |y| <= kTanhRange (fa_scores.cuh).
+constexpr float kTanhRange = 0.4f;
+constexpr float kTanhC0 = 0.9999999019009195f;
+constexpr float kTanhC1 = -0.33331362458867403f;
+constexpr float kTanhC2 = 0.13270976757985897f;
+constexpr float kTanhC3 = -0.04755360359006216f;
 
 __host__ __device__ inline ScoreFactors score_factors(float k, float cap2) {
   ScoreFactors f;
@@ -37,9 +36,8 @@ __host__ __device__ inline ScoreFactors score_factors(float k, float cap2) {
   f.a[1] = kTanhC1 * cap2 * k * k2;
   f.a[2] = kTanhC2 * cap2 * k * k2 * k2;
   f.a[3] = kTanhC3 * cap2 * k * k2 * k2 * k2;
-  f.a[4] = kTanhC4 * cap2 * k * k2 * k2 * k2 * k2;
   // (where a coefficient leaves fp32's range, the other way always)
-  const float last = f.a[4] < 0.0f ? -f.a[4] : f.a[4];
+  const float last = f.a[3] < 0.0f ? -f.a[3] : f.a[3];
   f.range = k2 > 1e-18f && k2 < 1e12f && last > 1e-30f && last < 1e30f ? kTanhRange / k : -1.0f;
   f.neg_inv_cap_sq = cap2 > 0.0f ? -1.0f / (cap2 * cap2) : 0.0f;
   return f;

@@ -301,11 +301,18 @@ def test_captured_steps_see_new_spans():
 
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_masked_keys_may_hold_anything(d):
-    """Scores of keys that no row sees never count, whatever k holds there (v must be finite)."""
+    """Scores of keys that no row sees never count, whatever k holds there (v must be finite): the
+    values and bounds are those of the finite k.  (Not the bits: of the two ways to a tanh, each
+    within 2e-7, a warp takes the one that all of its scores allow, masked ones among them.)"""
     N = 200
     p = Problem(1, 2, 1, N, d, end=i32([[150] * N]), softcap=20.0, seed=6)
-    q = p.run()
-    p.k[:, :, 150:] = float("inf")
-    o = p.run()
-    for name in ("o", "lse", "dv"):
-        assert torch.equal(q[name], o[name]), name
+    k = p.k.clone()
+    for far in (float("inf"), float("nan"), 1e30):
+        p.k[:, :, 150:] = far
+        got = p.run()
+        p.k = k.clone()
+        if not math.isfinite(far):  # dk of such keys is 0, and dq never takes them in
+            got["dq"] = None
+        val, tol = whole(p.q, p.k, p.v, p.see(), p.scale, p.softcap, do=p.do)
+        for name in ("o", "lse", "dv", "dk"):
+            assert off_by(got[name], val[name], tol[name]) <= 1, name
