@@ -34,7 +34,7 @@ __all__ = [
     "fa_paged_append", "fa_forward_paged", "paged_workspace", "rotary_forward", "rotary_backward",
     "paged_append", "paged_attention", "Scores", "KeySpans", "fa_forward_scores",
     "fa_backward_scores", "HeadNorm", "fa_norm_rotary", "fa_norm_rotary_backward",
-    "norm_rotary_workspace", "norm_rotary_forward", "norm_rotary_backward",
+    "norm_rotary_workspace", "scores_workspace", "norm_rotary_forward", "norm_rotary_backward",
 ]
 
 FA_OK = 0
@@ -271,10 +271,12 @@ def attention_backward(q, k, v, o, lse, do, causal=False, scale=None, determinis
         if stream is not None:
             with _on(stream):
                 grads = tuple(torch.empty_like(t) for t in (q, k, v))
+                workspace = scores_workspace(q, k, causal, q_offset or 0)
         else:
             grads = tuple(torch.empty_like(t) for t in (q, k, v))
-        fa_backward_scores(q, k, v, o, lse, do, *grads, scale, causal, q_offset or 0, scores, spans,
-                           stream)
+            workspace = scores_workspace(q, k, causal, q_offset or 0)
+        fa_backward_scores(q, k, v, o, lse, do, *grads, scale, causal, workspace, q_offset or 0,
+                           scores, spans, stream)
         return grads
     dq = torch.empty_like(q)
     dk = torch.empty_like(k)
@@ -289,4 +291,5 @@ from .paged import (_on, HeadNorm, PagedBatch, PagedCache, Rotary, fa_forward_pa
                     fa_rotary_backward, norm_rotary_backward, norm_rotary_forward,
                     norm_rotary_workspace, paged_append, paged_attention, paged_workspace,
                     rotary_backward, rotary_forward)
-from .scores import KeySpans, Scores, fa_backward_scores, fa_forward_scores  # noqa: E402
+from .scores import (KeySpans, Scores, fa_backward_scores, fa_forward_scores,  # noqa: E402
+                     scores_workspace)

@@ -106,7 +106,9 @@ def _declare(lib):
     lib.fa_forward_scores.argtypes = [p, p, p, p, p, i, i, i, i, i, i, f, i, i, p, p, p]
     lib.fa_backward_scores.restype = i
     lib.fa_backward_scores.argtypes = [p, p, p, p, p, p, p, p, p, i, i, i, i, i, i, f, i, i, p, p,
-                                       p]
+                                       p, ctypes.c_size_t, p]
+    lib.fa_backward_scores_workspace_bytes.restype = ctypes.c_size_t
+    lib.fa_backward_scores_workspace_bytes.argtypes = [i, i, i, i, i, i, i, i]
     for name in ("fa_rotary", "fa_rotary_backward"):
         fn = getattr(lib, name)
         fn.restype = i

@@ -119,20 +119,21 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // Scores of two 8-key tiles (keys key + 8 i + (x & 1); rows by x >> 1) to exponents: products
-// capped (f) and lowered (fa_scores.cuh; the tanh as there).  The whole warp calls this.
+// times `by` (capped: scale / softcap, see paged_softmax), capped and lowered (fa_scores.cuh; the
+// tanh as there).  The whole warp calls this.
 __device__ __forceinline__ void shape_rows(const PagedParams& p, float (&s)[2][4],
-                                           const ScoreFactors (&f)[2], const float (&slope2)[2],
-                                           const float (&pos)[2], int key) {
+                                           const ScoreFactors& f, const float (&by)[2],
+                                           const float (&slope2)[2], const float (&pos)[2],
+                                           int key) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float v[4] = {s[0][2 * h], s[0][2 * h + 1], s[1][2 * h], s[1][2 * h + 1]}, none[1];
-    auto again = [&](float (&y)[4]) {
-      y[0] = s[0][2 * h], y[1] = s[0][2 * h + 1], y[2] = s[1][2 * h], y[3] = s[1][2 * h + 1];
+    float v[4], none[1];
+    auto load = [&](float (&y)[4]) {
+      y[0] = s[0][2 * h] * by[h], y[1] = s[0][2 * h + 1] * by[h];
+      y[2] = s[1][2 * h] * by[h], y[3] = s[1][2 * h + 1] * by[h];
     };
-    if (p.cap2 > 0.0f)
-      shape_scores<4, true, false, false>(v, none, f[h], 0.0f, 0.0f, 0.0f, again);
-    else
-      shape_scores<4, false, false, false>(v, none, f[h], 0.0f, 0.0f, 0.0f, again);
+    load(v);
+    if (p.cap2 > 0.0f) shape_scores<4, true, false, false>(v, none, f, 0.0f, 0.0f, 0.0f, load);
     if (p.slopes) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -319,11 +320,12 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
           }
         }
       }
-      ScoreFactors factors[2];
+      ScoreFactors factors;
+      float by[2];
       if constexpr (SHAPED) {
+        factors = score_factors(1.0f, p.cap2);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          factors[i] = score_factors(p.cap2 > 0.0f ? cs[i] / p.cap2 : cs[i], p.cap2);
+        for (int i = 0; i < 2; ++i) by[i] = p.cap2 > 0.0f ? cs[i] / p.cap2 : cs[i];
       }
       if constexpr (C::QS) {
         if (kg == 0) {
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
               mma16816<false>(s[1], a, b[2], b[3]);
             }
           }
-          if constexpr (SHAPED) shape_rows(p, s, factors, slope2, pos, key0 + 2 * c);
+          if constexpr (SHAPED) shape_rows(p, s, factors, by, slope2, pos, key0 + 2 * c);
           if (key0 + 15 > all_see || (SHAPED && key0 < from_all)) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)

@@ -198,26 +198,36 @@ __device__ __forceinline__ float paged_softmax(const PagedParams& p, const Paged
                                                float& m, float& l, bool& moved) {
   const int see = x.last - kbase;
   float s[BN];
-  auto load = [&](float (&y)[BN]) {
+  if constexpr (SHAPED) {
+    // 32 columns at a time: fewer registers than all at once.  A row's c may be far from 1 (over
+    // e4m3 pages it takes in a power of two of q): the products are brought to the tanh's
+    // argument first, so that its coefficients keep within fp32.
+    const bool cap = p.cap2 > 0.0f;
+    const ScoreFactors f = score_factors(1.0f, p.cap2);
+    const float by = cap ? c / p.cap2 : c;
+#pragma unroll
+    for (int c0 = 0; c0 < BN; c0 += 32) {
+      float(&y)[32] = *reinterpret_cast<float(*)[32]>(&s[c0]);
+      float none[1];
+      auto load = [&](float (&z)[32]) {
+        load_scores(s_addr + c0, z);
+        const uint64_t by2 = f2_pack(by, by);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) f2_unpack(f2_mul(f2_pack(z[k], z[k + 1]), by2), z[k], z[k + 1]);
+      };
+      load(y);
+      if (cap) shape_scores<32, true, false, false>(y, none, f, 0.0f, 0.0f, 0.0f, load);
+      if (p.slopes) lower_scores<32>(y, x.slope2, static_cast<float>(x.pos - kbase - c0));
+    }
+    c = 1.0f;
+  } else {
     uint32_t raw[BN];
 #pragma unroll
     for (int q4 = 0; q4 < BN / 32; ++q4)
       tmem_ld32(s_addr + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[q4 * 32]));
     tmem_wait_ld();
 #pragma unroll
-    for (int k = 0; k < BN; ++k) y[k] = __uint_as_float(raw[k]);
-  };
-  load(s);
-  if constexpr (SHAPED) {
-    float none[1];
-    if (p.cap2 > 0.0f)
-      shape_scores<BN, true, false, false>(s, none, score_factors(c / p.cap2, p.cap2), 0.0f, 0.0f,
-                                           0.0f, load);
-    else
-      shape_scores<BN, false, false, false>(s, none, score_factors(c, 0.0f), 0.0f, 0.0f, 0.0f,
-                                            load);
-    if (p.slopes) lower_scores<BN>(s, x.slope2, static_cast<float>(x.pos - kbase));
-    c = 1.0f;
+    for (int k = 0; k < BN; ++k) s[k] = __uint_as_float(raw[k]);
   }
   if (mask) {
 #pragma unroll

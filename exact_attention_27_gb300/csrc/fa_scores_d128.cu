@@ -10,7 +10,7 @@ template cudaError_t launch_scores_forward<128>(const ScoreMaps&, void*, float*,
 template cudaError_t launch_scores_dq<128>(const ScoreMaps&, const float*, float*, void*,
                                           const ScoreParams&, int, cudaStream_t);
 template cudaError_t launch_scores_dkdv<128>(const ScoreMaps&, const float*, const float*,
-                                            const int2*, void*, void*, const ScoreParams&, int,
-                                            cudaStream_t);
+                                            const int2*, void*, void*, float*, int,
+                                            const ScoreParams&, int, cudaStream_t);
 
 }  // namespace fa

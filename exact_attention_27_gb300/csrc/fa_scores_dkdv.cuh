@@ -10,7 +10,7 @@
 // Queries lie on the tensor-memory lanes, so that L, D, the span and the position of a row
 // are registers of its thread (with keys there, as in fa_bwd.cu, a thread would read four
 // values of each query from shared memory, where the mask and the tanh leave no room for L
-// and D to enter through the products).  Two threads share a row, 64 keys each.
+// and D to enter through the products).  Four threads share a row, 32 keys each.
 //
 // Order of the products: S(0) dP(0), then per step dV(s) S(s+1) dK(s) dP(s+1); dV and S(s+1)
 // wait for P(s) (S has been read then), dK and dP(s+1) for dS(s).  The P buffer is free when
@@ -18,7 +18,11 @@
 // read them, issued before by the same thread.  The threads work on dS(s) while dV(s) and
 // S(s+1) run, and on P(s+1) while dK(s) and dP(s+1) do.
 //
-// Warps: 0-7 query rows (warp w: rows 32 (w % 4).., keys 64 (w / 4)..), 8 TMA, 9 MMA issuer and
+// Few or unequal key tiles (one head's, a group's under the causal mask) are shared by `split`
+// CTAs each, which take equal stretches of its steps and leave fp32 sums that a second kernel
+// adds in order (fa_scores.cu says when): results repeat to the bit.
+//
+// Warps: 0-15 query rows (warp w: rows 32 (w % 4).., keys 32 (w / 4)..), 16 TMA, 17 MMA issuer and
 // tensor-memory owner.  Tensor memory: S [0,128), dP [128,256), dV [256, 256+DP), dK after it.
 
 #include <cuda.h>
@@ -80,6 +84,8 @@ struct ScoreDkdvParams {
   const int2* tiles;  // [B][n_qtiles] union of the spans of a query tile's rows
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
+  float* part;  // [2][split][B Hkv][Nk][D] sums for dV and dK of `split` CTAs a key tile; 1: none
+  int split;
   int n_qtiles, n_ktiles;
 };
 
@@ -102,10 +108,13 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
   uint32_t* err = p.s.err;
 
   const int warp = threadIdx.x >> 5;
-  // The first key tiles (the most query tiles, where the mask is causal) of all heads first.
+  // The first key tiles (the most query tiles, where the mask is causal) of all heads first,
+  // the CTAs that share a key tile next to each other.
   const int n_units = p.s.B * p.s.Hkv;
-  const int jt = static_cast<int>(blockIdx.x) / n_units;
-  const int kvz = static_cast<int>(blockIdx.x) - jt * n_units;  // flattened (batch, kv head)
+  const int unit = static_cast<int>(blockIdx.x) / p.split;
+  const int share = static_cast<int>(blockIdx.x) - unit * p.split;
+  const int jt = unit / n_units;
+  const int kvz = unit - jt * n_units;                          // flattened (batch, kv head)
   const int b = kvz / p.s.Hkv;
   const int bh0 = b * p.s.Hq + (kvz - b * p.s.Hkv) * p.s.G;     // first query head of the group
 
@@ -139,10 +148,13 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
   // Query tiles that see these keys: i0 .. i0 + per_head - 1 of each head.
   const int i0 = range[1] > 0 ? range[0] : 0;
   const int per_head = range[1] > 0 ? range[1] - i0 : 0;
-  const int n_steps = p.s.G * per_head;
+  // This CTA's steps of the G per_head there are.
+  const long long all = static_cast<long long>(p.s.G) * per_head;
+  const int step0 = static_cast<int>(all * share / p.split);
+  const int n_steps = static_cast<int>(all * (share + 1) / p.split) - step0;
   auto step_coords = [&](int s, int& bhq, int& it) {
-    const int g = s / per_head;
-    it = i0 + (s - g * per_head);
+    const int g = (step0 + s) / per_head;
+    it = i0 + (step0 + s - g * per_head);
     bhq = bh0 + g;
   };
 
@@ -272,8 +284,10 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
     // L, D and the span of this thread's row, loaded one step ahead; steps go through the query
     // tiles i0 .. i1 - 1 of one head after the other.
     const int i1 = i0 + per_head;
-    const float* lse = p.lse + static_cast<size_t>(bh0) * p.s.Nq;  // of the next step's head
-    const float* dvec = p.Dvec + static_cast<size_t>(bh0) * p.s.Nq;
+    int bhq0 = bh0, it = i0;
+    if (n_steps > 0) step_coords(0, bhq0, it);
+    const float* lse = p.lse + static_cast<size_t>(bhq0) * p.s.Nq;  // of the next step's head
+    const float* dvec = p.Dvec + static_cast<size_t>(bhq0) * p.s.Nq;
     auto load_row = [&](int it, float& l, float& dd, KeySpan& span) {
       const int q = it * C::BQ + row;
       span = row_span(p.s, b, q);
@@ -283,8 +297,8 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
     };
     float l_cur = 0.0f, d_cur = 0.0f;
     KeySpan span_cur{0, 0};
-    if (n_steps > 0) load_row(i0, l_cur, d_cur, span_cur);
-    int it = i0, head = bh0 - b * p.s.Hq;
+    if (n_steps > 0) load_row(it, l_cur, d_cur, span_cur);
+    int head = bhq0 - b * p.s.Hq;
     float slope2 = BIAS && p.s.slopes ? p.s.slopes[head] * kScoreLog2e : 0.0f;
     bool ok = true;
     for (int s = 0; s < n_steps; ++s) {
@@ -391,8 +405,10 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
       const uint32_t col0 = is_dv ? C::COL_DV : C::COL_DK;
       const int key = jt * C::BK + row;
       const bool live = key < p.s.Nk;
-      __nv_bfloat16* out = (is_dv ? p.dv : p.dk) +
-                           (static_cast<size_t>(kvz) * p.s.Nk + (live ? key : 0)) * D;
+      const size_t at = (static_cast<size_t>(kvz) * p.s.Nk + (live ? key : 0)) * D;
+      __nv_bfloat16* out = (is_dv ? p.dv : p.dk) + at;
+      float* part = p.part + at + static_cast<size_t>((is_dv ? 0 : p.split) + share) * n_units *
+                                      p.s.Nk * D;
 #pragma unroll 1
       for (int q4 = g & 1; q4 < D / 32; q4 += 2) {
         uint32_t r[32];
@@ -402,6 +418,17 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
         } else {
 #pragma unroll
           for (int u = 0; u < 32; ++u) r[u] = 0u;  // no query sees these keys
+        }
+        if (p.split > 1) {
+          if (live) {
+            float4* dst = reinterpret_cast<float4*>(part + q4 * 32);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[u] = make_float4(
+                  __uint_as_float(r[4 * u]) * mul, __uint_as_float(r[4 * u + 1]) * mul,
+                  __uint_as_float(r[4 * u + 2]) * mul, __uint_as_float(r[4 * u + 3]) * mul);
+          }
+          continue;
         }
         uint32_t pk[16];
 #pragma unroll
@@ -431,8 +458,8 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
 
 template <int D, bool CAP, bool BIAS>
 cudaError_t launch_scores_dkdv_t(const ScoreMaps& m, const float* lse, const float* Dv,
-                                 const int2* tiles, void* dk, void* dv, const ScoreParams& s,
-                                 cudaStream_t stream) {
+                                 const int2* tiles, void* dk, void* dv, float* part, int split,
+                                 const ScoreParams& s, cudaStream_t stream) {
   using C = ScoreDkdvCfg<D>;
   auto kern = fa_scores_dkdv_kernel<D, CAP, BIAS>;
   cudaError_t e = set_smem_limit_once<fa_scores_dkdv_kernel<D, CAP, BIAS>>(C::SMEM_BYTES);
@@ -444,9 +471,11 @@ cudaError_t launch_scores_dkdv_t(const ScoreMaps& m, const float* lse, const flo
   p.tiles = tiles;
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.part = part;
+  p.split = split;
   p.n_qtiles = (s.Nq + C::BQ - 1) / C::BQ;
   p.n_ktiles = (s.Nk + C::BK - 1) / C::BK;
-  const long long grid = static_cast<long long>(p.n_ktiles) * s.B * s.Hkv;
+  const long long grid = static_cast<long long>(p.n_ktiles) * s.B * s.Hkv * split;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS),
                           C::SMEM_BYTES, stream, m.q, m.k, m.v, m.dO, p);
@@ -456,16 +485,16 @@ cudaError_t launch_scores_dkdv_t(const ScoreMaps& m, const float* lse, const flo
 
 template <int D>
 cudaError_t launch_scores_dkdv(const ScoreMaps& m, const float* lse, const float* Dv,
-                               const int2* tiles, void* dk, void* dv, const ScoreParams& p,
-                               int mode, cudaStream_t stream) {
+                               const int2* tiles, void* dk, void* dv, float* part, int split,
+                               const ScoreParams& p, int mode, cudaStream_t stream) {
   switch (mode) {
     case kScorePlain:
-      return launch_scores_dkdv_t<D, false, false>(m, lse, Dv, tiles, dk, dv, p, stream);
+      return launch_scores_dkdv_t<D, false, false>(m, lse, Dv, tiles, dk, dv, part, split, p, stream);
     case kScoreBias:
-      return launch_scores_dkdv_t<D, false, true>(m, lse, Dv, tiles, dk, dv, p, stream);
+      return launch_scores_dkdv_t<D, false, true>(m, lse, Dv, tiles, dk, dv, part, split, p, stream);
     case kScoreCap:
-      return launch_scores_dkdv_t<D, true, false>(m, lse, Dv, tiles, dk, dv, p, stream);
-    default: return launch_scores_dkdv_t<D, true, true>(m, lse, Dv, tiles, dk, dv, p, stream);
+      return launch_scores_dkdv_t<D, true, false>(m, lse, Dv, tiles, dk, dv, part, split, p, stream);
+    default: return launch_scores_dkdv_t<D, true, true>(m, lse, Dv, tiles, dk, dv, part, split, p, stream);
   }
 }
 

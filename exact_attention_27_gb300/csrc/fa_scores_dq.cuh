@@ -9,12 +9,13 @@
 //   dQ  += dS K_j             tcgen05.mma, A = dS (bf16) from tensor memory
 // and at the end dq = bf16(scale dQ): no atomics, so the bits repeat.
 //
-// D = rowsum(dO o O) is off by O's rounding to bf16, which shows in dS where a row sees few
-// keys (|O| is then as large as |V|, and dP - D far smaller than D).  So a CTA with at most
-// 384 keys goes through them twice and sums D = sum_j P dP first (three keys a row,
-// distance slopes: dQ off by 0.0055 of its norm without, 0.0017 of which is its own rounding),
-// and leaves that D to the dK/dV kernel, which runs after this one.  A row that sees one key has
-// dS = 0.
+// D = rowsum(dO o O) is off by O's rounding to bf16, which shows in dS where the weights lie on
+// few keys (|O| is then as large as |V|, and dP - D far smaller than D).  So a CTA with at most
+// 1024 keys goes through them twice and sums D = sum_j P dP first, and leaves that D to the dK/dV
+// kernel, which runs after this one.  (Errors relative to dq's norm, 0.0017 of which is its own
+// rounding and as much dS's: three keys a row, slopes: 0.0055 -> 0.0024; packed documents of 100 to
+// 2000 positions: 0.0026 -> 0.0024, for a third more of this kernel's time.  One of 8192 keys,
+// causal: 1 % more.)  A row that sees one key has dS = 0.
 //
 // Pipeline as in fa_bwd_dq.cu: S_j in one of two tensor-memory buffers, dP_j in one that the
 // row warps hand back as soon as they hold its values, dS_j over the S columns they have
@@ -44,7 +45,7 @@ struct ScoreDqCfg {
   static constexpr int DP = (D + 63) / 64 * 64;  // padded head dimension
   static constexpr int BM = 128;                 // query rows per CTA
   static constexpr int BN = (D == 256) ? 64 : 128;  // keys per tile
-  static constexpr int EXACT_TILES = 3 * 128 / BN;
+  static constexpr int EXACT_TILES = 1024 / BN;
   static constexpr int KH = 32;                  // key columns per row warp
   static constexpr int GROUPS = BN / KH;         // row warps that share a row
   static constexpr int WARPS = 4 * GROUPS;       // row warps; then TMA and MMA

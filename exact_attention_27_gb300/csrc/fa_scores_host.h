@@ -75,12 +75,12 @@ cudaError_t launch_scores_forward(const ScoreMaps& m, void* o, float* lse, const
                                   int mode, cudaStream_t stream);
 template <int D>
 cudaError_t launch_scores_dkdv(const ScoreMaps& m, const float* lse, const float* Dv,
-                               const int2* tiles, void* dk, void* dv, const ScoreParams& p,
-                               int mode, cudaStream_t stream);
+                               const int2* tiles, void* dk, void* dv, float* part, int split,
+                               const ScoreParams& p, int mode, cudaStream_t stream);
 template <>
 cudaError_t launch_scores_dkdv<256>(const ScoreMaps& m, const float* lse, const float* Dv,
-                                    const int2* tiles, void* dk, void* dv, const ScoreParams& p,
-                                    int mode, cudaStream_t stream);
+                                    const int2* tiles, void* dk, void* dv, float* part, int split,
+                                    const ScoreParams& p, int mode, cudaStream_t stream);
 template <int D>
 cudaError_t launch_scores_dq(const ScoreMaps& m, const float* lse, float* Dv, void* dq,
                              const ScoreParams& p, int mode, cudaStream_t stream);

@@ -74,6 +74,8 @@ struct ScoreKv256Params {
   const int2* tiles;  // [B][n_qtiles] union of the spans of a query tile's rows
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
+  float* part;  // [2][split][B Hkv][Nk][256] sums for dV and dK of `split` CTAs a key tile
+  int split;
   int n_qtiles, n_ktiles;
 };
 
@@ -96,10 +98,13 @@ __global__ void __launch_bounds__(320, 1)
   uint32_t* err = p.s.err;
 
   const int warp = threadIdx.x >> 5;
-  // Heaviest key tiles (most query tiles under the causal mask) first.
-  const int n_kv_units = static_cast<int>(gridDim.x) / p.n_ktiles;
-  const int jt = static_cast<int>(blockIdx.x) / n_kv_units;
-  const int kvz = static_cast<int>(blockIdx.x) - jt * n_kv_units;  // flattened (batch, kv head)
+  // The first key tiles (the most query tiles, where the mask is causal) of all heads first,
+  // the CTAs that share a key tile (as in fa_scores_dkdv.cuh) next to each other.
+  const int n_units = p.s.B * p.s.Hkv;
+  const int unit = static_cast<int>(blockIdx.x) / p.split;
+  const int share = static_cast<int>(blockIdx.x) - unit * p.split;
+  const int jt = unit / n_units;
+  const int kvz = unit - jt * n_units;  // flattened (batch, kv head)
   const int b = kvz / p.s.Hkv;
   const int hkv = kvz - b * p.s.Hkv;
 
@@ -111,11 +116,11 @@ __global__ void __launch_bounds__(320, 1)
   const uint32_t sDS = sbase + C::OFF_DS;
 
   // Query tiles that see these keys: i0 .. i0 + per_head - 1 of each head.
-  int i0 = 0, per_head = 0, n_steps = 0;
+  int i0 = 0, per_head = 0, n_steps = 0, step0 = 0;
   // step -> (flattened query head, query tile)
   auto step_coords = [&](int s, int& bhq, int& it) {
-    const int g = s / per_head;
-    it = i0 + (s - g * per_head);
+    const int g = (step0 + s) / per_head;
+    it = i0 + (step0 + s - g * per_head);
     bhq = b * p.s.Hq + hkv * p.s.G + g;
   };
 
@@ -147,7 +152,9 @@ __global__ void __launch_bounds__(320, 1)
     i0 = range[0];
     per_head = range[1] - i0;
   }
-  n_steps = p.s.G * per_head;
+  const long long all = static_cast<long long>(p.s.G) * per_head;
+  step0 = static_cast<int>(all * share / p.split);  // this CTA's steps
+  n_steps = static_cast<int>(all * (share + 1) / p.split) - step0;
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
@@ -429,6 +436,8 @@ __global__ void __launch_bounds__(320, 1)
       tc_fence_after();
       const float mul = g == 0 ? 1.0f : p.s.scale;
       __nv_bfloat16* out = g == 0 ? p.dv : p.dk;
+      float* part = p.part + static_cast<size_t>((g == 0 ? 0 : p.split) + share) * n_units *
+                                 p.s.Nk * C::D;
       const uint32_t col0 = g == 0 ? C::COL_DV : C::COL_DK;
       const int lane = static_cast<int>(threadIdx.x & 31);
 #pragma unroll 1
@@ -447,9 +456,12 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int key = jt * C::BK + 32 * kc + e;
-            if (key < p.s.Nk)
-              out[(static_cast<size_t>(kvz) * p.s.Nk + key) * C::D + dcol] =
-                  __float2bfloat16_rn(__uint_as_float(r[e]) * mul);
+            if (key >= p.s.Nk) continue;
+            const size_t at = (static_cast<size_t>(kvz) * p.s.Nk + key) * C::D + dcol;
+            if (p.split > 1)
+              part[at] = __uint_as_float(r[e]) * mul;
+            else
+              out[at] = __float2bfloat16_rn(__uint_as_float(r[e]) * mul);
           }
         }
       }
@@ -470,8 +482,8 @@ __global__ void __launch_bounds__(320, 1)
 
 template <bool CAP, bool BIAS>
 cudaError_t launch_scores_kv256_t(const ScoreMaps& m, const float* lse, const float* Dv,
-                                  const int2* tiles, void* dk, void* dv, const ScoreParams& s,
-                                  cudaStream_t stream) {
+                                  const int2* tiles, void* dk, void* dv, float* part, int split,
+                                  const ScoreParams& s, cudaStream_t stream) {
   using C = ScoreKv256Cfg;
   auto kern = fa_scores_kv256_kernel<CAP, BIAS>;
   cudaError_t e = set_smem_limit_once<fa_scores_kv256_kernel<CAP, BIAS>>(C::SMEM_BYTES);
@@ -483,9 +495,11 @@ cudaError_t launch_scores_kv256_t(const ScoreMaps& m, const float* lse, const fl
   p.tiles = tiles;
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.part = part;
+  p.split = split;
   p.n_qtiles = (s.Nq + C::BQ - 1) / C::BQ;
   p.n_ktiles = (s.Nk + C::BK - 1) / C::BK;
-  const long long grid = static_cast<long long>(p.n_ktiles) * s.B * s.Hkv;
+  const long long grid = static_cast<long long>(p.n_ktiles) * s.B * s.Hkv * split;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS),
                           C::SMEM_BYTES, stream, m.q, m.k, m.v, m.dO, p);
@@ -495,16 +509,16 @@ cudaError_t launch_scores_kv256_t(const ScoreMaps& m, const float* lse, const fl
 
 template <>
 cudaError_t launch_scores_dkdv<256>(const ScoreMaps& m, const float* lse, const float* Dv,
-                                    const int2* tiles, void* dk, void* dv, const ScoreParams& p,
-                                    int mode, cudaStream_t stream) {
+                                    const int2* tiles, void* dk, void* dv, float* part,
+                                    int split, const ScoreParams& p, int mode, cudaStream_t stream) {
   switch (mode) {
     case kScorePlain:
-      return launch_scores_kv256_t<false, false>(m, lse, Dv, tiles, dk, dv, p, stream);
+      return launch_scores_kv256_t<false, false>(m, lse, Dv, tiles, dk, dv, part, split, p, stream);
     case kScoreBias:
-      return launch_scores_kv256_t<false, true>(m, lse, Dv, tiles, dk, dv, p, stream);
+      return launch_scores_kv256_t<false, true>(m, lse, Dv, tiles, dk, dv, part, split, p, stream);
     case kScoreCap:
-      return launch_scores_kv256_t<true, false>(m, lse, Dv, tiles, dk, dv, p, stream);
-    default: return launch_scores_kv256_t<true, true>(m, lse, Dv, tiles, dk, dv, p, stream);
+      return launch_scores_kv256_t<true, false>(m, lse, Dv, tiles, dk, dv, part, split, p, stream);
+    default: return launch_scores_kv256_t<true, true>(m, lse, Dv, tiles, dk, dv, part, split, p, stream);
   }
 }
 

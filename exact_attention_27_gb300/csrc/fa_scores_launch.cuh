@@ -1,6 +1,8 @@
 // Launches of the forward with shaped scores: the kernel by its mode, one query tile a CTA or two.
 #pragma once
 
+#include "fa_internal.h"
+#include "fa_paged_host.h"
 #include "fa_scores_fwd.cuh"
 #include "fa_scores_fwd2.cuh"
 
@@ -11,7 +13,17 @@ namespace {
 // 2^-120 and up to 2^40.
 constexpr float kFixedCap = 80.0f;
 
-bool two_tiles(const ScoreFwdParams& p) { return getenv("FA_ONE") == nullptr; }
+// One query tile a CTA or two: as for the unshaped forward, whose steps cost about the same
+// (forward_rows_for: it estimates when either grid ends).  Masks that spans bring are not
+// known here.  (16 heads of 8192, causal, one / two: d = 64 187 / 157 us, with slopes 268 / 230;
+// d = 96 197 / 174, 282 / 250; d = 128 206 / 227, 297 / 313.)
+bool two_tiles(const ScoreParams& s, int d) {
+  const int sms = sm_count();
+  AttnShape a{s.B, s.Hq, s.Hkv, s.Nq, d, s.scale, s.causal};
+  a.Nk = s.Nk;
+  a.q_offset = s.q_offset;
+  return sms > 0 && forward_rows_for(a, sms) == 256;
+}
 
 template <int D, bool CAP, bool BIAS, bool FIXED>
 cudaError_t launch_scores_fwd_t(const ScoreMaps& m, void* o, float* lse, const ScoreParams& s,
@@ -24,7 +36,7 @@ cudaError_t launch_scores_fwd_t(const ScoreMaps& m, void* o, float* lse, const S
   p.n_heads = s.B * s.Hq;
   p.heads_per_group = static_cast<int>(heads_per_group(s.Nk, D, 2.0, s.G, p.n_heads));
   if constexpr (D <= 128 && !FIXED) {
-    if (two_tiles(p)) {
+    if (two_tiles(s, D)) {
       using C = ScoreFwd2Cfg<D>;
       const cudaError_t e =
           set_smem_limit_once<fa_scores_fwd2_kernel<D, CAP, BIAS, FIXED>>(C::SMEM_BYTES);

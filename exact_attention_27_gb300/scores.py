@@ -157,16 +157,32 @@ def fa_forward_scores(q, k, v, o, lse, scale, causal, q_offset=0, scores=None, s
         raise FaError(status, "fa_forward_scores")
 
 
-def fa_backward_scores(q, k, v, o, lse, do, dq, dk, dv, scale, causal, q_offset=0, scores=None,
-                       spans=None, stream=None):
+def scores_workspace(q, k, causal, q_offset=0):
+    """A workspace for fa_backward_scores calls of these sizes.  Its contents do not matter, and
+    calls on one stream may share it; calls that can overlap, such as two captured graphs, may
+    not."""
+    torch = _load_torch()
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B, H, N, d]")
+    B, Hq, Nq, d = q.shape
+    n = library().fa_backward_scores_workspace_bytes(B, Hq, k.shape[1], Nq, k.shape[2], d,
+                                                     int(bool(causal)), int(q_offset))
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def fa_backward_scores(q, k, v, o, lse, do, dq, dk, dv, scale, causal, workspace, q_offset=0,
+                       scores=None, spans=None, stream=None):
     """fa_backward_scores of include/fa.h with the arguments of the forward that gave o and lse;
     writes dq, dk and dv."""
     device, *sizes = _checked(q, k, [("v", v, k), ("o", o, q), ("do", do, q), ("dq", dq, q),
                                      ("dk", dk, k), ("dv", dv, k)], lse, scores, spans)
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
     status = library().fa_backward_scores(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes, ctypes.c_float(scale),
         int(bool(causal)), int(q_offset), scores._ref if scores is not None else None,
-        spans._ref if spans is not None else None, _stream(stream, device))
+        spans._ref if spans is not None else None, workspace.data_ptr(), workspace.nbytes,
+        _stream(stream, device))
     if status:
         raise FaError(status, "fa_backward_scores")

@@ -303,15 +303,21 @@ fa_status fa_forward_scores(const void* q, const void* k, const void* v, void* o
  *   P = exp(x - L);  dV = P^T dO;  dS = P o (1 - tanh^2) o (dO V^T - D);
  *   dQ = dS K scale;  dK = dS^T Q scale
  * (no 1 - tanh^2 without softcap), dK and dV of a shared head summed over its query heads.
- * One kernel for dK and dV and one for dQ, without atomics: results repeat to the bit.
- * Scratch: 4 bytes a query row and 8 for every 128 of them, taken and released stream-ordered
- * as by fa_backward.
+ * One kernel for dK and dV and one for dQ, without atomics: results repeat to the bit.  dq, dk
+ * and dv must not alias any input.
+ *   workspace  device memory of at least fa_backward_scores_workspace_bytes for the same sizes,
+ *              16-byte aligned; its contents do not matter before or after.  Calls whose work
+ *              can overlap (other streams, other captured graphs) need one each.
  */
 fa_status fa_backward_scores(const void* q, const void* k, const void* v, const void* o,
                              const float* lse, const void* dO, void* dq, void* dk, void* dv, int B,
                              int H_q, int H_kv, int N_q, int N_kv, int d, float scale, int causal,
                              int q_offset, const fa_score_spec* spec, const fa_key_spans* spans,
-                             cudaStream_t stream);
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace for fa_backward_scores on the current device; 0 for sizes it rejects. */
+size_t fa_backward_scores_workspace_bytes(int B, int H_q, int H_kv, int N_q, int N_kv, int d,
+                                          int causal, int q_offset);
 
 /* ---------------------------------------------------------------- rotary positions
  *

@@ -32,17 +32,18 @@ def spans(first=P, end=P, stride=64):
 
 def call(lib, backward=False, s=None, r=None, **kw):
     a = dict(q=P, k=P, v=P, o=P, lse=P, do=P, dq=P, dk=P, dv=P, B=1, Hq=2, Hkv=1, Nq=64, Nkv=64,
-             d=64, scale=0.125, causal=1, off=0)
+             d=64, scale=0.125, causal=1, off=0, ws=P, bytes=2 ** 40)
     a.update(kw)
     p = ctypes.c_void_p
     head = [p(a[x]) if a[x] else None for x in ("q", "k", "v", "o", "lse")]
     if backward:
         head += [p(a[x]) if a[x] else None for x in ("do", "dq", "dk", "dv")]
     fn = lib.fa_backward_scores if backward else lib.fa_forward_scores
+    work = [p(a["ws"]) if a["ws"] else None, a["bytes"]] if backward else []
     return fn(*head, a["B"], a["Hq"], a["Hkv"], a["Nq"], a["Nkv"], a["d"],
               ctypes.c_float(a["scale"]), a["causal"], a["off"],
               ctypes.byref(s) if s is not None else None,
-              ctypes.byref(r) if r is not None else None, None)
+              ctypes.byref(r) if r is not None else None, *work, None)
 
 
 BAD = [dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(lse=None), dict(q=Q), dict(o=Q),
@@ -62,7 +63,7 @@ def test_bad_calls_are_rejected(lib, kw, backward):
 
 
 @pytest.mark.parametrize("kw", [dict(do=None), dict(dq=None), dict(dk=None), dict(dv=Q),
-                                dict(do=Q)])
+                                dict(do=Q), dict(ws=None), dict(ws=Q), dict(bytes=64)])
 def test_backward_rejects(lib, kw):
     assert call(lib, True, **kw) == fa.FA_ERR_INVALID_ARGUMENT
 
@@ -71,6 +72,14 @@ def test_backward_rejects(lib, kw):
 @pytest.mark.parametrize("backward", [False, True])
 def test_unsupported_head_dim(lib, d, backward):
     assert call(lib, backward, d=d) == fa.FA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("args", [(0, 2, 1, 64, 64, 64, 1, 0), (1, 3, 2, 64, 64, 64, 1, 0),
+                                  (1, 2, 1, 0, 64, 64, 1, 0), (1, 2, 1, 64, 0, 64, 1, 0),
+                                  (1, 2, 1, 64, 64, 80, 1, 0), (1, 2, 1, 64, 64, 64, 2, 0),
+                                  (1, 2, 1, 64, 64, 64, 1, -1)])
+def test_workspace_rejects(lib, args):
+    assert lib.fa_backward_scores_workspace_bytes(*args) == 0
 
 
 def test_handles_check_their_arguments():

@@ -58,7 +58,11 @@ class Problem:
         lse = torch.full(q.shape[:3], float("nan"), device="cuda")
         fa.fa_forward_scores(q, k, v, o, lse, self.scale, self.causal, self.q_offset, scores, spans,
                              stream)
-        fa.fa_backward_scores(q, k, v, o, lse, do, dq, dk, dv, self.scale, self.causal,
+        ws = fa.scores_workspace(q, k, self.causal, self.q_offset)
+        ws.fill_(0xFF)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        fa.fa_backward_scores(q, k, v, o, lse, do, dq, dk, dv, self.scale, self.causal, ws,
                               self.q_offset, scores, spans, stream)
         torch.cuda.synchronize()
         assert fa.fa_last_device_error() == 0
