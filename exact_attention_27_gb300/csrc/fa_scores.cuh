@@ -81,6 +81,96 @@ __device__ __forceinline__ void lower_scores(float (&s)[N], float slope2, float 
   for (int t = 0; t < N; ++t) s[t] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(t)), s[t]);
 }
 
+// What N columns' exponents get besides their scores, in pairs: -sub, and BIAS less
+// slope2 |dist0 - t|.  ONE: dist0 - t has the sign `side` (or is 0) at all N, so that this is
+// linear in t: two FMAs for eight columns and an addition a pair (the distances one by one take
+// four operations a pair: 16 heads of 8192, d = 64, forward 232 us instead of 219, both passes 773
+// instead of 737).
+template <int N, bool BIAS, bool ONE>
+struct Lowering {
+  float slope2, dist0, sub, k, base;
+  uint64_t step[3], at;
+  __device__ __forceinline__ Lowering(float slope2_, float dist0_, float sub_, float side)
+      : slope2(slope2_), dist0(dist0_), sub(sub_) {
+    if constexpr (!BIAS) {
+      at = f2_pack(-sub, -sub);
+    } else if constexpr (ONE) {
+      k = side * slope2;
+      base = fmaf(-k, dist0, -sub);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) step[i] = f2_pack((2 * i + 2) * k, (2 * i + 2) * k);
+    }
+  }
+  // Of columns t, t + 1, in order.
+  __device__ __forceinline__ uint64_t pair(int t) {
+    if constexpr (!BIAS) return at;
+    if constexpr (ONE) {
+      if (t % 8 == 0) {
+        at = f2_pack(fmaf(k, static_cast<float>(t), base), fmaf(k, static_cast<float>(t + 1), base));
+        return at;
+      }
+      return f2_add(at, step[t % 8 / 2 - 1]);
+    }
+    return f2_pack(fmaf(-slope2, fabsf(dist0 - static_cast<float>(t)), -sub),
+                   fmaf(-slope2, fabsf(dist0 - static_cast<float>(t + 1)), -sub));
+  }
+};
+
+// shape_scores where it is known whether dist0 - t has one sign (Lowering).
+template <int N, bool CAP, bool BIAS, bool GRAD, bool ONE, typename Again>
+__device__ __forceinline__ void shape_columns(float (&s)[N], float (&g)[GRAD ? N : 1],
+                                              const ScoreFactors& f, float slope2, float dist0,
+                                              float sub, float side, Again&& again) {
+  Lowering<N, BIAS, ONE> low(slope2, dist0, sub, side);
+  if constexpr (CAP) {
+    constexpr int CHAINS = N < 16 ? 1 : 2;  // independent maxima
+    float part[CHAINS];
+#pragma unroll
+    for (int u = 0; u < CHAINS; ++u) part[u] = 0.0f;
+    const uint64_t a0 = f2_pack(f.a[0], f.a[0]), a1 = f2_pack(f.a[1], f.a[1]);
+    const uint64_t a2 = f2_pack(f.a[2], f.a[2]), a3 = f2_pack(f.a[3], f.a[3]);
+    const uint64_t one = f2_pack(1.0f, 1.0f), nz = f2_pack(f.neg_inv_cap_sq, f.neg_inv_cap_sq);
+#pragma unroll
+    for (int t = 0; t < N; t += 2) {
+      part[t / 2 % CHAINS] = fmax3_abs(part[t / 2 % CHAINS], s[t], s[t + 1]);
+      const uint64_t v = f2_pack(s[t], s[t + 1]);
+      const uint64_t v2 = f2_mul(v, v);
+      const uint64_t h = f2_fma(f2_fma(f2_fma(a3, v2, a2), v2, a1), v2, a0);
+      if constexpr (GRAD) {
+        const uint64_t x = f2_mul(v, h);
+        f2_unpack(f2_add(x, low.pair(t)), s[t], s[t + 1]);
+        f2_unpack(f2_fma(f2_mul(x, x), nz, one), g[t], g[t + 1]);
+      } else {
+        f2_unpack(f2_fma(v, h, low.pair(t)), s[t], s[t + 1]);
+      }
+    }
+    float big = part[0];
+#pragma unroll
+    for (int u = 1; u < CHAINS; ++u) big = fmaxf(big, part[u]);
+    // (a NaN takes either way to a NaN)
+    if (__any_sync(0xffffffffu, big > f.range)) {
+      again(s);
+      Lowering<N, BIAS, ONE> more(slope2, dist0, sub, side);
+#pragma unroll
+      for (int t = 0; t < N; t += 2) {
+        float lower[2];
+        f2_unpack(more.pair(t), lower[0], lower[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float r = rcp_approx(ex2_approx(s[t + e] * (2.0f * kScoreLog2e * f.k)) + 1.0f);
+          s[t + e] = fmaf(-2.0f * f.cap2, r, f.cap2) + lower[e];
+          if constexpr (GRAD) g[t + e] = 4.0f * r * (1.0f - r);
+        }
+      }
+    }
+  } else {
+    const uint64_t c = f2_pack(f.k, f.k);
+#pragma unroll
+    for (int t = 0; t < N; t += 2)
+      f2_unpack(f2_fma(f2_pack(s[t], s[t + 1]), c, low.pair(t)), s[t], s[t + 1]);
+  }
+}
+
 // What turns raw products s = q.k of keys kbase + t, t = 0 .. N-1, into exponents of the
 // weights, x (log2 domain), less `sub`:  CAP x = cap tanh(s k) (in f), else x = s f.k;
 // BIAS then - slope2 |pos - key|, dist0 = pos - kbase.  With GRAD, g gets 1 - tanh^2.  The
@@ -91,49 +181,17 @@ template <int N, bool CAP, bool BIAS, bool GRAD, typename Again>
 __device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N : 1],
                                              const ScoreFactors& f, float slope2, float dist0,
                                              float sub, Again&& again) {
-  if constexpr (CAP) {
-    constexpr int CHAINS = N < 16 ? 1 : 2;  // independent maxima
-    float part[CHAINS];
-#pragma unroll
-    for (int u = 0; u < CHAINS; ++u) part[u] = 0.0f;
-    const uint64_t a0 = f2_pack(f.a[0], f.a[0]), a1 = f2_pack(f.a[1], f.a[1]);
-    const uint64_t a2 = f2_pack(f.a[2], f.a[2]), a3 = f2_pack(f.a[3], f.a[3]);
-    const uint64_t ns = f2_pack(-sub, -sub);
-    const uint64_t one = f2_pack(1.0f, 1.0f), nz = f2_pack(f.neg_inv_cap_sq, f.neg_inv_cap_sq);
-#pragma unroll
-    for (int t = 0; t < N; t += 2) {
-      part[t / 2 % CHAINS] = fmax3_abs(part[t / 2 % CHAINS], s[t], s[t + 1]);
-      const uint64_t v = f2_pack(s[t], s[t + 1]);
-      const uint64_t v2 = f2_mul(v, v);
-      const uint64_t h = f2_fma(f2_fma(f2_fma(a3, v2, a2), v2, a1), v2, a0);
-      if constexpr (GRAD) {
-        const uint64_t x = f2_mul(v, h);
-        f2_unpack(f2_add(x, ns), s[t], s[t + 1]);
-        f2_unpack(f2_fma(f2_mul(x, x), nz, one), g[t], g[t + 1]);
-      } else {
-        f2_unpack(f2_fma(v, h, ns), s[t], s[t + 1]);
-      }
-    }
-    float big = part[0];
-#pragma unroll
-    for (int u = 1; u < CHAINS; ++u) big = fmaxf(big, part[u]);
-    // (a NaN takes either way to a NaN)
-    if (__any_sync(0xffffffffu, big > f.range)) {
-      again(s);
-#pragma unroll
-      for (int t = 0; t < N; ++t) {
-        const float r = rcp_approx(ex2_approx(s[t] * (2.0f * kScoreLog2e * f.k)) + 1.0f);
-        s[t] = fmaf(-2.0f * f.cap2, r, f.cap2) - sub;
-        if constexpr (GRAD) g[t] = 4.0f * r * (1.0f - r);
-      }
-    }
+  if constexpr (BIAS) {
+    const bool before = __all_sync(0xffffffffu, dist0 >= static_cast<float>(N - 1));
+    const bool after = __all_sync(0xffffffffu, dist0 <= 0.0f);
+    if (before || after)
+      shape_columns<N, CAP, BIAS, GRAD, true>(s, g, f, slope2, dist0, sub, before ? 1.0f : -1.0f,
+                                              again);
+    else
+      shape_columns<N, CAP, BIAS, GRAD, false>(s, g, f, slope2, dist0, sub, 0.0f, again);
   } else {
-    const uint64_t c = f2_pack(f.k, f.k), ns = f2_pack(-sub, -sub);
-#pragma unroll
-    for (int t = 0; t < N; t += 2)
-      f2_unpack(f2_fma(f2_pack(s[t], s[t + 1]), c, ns), s[t], s[t + 1]);
+    shape_columns<N, CAP, false, GRAD, false>(s, g, f, slope2, dist0, sub, 0.0f, again);
   }
-  if constexpr (BIAS) lower_scores<N>(s, slope2, dist0);
 }
 
 // TMEM -> registers, 16 or 32 consecutive columns.

@@ -119,13 +119,23 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
     static_assert(!FIXED || BN == 32, "columns of a part");
     tmem_st16(s_addr, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
   } else {
-    float s[BN], none[1];
-    load(s);
+    float s[BN];
     // Without a tanh or a distance the scale waits for the exponents' multiply-add.
     constexpr bool RAW = !CAP && !BIAS;
-    if constexpr (!RAW)
-      shape_scores<BN, CAP, BIAS, false>(s, none, p.f, slope2,
-                                         static_cast<float>(pos - kbase), 0.0f, load);
+    if constexpr (RAW) {
+      load(s);
+    } else {
+      // 32 columns at a time (at once, cap and distance spilled half of the row).
+#pragma unroll
+      for (int c0 = 0; c0 < BN; c0 += 32) {
+        float(&y)[32] = *reinterpret_cast<float(*)[32]>(&s[c0]);
+        float none[1];
+        auto part = [&](float (&z)[32]) { load_scores(s_addr + c0, z); };
+        part(y);
+        shape_scores<32, CAP, BIAS, false>(y, none, p.f, slope2,
+                                           static_cast<float>(pos - kbase - c0), 0.0f, part);
+      }
+    }
     if (mask) {
 #pragma unroll
       for (int t = 0; t < BN; ++t)
