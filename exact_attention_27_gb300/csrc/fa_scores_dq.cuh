@@ -25,6 +25,8 @@
 // Warps: 0-7 query rows (warp w: rows 32 (w % 4).., key columns KH (w / 4)..), 8 TMA, 9 MMA
 // issuer and tensor-memory owner.
 
+#include <algorithm>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -95,6 +97,7 @@ struct ScoreDqParams {
   float* Dvec;  // written where it is summed here
   __nv_bfloat16* dq;
   int n_qtiles, n_heads, heads_per_group;
+  int before;  // query tiles that go before the others
 };
 
 template <int D, bool CAP, bool BIAS>
@@ -115,14 +118,15 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
   uint32_t* err = p.s.err;
 
   const int warp = threadIdx.x >> 5;
-  // Same launch order as the forward: groups of heads, heaviest tiles first.
+  // Same launch order as the forward: groups of heads, the last tiles first; but before them,
+  // behind a long window, those that go through their few keys twice.
   const int per_group = p.heads_per_group * p.n_qtiles;
   const int grp = static_cast<int>(blockIdx.x) / per_group;
   const int rem = static_cast<int>(blockIdx.x) - grp * per_group;
   const int in_grp = min(p.heads_per_group, p.n_heads - grp * p.heads_per_group);
   const int qi_ = rem / in_grp;
   const int bh = grp * p.heads_per_group + (rem - qi_ * in_grp);
-  const int qt = p.n_qtiles - 1 - qi_;
+  const int qt = (qi_ < p.before ? p.before : p.n_qtiles + p.before) - 1 - qi_;
   const int b = bh / p.s.Hq;
   const int hq = bh - b * p.s.Hq;
   const int kvz = b * p.s.Hkv + hq / p.s.G;
@@ -480,6 +484,11 @@ cudaError_t launch_scores_dq_t(const ScoreMaps& m, const float* lse, float* Dv, 
   p.n_qtiles = (s.Nq + C::BM - 1) / C::BM;
   p.n_heads = s.B * s.Hq;
   p.heads_per_group = static_cast<int>(heads_per_group(s.Nk, D, 2.0, s.G, p.n_heads));
+  // (8 heads of 4000, d = 256, cap, window 1024: 78 us instead of 97)
+  constexpr int kFew = C::EXACT_TILES * C::BN;
+  p.before = 0;
+  if (s.causal && s.window > kFew - C::BM)
+    p.before = std::min(std::max(kFew - s.q_offset, 0) / C::BM, p.n_qtiles);
   const long long grid = static_cast<long long>(p.n_heads) * p.n_qtiles;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(C::THREADS),
