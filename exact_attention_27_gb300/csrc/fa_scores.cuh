@@ -73,14 +73,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// Scores of keys kbase + t less slope2 |pos - key|, dist0 = pos - kbase (distances are whole
-// numbers, exact in fp32 up to 2^24).
-template <int N>
-__device__ __forceinline__ void lower_scores(float (&s)[N], float slope2, float dist0) {
-#pragma unroll
-  for (int t = 0; t < N; ++t) s[t] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(t)), s[t]);
-}
-
 // What N columns' exponents get besides their scores, in pairs: -sub, and BIAS less
 // slope2 |dist0 - t|.  ONE: dist0 - t has the sign `side` (or is 0) at all N, so that this is
 // linear in t: two FMAs for eight columns and an addition a pair (the distances one by one take
@@ -115,6 +107,23 @@ struct Lowering {
                    fmaf(-slope2, fabsf(dist0 - static_cast<float>(t + 1)), -sub));
   }
 };
+
+// Scores of keys kbase + t less slope2 |pos - key|, dist0 = pos - kbase (distances are whole
+// numbers, exact in fp32 up to 2^24).  The whole warp calls this.
+template <int N>
+__device__ __forceinline__ void lower_scores(float (&s)[N], float slope2, float dist0) {
+  const bool before = __all_sync(0xffffffffu, dist0 >= static_cast<float>(N - 1));
+  const bool after = __all_sync(0xffffffffu, dist0 <= 0.0f);
+  if (before || after) {
+    Lowering<N, true, true> low(slope2, dist0, 0.0f, before ? 1.0f : -1.0f);
+#pragma unroll
+    for (int t = 0; t < N; t += 2)
+      f2_unpack(f2_add(f2_pack(s[t], s[t + 1]), low.pair(t)), s[t], s[t + 1]);
+  } else {
+#pragma unroll
+    for (int t = 0; t < N; ++t) s[t] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(t)), s[t]);
+  }
+}
 
 // shape_scores where it is known whether dist0 - t has one sign (Lowering).
 template <int N, bool CAP, bool BIAS, bool GRAD, bool ONE, typename Again>

@@ -62,8 +62,8 @@ struct ScoreDkdvCfg {
   static constexpr int B_DOEMPTY = B_DOFULL + NDO;  // [NDO]
   static constexpr int B_S = B_DOEMPTY + NDO;       // S in tensor memory
   static constexpr int B_DP = B_S + 1;              // dP there
-  static constexpr int B_P = B_DP + 1;              // P in shared memory, S read (8 warps)
-  static constexpr int B_DS = B_P + 1;              // dS in shared memory, dP read (8 warps)
+  static constexpr int B_P = B_DP + 1;              // P in shared memory, S read (every row warp)
+  static constexpr int B_DS = B_P + 1;              // dS in shared memory, dP read (every row warp)
   static constexpr int B_FINAL = B_DS + 1;          // every product completed (once)
   static constexpr int B_DRAIN = B_FINAL + 1;
   static constexpr int NBAR = B_DRAIN + 1;

@@ -74,8 +74,8 @@ struct ScoreDqCfg {
   static constexpr int B_VEMPTY = B_VFULL + NSV;   // [NSV]
   static constexpr int B_SFULL = B_VEMPTY + NSV;   // [2] S_j in S buffer j % 2
   static constexpr int B_DPFULL = B_SFULL + 2;     // dP_j in the dP buffer
-  static constexpr int B_DPFREE = B_DPFULL + 1;    // dP_j read by every row warp (8 arrivals)
-  static constexpr int B_DSREADY = B_DPFREE + 1;   // [2] dS_j in S buffer j % 2 (8 arrivals)
+  static constexpr int B_DPFREE = B_DPFULL + 1;    // dP_j read by every row warp
+  static constexpr int B_DSREADY = B_DPFREE + 1;   // [2] dS_j in S buffer j % 2 (every row warp)
   static constexpr int B_DQDONE = B_DSREADY + 2;   // every dQ MMA done (completes once)
   static constexpr int B_DSUM = B_DQDONE + 1;      // the parts' sums of P dP (every row warp, twice)
   static constexpr int B_DRAIN = B_DSUM + 1;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
   } else {
     // ------------------------------------------------------------ query rows
     // Warp w reads tensor-memory lanes 32 (w % 4) .. +31 (its query rows)
-    // and key columns 64 (w / 4) .. +63 of each tile.
+    // and key columns KH (w / 4) .. of each tile.
     const int wq = warp & 3, g = warp >> 2;
     const int row = wq * 32 + static_cast<int>(threadIdx.x & 31);
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
       mbar_arrive_warp(bar(C::B_DSREADY + (j & 1)));
     }
     // ---- epilogue: dq = bf16(scale dQ), one row per thread, 32-column
-    // chunks split between the two warps of a row
+    // chunks split between the warps of a row
     if (ok && n_kv > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_DQDONE), 0, abort_flag, err,
                                              kErrTimeoutEpilogue));

@@ -125,15 +125,26 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
     if constexpr (RAW) {
       load(s);
     } else {
-      // 32 columns at a time (at once, cap and distance spilled half of the row).
+      // All columns at once, or 64 with the tanh and distances too, where all spill (16 heads of
+      // 8192, two tiles at d = 64, one at d = 128: distances 219 / 210 / 207 and 306 / 286 / 276 us
+      // with 32, 64 and 128 columns; both 324 / 309 / 408 and 415 / 370 / 417).
+      constexpr int PART = CAP && BN > 64 ? 64 : BN;
 #pragma unroll
-      for (int c0 = 0; c0 < BN; c0 += 32) {
-        float(&y)[32] = *reinterpret_cast<float(*)[32]>(&s[c0]);
+      for (int c0 = 0; c0 < BN; c0 += PART) {
+        float(&y)[PART] = *reinterpret_cast<float(*)[PART]>(&s[c0]);
         float none[1];
-        auto part = [&](float (&z)[32]) { load_scores(s_addr + c0, z); };
+        auto part = [&](float (&z)[PART]) {
+          uint32_t r[PART];
+#pragma unroll
+          for (int c = 0; c < PART / 32; ++c)
+            tmem_ld32(s_addr + c0 + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
+          tmem_wait_ld();
+#pragma unroll
+          for (int t = 0; t < PART; ++t) z[t] = __uint_as_float(r[t]);
+        };
         part(y);
-        shape_scores<32, CAP, BIAS, false>(y, none, p.f, slope2,
-                                           static_cast<float>(pos - kbase - c0), 0.0f, part);
+        shape_scores<PART, CAP, BIAS, false>(y, none, p.f, slope2,
+                                             static_cast<float>(pos - kbase - c0), 0.0f, part);
       }
     }
     if (mask) {

@@ -11,9 +11,7 @@
 // 11 idle.  Registers: 384 threads at 168: 224 / 224 / 56.  Tensor memory: S of tile x at
 // columns 128 x (P, packed in pairs, over its first half), O at 256 + DP x.
 //
-// The reference of the online softmax is fixed where the cap allows it (fa_scores_fwd.cuh says
-// when); a row's scores then go through in four parts of 32 columns, the next one's load behind
-// the arithmetic of the one at hand, as no maximum over all 128 is needed first.
+// Not for scores whose cap fixes the reference (fa_scores_fwd.cuh): there four warps share a row.
 #pragma once
 
 #include <cuda.h>
@@ -60,7 +58,7 @@ struct ScoreFwd2Cfg {
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
-template <int D, bool CAP, bool BIAS, bool FIXED>
+template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(384, 1)
     fa_scores_fwd2_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK,
@@ -283,7 +281,7 @@ __global__ void __launch_bounds__(384, 1)
     const int j1 = x == 0 ? a1 : b1;
     const float slope2 = BIAS && p.s.slopes ? p.s.slopes[hq] * kScoreLog2e : 0.0f;
     const int pos = p.s.q_offset + qi;
-    float m_used = FIXED ? 0.5f * p.s.f.cap2 : -INFINITY;  // reference, log2 domain
+    float m_used = -INFINITY;  // reference, log2 domain
     float l = 0.0f;
     bool ok = true;
     for (int j = j0; j < j1; ++j) {
@@ -297,11 +295,11 @@ __global__ void __launch_bounds__(384, 1)
       const bool need_mask = __any_sync(0xffffffffu, span.lo > kbase || span.hi < kbase + C::BN);
       bool moved = false;
       const float alpha =
-          score_row<C::BN, CAP, BIAS, FIXED>(p.s, col_s, need_mask, span, kbase, pos, slope2,
+          score_row<C::BN, CAP, BIAS, false>(p.s, col_s, need_mask, span, kbase, pos, slope2,
                                              m_used, l, moved);
       // S of this tile was issued after its last O += P V, whose completion the commit behind S
       // covers: the wait for the rescale returns at once.
-      if (!FIXED && j > j0 && __any_sync(0xffffffffu, moved)) {
+      if (j > j0 && __any_sync(0xffffffffu, moved)) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_ODONE + x), (j - j0 - 1) & 1, abort_flag,
                                                err, kErrTimeoutSoftmax));
         if (!ok) break;

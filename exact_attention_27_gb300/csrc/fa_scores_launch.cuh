@@ -15,8 +15,8 @@ constexpr float kFixedCap = 80.0f;
 
 // One query tile a CTA or two: as for the unshaped forward, whose steps cost about the same
 // (forward_rows_for: it estimates when either grid ends).  Masks that spans bring are not
-// known here.  (16 heads of 8192, causal, one / two: d = 64 187 / 157 us, with slopes 268 / 230;
-// d = 96 197 / 174, 282 / 250; d = 128 206 / 227, 297 / 313.)
+// known here.  (16 heads of 8192, causal, one / two: d = 64 187 / 152 us, with slopes 268 / 219;
+// d = 96 197 / 170, 282 / 234; d = 128 200 / 225, 321 / 307.)
 bool two_tiles(const ScoreParams& s, int d) {
   const int sms = sm_count();
   AttnShape a{s.B, s.Hq, s.Hkv, s.Nq, d, s.scale, s.causal};
@@ -39,11 +39,11 @@ cudaError_t launch_scores_fwd_t(const ScoreMaps& m, void* o, float* lse, const S
     if (two_tiles(s, D)) {
       using C = ScoreFwd2Cfg<D>;
       const cudaError_t e =
-          set_smem_limit_once<fa_scores_fwd2_kernel<D, CAP, BIAS, FIXED>>(C::SMEM_BYTES);
+          set_smem_limit_once<fa_scores_fwd2_kernel<D, CAP, BIAS>>(C::SMEM_BYTES);
       if (e != cudaSuccess) return e;
       const long long grid = static_cast<long long>(p.n_heads) * ((p.n_qtiles + 1) / 2);
       if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-      return launch_dependent(fa_scores_fwd2_kernel<D, CAP, BIAS, FIXED>,
+      return launch_dependent(fa_scores_fwd2_kernel<D, CAP, BIAS>,
                               dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), C::SMEM_BYTES,
                               stream, m.q, m.k, m.v, p);
     }
