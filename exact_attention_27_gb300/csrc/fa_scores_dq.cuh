@@ -15,15 +15,19 @@
 // kernel, which runs after this one.  (Errors relative to dq's norm, 0.0017 of which is its own
 // rounding and as much dS's: three keys a row, slopes: 0.0055 -> 0.0024; packed documents of 100 to
 // 2000 positions: 0.0026 -> 0.0024, for a third more of this kernel's time.  One of 8192 keys,
-// causal: 1 % more.)  A row that sees one key has dS = 0.
+// causal: 1 % more.)  So does a head whose weights fall by e within 10 keys or fewer, however
+// many it sees (slopes of 0.71, 0.35, 0.18, 0.09: 0.0031, 0.0028, 0.0027, 0.0025 otherwise).  A
+// row that sees one key has dS = 0.
 //
 // Pipeline as in fa_bwd_dq.cu: S_j in one of two tensor-memory buffers, dP_j in one that the
 // row warps hand back as soon as they hold its values, dS_j over the S columns they have
-// read.  Eight row warps, a row's keys split between two, since L is known and no row
-// reduction is needed.
+// read.  Sixteen row warps (eight at d = 256), a row's keys split between four (two), since L
+// is known and no row reduction is needed.
 //
-// Warps: 0-7 query rows (warp w: rows 32 (w % 4).., key columns KH (w / 4)..), 8 TMA, 9 MMA
-// issuer and tensor-memory owner.
+// Warps: 0 .. WARPS - 1 query rows (warp w: rows 32 (w % 4).., key columns KH (w / 4)..), then
+// TMA, and MMA issuer and tensor-memory owner.  Bound by issue and the FMA pipe with a cap
+// (60 % and 35 % at 16 heads of 8192, d = 64: 332 us, uncapped 189), by the tensor core otherwise
+// (70 % at d = 128: 264 us, 1.04 PFLOP/s; capped 346).
 
 #include <algorithm>
 
@@ -38,6 +42,8 @@
 
 namespace fa {
 namespace {
+
+constexpr float kSteep = 0.1f;  // slopes from here on: D is summed
 
 // Head dimension D in {64, 96, 128, 256}; tiles are DP = D rounded up to a
 // multiple of 64 columns wide (zero-filled past D), S and dP contract over the
@@ -174,7 +180,8 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
   const int j0 = hi > 0 ? lo / C::BN : 0;  // first key tile
   const int n_keys = hi > 0 ? (hi + C::BN - 1) / C::BN - j0 : 0;  // key tiles
   // Tiles gone through, v = 0 .. n_kv - 1; before n_sum D is summed.
-  const int n_sum = n_keys <= C::EXACT_TILES ? n_keys : 0;
+  const bool steep = BIAS && p.s.slopes && fabsf(p.s.slopes[hq]) >= kSteep;
+  const int n_sum = steep || n_keys <= C::EXACT_TILES ? n_keys : 0;
   const int n_kv = n_sum + n_keys;
   auto key_tile = [&](int v) -> int { return j0 + (v < n_sum ? v : v - n_sum); };
 
@@ -352,9 +359,10 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
       // so that it is there, and its columns are handed back at once.
       float w[KH];
       load_scores(tmem + lane_off + scol, w);
-      // CH columns at a time: all, or half of them where the tanh's derivative takes registers
-      // too (96 a thread).
-      constexpr int CH = CAP ? KH / 2 : KH;
+      // CH columns at a time: all, or half of them where the tanh's derivative and the distances
+      // both take registers (96 a thread; both passes of 16 heads of 8192, d = 64: cap 946 us in
+      // halves, 932 at once, with slopes too 1098 and 1136).
+      constexpr int CH = CAP && BIAS ? KH / 2 : KH;
 #pragma unroll
       for (int c0 = 0; c0 < KH; c0 += CH) {
         float(&x)[CH] = *reinterpret_cast<float(*)[CH]>(&w[c0]);

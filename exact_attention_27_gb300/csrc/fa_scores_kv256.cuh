@@ -8,7 +8,8 @@
 //   P = exp(x - L), dS = P o (1 - tanh^2) o (dP - D)    a query row a thread and half tile
 //   dV^T += dO^T P, dK^T += Q^T dS              two MMAs each (halves of d)
 // Q and dO come as two halves of d with a barrier each, reloaded as soon as the product that
-// reads a half is done: shared memory has room for one stage.
+// reads a half is done: shared memory has room for one stage.  8 query heads of 4 groups, 4000
+// positions, cap, window 1024: 121 us in two rounds of CTAs.
 //
 // Warps: 0-7 query rows (warp w: rows 32 (w % 4).., keys 32 (w / 4)..), 8 TMA, 9 MMA issuer
 // and tensor-memory owner.  Tensor memory: dV^T [0,128), dK^T [128,256), S [256,320), dP
