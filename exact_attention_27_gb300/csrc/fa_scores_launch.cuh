@@ -15,8 +15,8 @@ constexpr float kFixedCap = 80.0f;
 
 // One query tile a CTA or two: as for the unshaped forward, whose steps cost about the same
 // (forward_rows_for: it estimates when either grid ends).  Masks that spans bring are not
-// known here.  (16 heads of 8192, causal, one / two: d = 64 187 / 152 us, with slopes 268 / 219;
-// d = 96 197 / 170, 282 / 234; d = 128 200 / 225, 321 / 307.)
+// known here.  (16 heads of 8192, causal, one / two: d = 64 187 / 152 us, with slopes 241 / 207;
+// d = 96 197 / 170, 259 / 219; d = 128 200 / 225, 276 / 287.)
 bool two_tiles(const ScoreParams& s, int d) {
   const int sms = sm_count();
   AttnShape a{s.B, s.Hq, s.Hkv, s.Nq, d, s.scale, s.causal};

@@ -290,3 +290,56 @@ def test_norm_then_shaped_attention_then_back():
     for got, want in zip((dq, dk, dv, dqw, dkw), grads):
         err = (got.cpu().double() - want).norm() / want.norm()
         assert err <= limit, err
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("B,N", [(2, 1901), (900, 5), (1, 7407), (3, 4999)])
+def test_many_positions(B, N, d):
+    """Blocks of several positions, and of the gradient's kernel several steps each, some of them
+    over many short batch entries."""
+    import exact_attention_27_gb300 as fa
+    p = Problem(B, 3, 1, N, d, d if N % 2 else d // 2, interleaved=B == 1, seed=N)
+    norm, positions, rotary = p.handles()
+    q, k, dq, dk = (x.cuda() for x in (p.q, p.k, p.dq, p.dk))
+    p.check_forward(*fa.norm_rotary_forward(q, k, norm, positions, rotary))
+    p.check_backward(*fa.norm_rotary_backward(dq, dk, q, k, norm, positions, rotary))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("new", [[2, 1500, 1, 900, 1600], [7400, 3], [1] * 40, [9000, 6000]])
+@pytest.mark.parametrize("with_q", [True, False])
+def test_append_many_rows_at_their_places(new, d, e4m3, with_q):
+    """Steps of many tokens and of many sequences, positions those in the sequences, with and
+    without q."""
+    import exact_attention_27_gb300 as fa
+    Hq, Hkv, page = 3, 1, 64
+    past = [(5 * i) % 23 for i in range(len(new))]
+    step = Step(new, [n + m for n, m in zip(new, past)], Hq, Hkv, d, page, e4m3, seed=d)
+    cache, batch = step.handles()
+    T = step.T
+    place = torch.cat([torch.arange(m, m + n) for n, m in zip(new, past)])
+    p = Problem(1, Hq, Hkv, T, d, d, dtype=torch.bfloat16, seed=T)
+    p.axes, p.axis = 1, torch.zeros(d // 2, dtype=torch.long)
+    p.angle = angles64(place.to(torch.int32)[None, None], p.inv, p.axis)[:, None]
+    norm, _, rotary = p.handles()
+    rows = lambda x: x[0].transpose(0, 1).contiguous().cuda()  # noqa: E731
+    v = torch.randn(T, Hkv, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    out = torch.full((T, Hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fa.fa_paged_append(cache, batch, rows(p.k), v.cuda(), rotary, None,
+                       rows(p.q) if with_q else None, out if with_q else None, norm=norm)
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_error() == 0
+    if with_q:
+        p.check_forward(out.transpose(0, 1)[None], None)
+    seq = torch.cat([torch.full((n,), s) for s, n in enumerate(new)])
+    where = step.table_cpu[seq, place // page].long(), place % page
+    want, slack = forward64(p.k.double(), p.kw.double(), EPS, p.angle, d)
+    for pages, x, sl, ds in ((step.k_pages, want[0].transpose(0, 1), slack[0].transpose(0, 1),
+                              step.kd),
+                             (step.v_pages, v.double(), torch.zeros(()), step.vd)):
+        got = pages.cpu().float().double()[where[0], :, where[1]]
+        x = (x / ds).clamp(-448, 448) if e4m3 else x
+        sl = sl / ds
+        tol = (E4M3 if e4m3 else BF16) * (x.abs() + sl) + sl + (2.0 ** -10 if e4m3 else 0)
+        assert torch.all((got - x).abs() <= tol)
