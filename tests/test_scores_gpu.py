@@ -320,3 +320,17 @@ def test_masked_keys_may_hold_anything(d):
         val, tol = whole(p.q, p.k, p.v, p.see(), p.scale, p.softcap, do=p.do)
         for name in ("o", "lse", "dv", "dk"):
             assert off_by(got[name], val[name], tol[name]) <= 1, name
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+def test_long_windows_and_steep_heads(d, softcap):
+    """Windows past the keys that dQ goes through twice, with a history and without; heads whose
+    few keys that count lie among many; distances of both signs over long rows."""
+    N = 2300
+    Problem(1, 3, 1, N, d, causal=True, window=1500, softcap=softcap, seed=d).check()
+    Problem(1, 2, 1, N, d, Nkv=N + 700, q_offset=700, causal=True, window=1000, softcap=softcap,
+            seed=d + 1).check()
+    Problem(1, 3, 3, N, d, causal=True, softcap=softcap, slopes=[0.7, 0.12, 0.05],
+            seed=d + 2).check()
+    Problem(1, 2, 1, 1400, d, softcap=softcap, slopes=[-0.2, 0.1], q_offset=90, seed=d + 3).check()
