@@ -22,8 +22,8 @@
 // CTAs each, which take equal stretches of its steps and leave fp32 sums that a second kernel
 // adds in order (fa_scores.cu says when): results repeat to the bit.
 //
-// Bound by shared memory and the tensor core: a step's four products read 3072 cycles' worth of
-// operands at 128 bytes a cycle where d = 128, and the rows write P and dS there.  16 heads of
+// Bound by shared memory and the tensor core: a step's four products read 384 KiB of
+// operands where d = 128, at 128 bytes a cycle, and the rows write P and dS there.  16 heads of
 // 8192, causal: d = 128 363 us (1.51 PFLOP/s), cap 470; d = 64 321, cap 414.
 //
 // Warps: 0-15 query rows (warp w: rows 32 (w % 4).., keys 32 (w / 4)..), 16 TMA, 17 MMA issuer and
