@@ -11,11 +11,12 @@
 // with 16 values each, which add their sums by shuffles among themselves, all lanes of a warp
 // together: the loops run to the same count in every lane.  A thread's rows come through shared
 // memory by asynchronous copies, several on their way (no other thread reads them: no barrier).
-// Appending 8527 tokens of 32 + 8 + 8 heads, d = 128, to e4m3 pages: 40.6 us, 4.7 TB/s (in
-// registers instead, two rows at a time, the kernel spilled: 47.3; without the norms 37.5).  The
-// gradient of 8192 positions of 32 + 8 heads, d = 128: 51.8 us, 4.9 TB/s, and 2 us for the
-// weights' sums (one row ahead in registers: 69.5 and 7.8).  Half of the issue slots are taken:
-// widening, the two sums and the turn are some 200 instructions for a lane's 16 values.
+// Appending 8527 tokens of 32 + 8 + 8 heads, d = 128, to e4m3 pages: 36.9 us, 5.2 TB/s (with
+// 2 / 3 / 5 / 6 / 8 slots instead of 4: 43.3 / 37.2 / 38.6 / 40.6 / 44.8; two rows at a time in
+// registers spilled: 47.3; without the norms 37.4).  The gradient of 8192 positions of 32 + 8
+// heads, d = 128: 52.1 us, 4.8 TB/s, with the weights' sums (2 / 4 / 6 slots 57.7 / 52.8 / 54.1;
+// one row ahead in registers 77.3).  Half of the issue slots are taken: widening, the two sums
+// and the turn are some 200 instructions for a lane's 16 values.
 //
 // The gradient's thread keeps the sum for dw of its 16 values of a row over all rows that it
 // goes through, in fp32; the threads of a block are added in a fixed order through shared
@@ -30,7 +31,7 @@
 namespace fa {
 namespace {
 
-constexpr int kTurnSlots = 6, kGradSlots = 4;  // rows of a thread in shared memory
+constexpr int kTurnSlots = 4, kGradSlots = 3;  // rows of a thread in shared memory
 
 __host__ __device__ constexpr int row_lanes(int d) { return d == 96 ? 8 : d / 16; }
 
@@ -210,7 +211,7 @@ struct NormTurnCfg {
 
 // Thread: 16 values of token tt, heads hg, hg + HG, ... of q, then of k (and v).
 template <int D, int TOK, int TO>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, TO == kTurnOnly ? 4 : 3)
     fa_norm_turn_kernel(const __grid_constant__ TurnParams p) {
   using C = NormTurnCfg<D, TOK>;
   constexpr int LANES = C::LANES, HG = C::HG;
@@ -390,14 +391,17 @@ template <int D, int TO>
 cudaError_t launch_norm_d(const TurnParams& p, cudaStream_t stream) {
   const long long sms = sm_count();
   if (sms < 1) return cudaErrorInvalidDevice;
-  // The most positions a block that leave six blocks for every SM, two for each that it holds at
-  // a time, and a thread at most ten heads (8192 positions of 16 heads, d = 64, with one, three
-  // and six blocks: 13.5 / 15.1 / 13.4 us; appending 8527 tokens 41.7 with each).
+  // The most positions a block that give a thread at most ten heads and leave two blocks for every
+  // SM, or one where a thread has four heads or fewer (2000 positions of 40 heads, d = 64 / 128 /
+  // 256, with 1 / 4 / 8 positions: 13.7 / 6.4 / 8.4 us, 15.7 / 9.2 / 14.3, 21.0 / 16.1 / -; 1025 of
+  // 32 with 1 / 4: 7.8 / 5.3, 8.7 / 7.7, 10.0 / 12.9).
   const int heads = p.q.heads + p.k.heads + p.v.heads;
   int tok = 1;
-  for (int more : {4, 8, 16})
-    if (p.tokens >= 6 * sms * more && heads * (D / 16) * more <= 10 * kThreads)
+  for (int more : {4, 8, 16}) {
+    const int rows = heads * (D / 16) * more;  // of 16 values
+    if (rows <= 10 * kThreads && p.tokens >= (rows <= 4 * kThreads ? 1 : 2) * sms * more)
       tok = more;
+  }
   switch (tok) {
     case 1: return launch_norm_tok<D, 1, TO>(p, stream);
     case 4: return launch_norm_tok<D, 4, TO>(p, stream);
@@ -652,17 +656,21 @@ template <int D>
 cudaError_t launch_grad_d(NormGradParams& p, float* dqw, float* dkw, cudaStream_t stream) {
   const int most = grad_blocks();
   if (most < 2) return cudaErrorInvalidDevice;
-  // Positions at a time: the most of which a block's threads make kGradAngles angles each and go
-  // through four rows or more, and that leave its share of the blocks four steps.  The blocks are
+  // Positions at a time, of which a block's threads make kGradAngles angles each at most: enough
+  // that all threads have a row, and then the most that leave a thread eight rows and the blocks
+  // four steps each.  The blocks are
   // shared out by the work, a step's beside its rows counted as one row (by rows alone, with k's
-  // steps of one row each: 64.2 us instead of 53.8 with the weights' sums).
+  // steps of one row each: 64.2 us instead of 53.8; four rows or more instead of eight: 52.8
+  // instead of 52.2).
   constexpr int SLOTS = kThreads / row_lanes(D);
   const int all = p.t.q.heads + p.t.k.heads;
   auto tok_for = [&](int heads) {
     int log = 0;
     while ((2 << log) <= kGradTok && (2 << log) <= SLOTS &&
-           (p.t.half << log) * 2 <= kGradAngles * kThreads && (SLOTS >> log) * 4 > heads &&
-           p.t.tokens * all >= static_cast<long long>(most) * heads * (8 << log))
+           (p.t.half << log) * 2 <= kGradAngles * kThreads &&
+           ((SLOTS >> log) > heads ||
+            ((SLOTS >> log) * 8 > heads &&
+             p.t.tokens * all >= static_cast<long long>(most) * heads * (8 << log))))
       ++log;
     return log;
   };
