@@ -343,3 +343,26 @@ def test_append_many_rows_at_their_places(new, d, e4m3, with_q):
         sl = sl / ds
         tol = (E4M3 if e4m3 else BF16) * (x.abs() + sl) + sl + (2.0 ** -10 if e4m3 else 0)
         assert torch.all((got - x).abs() <= tol)
+
+
+def test_offsets_past_32_bits():
+    """Positions so far apart in memory that their offsets pass 2^31 values."""
+    import exact_attention_27_gb300 as fa
+    B, H, N, d = 1, 3, 21, 128
+    p = Problem(B, H, H, N, d, d, seed=9)
+    norm, positions, rotary = p.handles()
+    q, k, dq, dk = (x.cuda() for x in (p.q, p.k, p.dq, p.dk))
+    apart = 2 ** 31 // 20 // 64 * 64 + 64
+    far = [torch.empty(20 * apart + H * d, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    x, g, out = (t.as_strided((B, H, N, d), (0, d, apart, 1)) for t in far)
+    x.copy_(q)
+    g.copy_(dq)
+    a, b = torch.empty_like(q), torch.empty_like(k)
+    fa.fa_norm_rotary(x, out, k, b, norm, positions, rotary)
+    p.check_forward(out, b)
+    dqw, dkw = torch.empty(2, d, device="cuda")
+    ws = fa.norm_rotary_workspace(d)
+    fa.fa_norm_rotary_backward(g, out, dk, b, x, k, norm, dqw, dkw, ws, positions, rotary)
+    p.check_backward(out, b, dqw, dkw)
+    fa.fa_norm_rotary_backward(g, a, None, None, x, None, norm, None, None, ws, positions, rotary)
+    assert torch.equal(a, out)

@@ -334,3 +334,22 @@ def test_long_windows_and_steep_heads(d, softcap):
     Problem(1, 3, 3, N, d, causal=True, softcap=softcap, slopes=[0.7, 0.12, 0.05],
             seed=d + 2).check()
     Problem(1, 2, 1, 1400, d, softcap=softcap, slopes=[-0.2, 0.1], q_offset=90, seed=d + 3).check()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values of k: 5 queries at its end, behind a window."""
+    import exact_attention_27_gb300 as fa
+    d, few, many = 128, 1100, 17_000_000
+    p = Problem(1, 2, 1, 5, d, Nkv=few, q_offset=few - 5, causal=True, window=1000,
+                slopes=[0.3, 0.01], seed=4)
+    scores, _ = p.handles()
+    q, do = p.q.cuda(), p.do.cuda()
+    k, v = (torch.zeros(1, 1, many, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[:, :, -few:], v[:, :, -few:] = p.k.cuda(), p.v.cuda()
+    o, lse = fa.attention_forward(q, k, v, causal=True, q_offset=many - 5, scores=scores)
+    dq, dk, dv = fa.attention_backward(q, k, v, o, lse, do, causal=True, q_offset=many - 5,
+                                       scores=scores)
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_error() == 0
+    assert not torch.any(dk[:, :, :-few]) and not torch.any(dv[:, :, :-few])
+    p.check({"o": o, "lse": lse, "dq": dq, "dk": dk[:, :, -few:], "dv": dv[:, :, -few:]})
