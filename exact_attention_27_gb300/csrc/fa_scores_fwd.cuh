@@ -200,13 +200,14 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
   return alpha;
 }
 
-// A row's O out of TMEM at `col_o` (any: there is one) over l, and its lse; zeros and
+// A row's O out of TMEM at `col_o` (any: there is one) over `weight`, and its lse; zeros and
 // -infinity for a row that sees no key.  Every GROUPS-th part of 32 columns, from the g-th on.
 // The whole warp calls this.
 template <int D, int GROUPS>
 __device__ __forceinline__ void store_row(const ScoreFwdParams& p, int bh, int qi, uint32_t col_o,
-                                          int g, bool any, bool empty, float m, float l) {
-  const float inv_l = 1.0f / l;
+                                          int g, bool any, bool empty, float m, float l,
+                                          float weight) {
+  const float inv_l = 1.0f / weight;
   const bool live = qi < p.s.Nq;
   __nv_bfloat16* orow = p.o + (static_cast<size_t>(bh) * p.s.Nq + (live ? qi : 0)) * D;
 #pragma unroll 1
@@ -462,8 +463,12 @@ __global__ void __launch_bounds__((ScoreFwdCfg<D, FIXED>::THREADS), 1)
                                              kErrTimeoutEpilogue));
     if (ok) {
       tc_fence_after();
+      // A row of one key is its v: over the weight as P holds it (with a moving reference it is 1).
+      const float weight = FIXED && span.hi - span.lo == 1
+                               ? __bfloat162float(__float2bfloat16_rn(l))
+                               : l;
       store_row<D, C::GROUPS>(p, bh, qi, tmem + lane_off + C::COL_O, g, n_kv > 0, span.hi == 0,
-                              m_used, l);
+                              m_used, l, weight);
     }
   }
 

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(384, 1)
                                              err, kErrTimeoutEpilogue));
     if (ok) {
       tc_fence_after();
-      store_row<D, 1>(p, bh, qi, col_o, 0, j1 > j0, span.hi == 0, m_used, l);
+      store_row<D, 1>(p, bh, qi, col_o, 0, j1 > j0, span.hi == 0, m_used, l, l);
     }
   }
 

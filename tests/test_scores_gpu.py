@@ -353,3 +353,13 @@ def test_offsets_past_32_bits():
     assert fa.fa_last_device_error() == 0
     assert not torch.any(dk[:, :, :-few]) and not torch.any(dv[:, :, :-few])
     p.check({"o": o, "lse": lse, "dq": dq, "dk": dk[:, :, -few:], "dv": dv[:, :, -few:]})
+
+
+@pytest.mark.parametrize("softcap", [0.0, 5.0, 50.0, 70.0])
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+def test_a_row_of_one_key_is_its_v(d, softcap):
+    """To the bit: v is in bf16, and the weight over itself is 1 to fp32."""
+    p = Problem(1, 2, 1, 300, d, causal=True, window=1, softcap=softcap, seed=d)
+    got = p.run()
+    assert torch.equal(got["o"].cpu(), p.v.expand(1, 2, 300, d))
+    p.check(got)
