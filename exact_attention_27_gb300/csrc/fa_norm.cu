@@ -163,8 +163,13 @@ struct Angles {
       const int i = threadIdx.x + e * kThreads;
       const int w = p.half > 0 ? i / p.half : tok;
       place[e] = w < tok ? w : -1;
-      from[e] = p.positions && w < tok ? p.positions + p.axis[i - w * p.half] * p.axis_stride
-                                       : nullptr;
+      from[e] = nullptr;
+      if (p.positions && w < tok) {
+        // (four axes a word: the constant cache serves one address of a warp at a time)
+        const int pair = i - w * p.half;
+        const uint32_t four = reinterpret_cast<const uint32_t*>(p.axis)[pair >> 2];
+        from[e] = p.positions + (four >> (8 * (pair & 3)) & 0xffu) * p.axis_stride;
+      }
       pos[e] = 0;
     }
   }

@@ -51,7 +51,7 @@ struct TurnParams {
   int half;         // pairs turned, rot_dim / 2
   int interleaved;
   float sign;       // -1 for the gradient
-  unsigned char axis[kMaxPairs];
+  alignas(4) unsigned char axis[kMaxPairs];
   // norms of the heads' rows before they are turned
   const void* q_weight;  // [d], nullptr: ones
   const void* k_weight;
