@@ -12,6 +12,7 @@
 #include "fa_internal.h"
 #include "fa_paged_host.h"
 #include "fa_ptx.cuh"
+#include "fa_scores_host.h"
 
 namespace {
 

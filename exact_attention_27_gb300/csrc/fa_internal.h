@@ -206,11 +206,9 @@ cudaError_t launch_backward_dq(const BwdMaps& m, const float* lse, const float* 
 
 // Helpers defined in fa_api.cu for other translation units: the per-device
 // error word the kernels' bounded waits report into, and tensor-map encoding
-// for bf16 [planes][N][d] tensors (boxes of 128 rows; `kv`: of one key tile) and the
-// fp32 dQ accumulator.
+// for bf16 [planes][N][d] tensors and the fp32 dQ accumulator.
 uint32_t* device_error_word();
 bool encode_map_bf16(CUtensorMap* m, const void* ptr, int d, int N, long long planes);
-bool encode_map_kv_bf16(CUtensorMap* m, const void* ptr, int d, int N, long long planes);
 bool encode_map_f32_acc(CUtensorMap* m, const void* ptr, int d, int N, long long planes);
 bool encode_map_f32_acc32(CUtensorMap* m, const void* ptr, int d, int N, long long planes);
 

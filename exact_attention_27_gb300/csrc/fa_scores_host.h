@@ -65,6 +65,9 @@ struct ScoreMaps {
   CUtensorMap k, v;   // boxes of 64 columns x 128 rows (64 rows at d = 256)
 };
 
+// As encode_map_bf16 (fa_internal.h), with boxes of one key tile's rows (fa_api.cu).
+bool encode_map_kv_bf16(CUtensorMap* m, const void* ptr, int d, int N, long long planes);
+
 // Fills in what `spec` (may be NULL) and `scale` say; refuses what it cannot hold.
 fa_status put_scores(ScoreParams* p, const fa_score_spec* spec, float scale);
 int score_mode(const ScoreParams& p);
