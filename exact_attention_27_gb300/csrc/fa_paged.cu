@@ -240,6 +240,7 @@ fa_status forward_paged(const fa_paged_cache* cache, const fa_paged_batch* batch
   p.scale_log2 = s_eff * kPagedLog2e;
   p.v_scale = cache->v_descale;
   p.cap2 = shape.f.cap2;
+  p.f = cache->dtype == FA_CACHE_E4M3 ? score_factors(1.0f, shape.f.cap2) : shape.f;
   p.slopes = shape.slopes;
   p.window = shape.window;
   char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) &

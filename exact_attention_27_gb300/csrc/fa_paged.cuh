@@ -28,6 +28,7 @@
 
 #include "fa_paged_host.h"
 #include "fa_ptx.cuh"
+#include "fa_scores_host.h"
 
 namespace fa {
 
@@ -113,6 +114,7 @@ struct PagedParams {
   // Shaped scores (fa_score_spec; the SHAPED kernels): softcap log2(e), 0: none; slopes, nullptr:
   // none; window, 0: none.
   float cap2;
+  ScoreFactors f;  // of the tcgen05 kernels: of products over bf16 pages, of y over e4m3 pages
   const float* slopes;
   int window;
   float* part_o;           // [CTA][2][ROWS][D]

@@ -128,12 +128,12 @@ __device__ __forceinline__ void shape_rows(const PagedParams& p, float (&s)[2][4
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float v[4], none[1];
-    auto load = [&](float (&y)[4]) {
+    auto load = [&](float (&y)[4], int) {
       y[0] = s[0][2 * h] * by[h], y[1] = s[0][2 * h + 1] * by[h];
       y[2] = s[1][2 * h] * by[h], y[3] = s[1][2 * h + 1] * by[h];
     };
-    load(v);
-    if (p.cap2 > 0.0f) shape_scores<4, true, false, false>(v, none, f, 0.0f, 0.0f, 0.0f, load);
+    load(v, 0);
+    if (p.cap2 > 0.0f) shape_scores<4, true, false, false, false>(v, none, f, 0.0f, 0.0f, 0.0f, load);
     if (p.slopes) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {

@@ -206,26 +206,25 @@ __device__ __forceinline__ float paged_softmax(const PagedParams& p, const Paged
     // folded into a row's own coefficients, and out of its c, instead: 347 us for 329).
     const bool cap = p.cap2 > 0.0f;
     const float by = cap ? c / p.cap2 : c;
-    const float k = F16 || !cap ? 1.0f : by;
-    const ScoreFactors f = score_factors(k, p.cap2);
     float none[1];
-    auto load = [&](float (&z)[BN]) {
-      uint32_t r[BN];
+    auto load = [&](auto& z, int c0) {
+      constexpr int N = sizeof(z) / sizeof(float);
+      uint32_t r[N];
 #pragma unroll
-      for (int q = 0; q < BN / 32; ++q)
-        tmem_ld32(s_addr + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * q]));
+      for (int q = 0; q < N / 32; ++q)
+        tmem_ld32(s_addr + c0 + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * q]));
       tmem_wait_ld();
 #pragma unroll
-      for (int t = 0; t < BN; ++t) z[t] = __uint_as_float(r[t]);
+      for (int t = 0; t < N; ++t) z[t] = __uint_as_float(r[t]);
       if (F16 || !cap) {
         const uint64_t by2 = f2_pack(by, by);
 #pragma unroll
-        for (int t = 0; t < BN; t += 2)
+        for (int t = 0; t < N; t += 2)
           f2_unpack(f2_mul(f2_pack(z[t], z[t + 1]), by2), z[t], z[t + 1]);
       }
     };
-    load(s);
-    if (cap) shape_scores<BN, true, false, false>(s, none, f, 0.0f, 0.0f, 0.0f, load);
+    load(s, 0);
+    if (cap) shape_scores<BN, true, false, false, !F16>(s, none, p.f, 0.0f, 0.0f, 0.0f, load);
     if (p.slopes) lower_scores<BN>(s, x.slope2, static_cast<float>(x.pos - kbase));
     c = 1.0f;
   } else {

@@ -17,7 +17,9 @@
 // operations on the FMA pipe in place of the one that scales a score, where one ex2 and one rcp
 // more for each score would take the special-function unit longer than the weights' own
 // exponentials.  A warp with a score beyond goes by tanh y = 1 - 2 / (e^{2y} + 1), which holds
-// everywhere, to 2e-7.  (16 heads of 8192, d = 64, causal: dQ takes 381 us if all go that way.)
+// everywhere, to 2e-7 of the cap.  (16 heads of 8192, d = 64, causal: dQ takes 381 us if all go
+// that way.)  Caps of many thousands, whose folded coefficients would leave fp32's range, choose
+// between the two score by score: there 2e-7 of the cap is more than a score.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -126,7 +128,7 @@ __device__ __forceinline__ void lower_scores(float (&s)[N], float slope2, float 
 }
 
 // shape_scores where it is known whether dist0 - t has one sign (Lowering).
-template <int N, bool CAP, bool BIAS, bool GRAD, bool ONE, typename Again>
+template <int N, bool CAP, bool BIAS, bool GRAD, bool FOLDS, bool ONE, typename Again>
 __device__ __forceinline__ void shape_columns(float (&s)[N], float (&g)[GRAD ? N : 1],
                                               const ScoreFactors& f, float slope2, float dist0,
                                               float sub, float side, Again&& again) {
@@ -158,17 +160,42 @@ __device__ __forceinline__ void shape_columns(float (&s)[N], float (&g)[GRAD ? N
     for (int u = 1; u < CHAINS; ++u) big = fmaxf(big, part[u]);
     // (a NaN takes either way to a NaN)
     if (__any_sync(0xffffffffu, big > f.range)) {
-      again(s);
       Lowering<N, BIAS, ONE> more(slope2, dist0, sub, side);
+      constexpr int P = N < 32 ? N : 32;  // columns put back at a time
 #pragma unroll
-      for (int t = 0; t < N; t += 2) {
-        float lower[2];
-        f2_unpack(more.pair(t), lower[0], lower[1]);
+      for (int c0 = 0; c0 < N; c0 += P) {
+        float(&y)[P] = *reinterpret_cast<float(*)[P]>(&s[c0]);
+        again(y, c0);
+        if (FOLDS && f.range < 0.0f) {
+          // Scores one by one: within the polynomial's reach by it (the other way is off by as
+          // much of a large cap, more than the scores themselves).
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float r = rcp_approx(ex2_approx(s[t + e] * (2.0f * kScoreLog2e * f.k)) + 1.0f);
-          s[t + e] = fmaf(-2.0f * f.cap2, r, f.cap2) + lower[e];
-          if constexpr (GRAD) g[t + e] = 4.0f * r * (1.0f - r);
+          for (int t = 0; t < P; t += 2) {
+            float lower[2];
+            f2_unpack(more.pair(c0 + t), lower[0], lower[1]);
+#pragma unroll
+            for (int e = t; e < t + 2; ++e) {
+              const float z = y[e] * f.k, z2 = z * z;
+              const float h =
+                  z * fmaf(fmaf(fmaf(kTanhC3, z2, kTanhC2), z2, kTanhC1), z2, kTanhC0);
+              const float r = rcp_approx(ex2_approx(z * (2.0f * kScoreLog2e)) + 1.0f);
+              const bool near = fabsf(z) <= kTanhRange;
+              y[e] = (near ? f.cap2 * h : fmaf(-2.0f * f.cap2, r, f.cap2)) + lower[e - t];
+              if constexpr (GRAD) g[c0 + e] = near ? fmaf(-h, h, 1.0f) : 4.0f * r * (1.0f - r);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < P; t += 2) {
+            float lower[2];
+            f2_unpack(more.pair(c0 + t), lower[0], lower[1]);
+#pragma unroll
+            for (int e = t; e < t + 2; ++e) {
+              const float r = rcp_approx(ex2_approx(y[e] * (2.0f * kScoreLog2e * f.k)) + 1.0f);
+              y[e] = fmaf(-2.0f * f.cap2, r, f.cap2) + lower[e - t];
+              if constexpr (GRAD) g[c0 + e] = 4.0f * r * (1.0f - r);
+            }
+          }
         }
       }
     }
@@ -183,10 +210,11 @@ __device__ __forceinline__ void shape_columns(float (&s)[N], float (&g)[GRAD ? N
 // What turns raw products s = q.k of keys kbase + t, t = 0 .. N-1, into exponents of the
 // weights, x (log2 domain), less `sub`:  CAP x = cap tanh(s k) (in f), else x = s f.k;
 // BIAS then - slope2 |pos - key|, dist0 = pos - kbase.  With GRAD, g gets 1 - tanh^2.  The
-// whole warp calls this (f may differ between its lanes).  `again` puts the products into s
-// once more, for the warp that finds only after the polynomial that it did not hold (to look
-// first would have all of the arithmetic wait for all of the maxima: 5 % of dQ).
-template <int N, bool CAP, bool BIAS, bool GRAD, typename Again>
+// whole warp calls this (f may differ between its lanes).  `again` puts the products of columns
+// from c0 on into its argument once more, for the warp that finds only after the polynomial that
+// it did not hold (to look first would have all of the arithmetic wait for all of the maxima: 5 %
+// of dQ).  FOLDS: the coefficients take in factors, and may not hold it at all.
+template <int N, bool CAP, bool BIAS, bool GRAD, bool FOLDS = true, typename Again>
 __device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N : 1],
                                              const ScoreFactors& f, float slope2, float dist0,
                                              float sub, Again&& again) {
@@ -194,12 +222,12 @@ __device__ __forceinline__ void shape_scores(float (&s)[N], float (&g)[GRAD ? N 
     const bool before = __all_sync(0xffffffffu, dist0 >= static_cast<float>(N - 1));
     const bool after = __all_sync(0xffffffffu, dist0 <= 0.0f);
     if (before || after)
-      shape_columns<N, CAP, BIAS, GRAD, true>(s, g, f, slope2, dist0, sub, before ? 1.0f : -1.0f,
-                                              again);
+      shape_columns<N, CAP, BIAS, GRAD, FOLDS, true>(s, g, f, slope2, dist0, sub,
+                                                     before ? 1.0f : -1.0f, again);
     else
-      shape_columns<N, CAP, BIAS, GRAD, false>(s, g, f, slope2, dist0, sub, 0.0f, again);
+      shape_columns<N, CAP, BIAS, GRAD, FOLDS, false>(s, g, f, slope2, dist0, sub, 0.0f, again);
   } else {
-    shape_columns<N, CAP, false, GRAD, false>(s, g, f, slope2, dist0, sub, 0.0f, again);
+    shape_columns<N, CAP, false, GRAD, FOLDS, false>(s, g, f, slope2, dist0, sub, 0.0f, again);
   }
 }
 

@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(ScoreDkdvCfg<D>::THREADS, 1)
         float(&x)[CH] = *reinterpret_cast<float(*)[CH]>(&w[c0]);
         float gr[CAP ? CH : 1];
         shape_scores<CH, CAP, BIAS, CAP>(
-            x, gr, p.s.f, slope_now, dist0 - c0, L2, [&](float (&y)[CH]) {
+            x, gr, p.s.f, slope_now, dist0 - c0, L2, [&](float (&y)[CH], int) {
               load_scores(tmem + lane_off + C::COL_S + 32 * g + c0, y);
             });
 #pragma unroll

@@ -367,9 +367,10 @@ __global__ void __launch_bounds__(ScoreDqCfg<D>::THREADS, 1)
       for (int c0 = 0; c0 < KH; c0 += CH) {
         float(&x)[CH] = *reinterpret_cast<float(*)[CH]>(&w[c0]);
         float gr[CAP ? CH : 1];
-        shape_scores<CH, CAP, BIAS, CAP>(x, gr, p.s.f, slope2, dist0 - c0, L2, [&](float (&y)[CH]) {
-          load_scores(tmem + lane_off + scol + c0, y);
-        });
+        shape_scores<CH, CAP, BIAS, CAP>(x, gr, p.s.f, slope2, dist0 - c0, L2,
+                                         [&](float (&y)[CH], int) {
+                                           load_scores(tmem + lane_off + scol + c0, y);
+                                         });
 #pragma unroll
         for (int t = 0; t < CH; t += 2) {
           uint64_t v = f2_pack(ex2_approx(x[t]), ex2_approx(x[t + 1]));

@@ -96,18 +96,20 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
 #pragma unroll
   for (int u = 0; u < 4; ++u) ps2[u] = 0ull;
   float alpha = 1.0f;
-  auto load = [&](float (&x)[BN]) {
-    uint32_t r[BN];
+  // Products of columns from c0 on.
+  auto load = [&](auto& x, int c0) {
+    constexpr int N = sizeof(x) / sizeof(float);
+    uint32_t r[N];
 #pragma unroll
-    for (int c = 0; c < BN / 32; ++c)
-      tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
+    for (int c = 0; c < N / 32; ++c)
+      tmem_ld32(s_addr + c0 + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
     tmem_wait_ld();
 #pragma unroll
-    for (int t = 0; t < BN; ++t) x[t] = __uint_as_float(r[t]);
+    for (int t = 0; t < N; ++t) x[t] = __uint_as_float(r[t]);
   };
   if constexpr (FIXED) {
     float x[BN], none[1];
-    load(x);
+    load(x, 0);
     shape_scores<BN, CAP, BIAS, false>(x, none, p.f, slope2,
                                        static_cast<float>(pos - kbase), m, load);
     if (mask) {
@@ -130,7 +132,7 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
     // Without a tanh or a distance the scale waits for the exponents' multiply-add.
     constexpr bool RAW = !CAP && !BIAS;
     if constexpr (RAW) {
-      load(s);
+      load(s, 0);
     } else {
       // All columns at once, or 64 with the tanh and distances too, where all spill (16 heads of
       // 8192, two tiles at d = 64, one at d = 128: distances 219 / 210 / 207 and 306 / 286 / 276 us
@@ -140,18 +142,10 @@ __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr
       for (int c0 = 0; c0 < BN; c0 += PART) {
         float(&y)[PART] = *reinterpret_cast<float(*)[PART]>(&s[c0]);
         float none[1];
-        auto part = [&](float (&z)[PART]) {
-          uint32_t r[PART];
-#pragma unroll
-          for (int c = 0; c < PART / 32; ++c)
-            tmem_ld32(s_addr + c0 + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
-          tmem_wait_ld();
-#pragma unroll
-          for (int t = 0; t < PART; ++t) z[t] = __uint_as_float(r[t]);
-        };
-        part(y);
+        load(y, c0);
         shape_scores<PART, CAP, BIAS, false>(y, none, p.f, slope2,
-                                             static_cast<float>(pos - kbase - c0), 0.0f, part);
+                                             static_cast<float>(pos - kbase - c0), 0.0f,
+                                             [&](auto& z, int c1) { load(z, c0 + c1); });
       }
     }
     if (mask) {

@@ -14,7 +14,8 @@ namespace fa {
 struct ScoreFactors {
   float k;      // CAP: the tanh's factor of q.k, scale / softcap; otherwise scale log2(e)
   float cap2;   // softcap log2(e); 0: none
-  // cap2 tanh(s k) = s (a0 + a1 s^2 + a2 s^4 + a3 s^6) for |s| <= range (below 0: never)
+  // cap2 tanh(s k) = s (a0 + a1 s^2 + a2 s^4 + a3 s^6) for |s| <= range; below 0: these do not
+  // hold the polynomial
   float a[4];
   float range;
   float neg_inv_cap_sq;  // -1 / cap2^2
@@ -27,6 +28,9 @@ constexpr float kTanhC1 = -0.33331362458867403f;
 constexpr float kTanhC2 = 0.13270976757985897f;
 constexpr float kTanhC3 = -0.04755360359006216f;
 
+// For k = 1 the coefficients are the tanh's own times cap2.  Otherwise they hold caps up to some
+// thousands at usual scales; beyond (and where any of them leaves fp32's range otherwise) range is
+// -1, and shape_columns takes each score by itself.
 __host__ __device__ inline ScoreFactors score_factors(float k, float cap2) {
   ScoreFactors f;
   f.k = k;
@@ -36,9 +40,10 @@ __host__ __device__ inline ScoreFactors score_factors(float k, float cap2) {
   f.a[1] = kTanhC1 * cap2 * k * k2;
   f.a[2] = kTanhC2 * cap2 * k * k2 * k2;
   f.a[3] = kTanhC3 * cap2 * k * k2 * k2 * k2;
-  // (where a coefficient leaves fp32's range, the other way always)
   const float last = f.a[3] < 0.0f ? -f.a[3] : f.a[3];
-  f.range = k2 > 1e-18f && k2 < 1e12f && last > 1e-30f && last < 1e30f ? kTanhRange / k : -1.0f;
+  f.range = k == 1.0f || (k2 > 1e-18f && k2 < 1e12f && last > 1e-30f && last < 1e30f)
+                ? kTanhRange / k
+                : -1.0f;
   f.neg_inv_cap_sq = cap2 > 0.0f ? -1.0f / (cap2 * cap2) : 0.0f;
   return f;
 }

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(320, 1)
       for (int e = 0; e < 32; ++e) pv[e] = __uint_as_float(sv[e]);
       shape_scores<32, CAP, BIAS, CAP>(
           pv, gr, p.s.f, slope2, static_cast<float>(p.s.q_offset + it * C::BQ + row - kbase), L2,
-          [&](float (&y)[32]) { load_scores(tmem + lane_off + C::COL_S + 32 * g, y); });
+          [&](float (&y)[32], int) { load_scores(tmem + lane_off + C::COL_S + 32 * g, y); });
 #pragma unroll
       for (int e = 0; e < 32; ++e) pv[e] = ex2_approx(pv[e]);
       if (masked) {
