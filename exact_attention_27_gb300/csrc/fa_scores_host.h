@@ -30,7 +30,8 @@ constexpr float kTanhC3 = -0.04755360359006216f;
 
 // For k = 1 the coefficients are the tanh's own times cap2.  Otherwise they hold caps up to some
 // thousands at usual scales; beyond (and where any of them leaves fp32's range otherwise) range is
-// -1, and shape_columns takes each score by itself.
+// -1, and shape_columns takes each score by itself; as it is for caps so small that 1 / cap2^2,
+// from which the polynomial's way has 1 - tanh^2, would leave it.
 __host__ __device__ inline ScoreFactors score_factors(float k, float cap2) {
   ScoreFactors f;
   f.k = k;
@@ -41,9 +42,9 @@ __host__ __device__ inline ScoreFactors score_factors(float k, float cap2) {
   f.a[2] = kTanhC2 * cap2 * k * k2 * k2;
   f.a[3] = kTanhC3 * cap2 * k * k2 * k2 * k2;
   const float last = f.a[3] < 0.0f ? -f.a[3] : f.a[3];
-  f.range = k == 1.0f || (k2 > 1e-18f && k2 < 1e12f && last > 1e-30f && last < 1e30f)
-                ? kTanhRange / k
-                : -1.0f;
+  const bool holds =
+      k == 1.0f || (k2 > 1e-18f && k2 < 1e12f && last > 1e-30f && last < 1e30f);
+  f.range = cap2 > 1e-15f && holds ? kTanhRange / k : -1.0f;
   f.neg_inv_cap_sq = cap2 > 0.0f ? -1.0f / (cap2 * cap2) : 0.0f;
   return f;
 }

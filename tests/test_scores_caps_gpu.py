@@ -1,4 +1,4 @@
-"""Caps far above the scores, against 64-bit values."""
+"""Caps far above and far below the scores, against 64-bit values."""
 
 import math
 
@@ -8,6 +8,7 @@ import torch
 import scores_plain
 import test_paged_scores_gpu as paged
 from paged_plain import Step
+from scores_plain import off_by, whole
 from test_scores_gpu import Problem, _built, alibi  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,44 @@ def test_caps_far_above_the_scores_over_pages(monkeypatch, new, d, e4m3):
             x.norm(dim=2).max() for x in step.k64) / math.sqrt(d)
         share_of_scores(monkeypatch, softcap, far.item())
         paged.go(step, softcap=softcap)
+
+
+# ------------------------------------------------------------------ caps far below the scores
+
+def derivative_slack(p):
+    """What fp32 sums of d products (d + 2 roundings with the scale, 2^-24 of the sum of sizes each)
+    do to the cap's derivative: its argument is off by e = (d + 2) 2^-24 size / softcap, and
+    1 - tanh^2 moves by 2 tanh (1 - tanh^2) <= 4 / sqrt(27) < 0.77 of that, and by 1 at most.  Heads'
+    bounds of dq and dk take this as nothing, which it is but for caps of next to nothing."""
+    n, d = p.q.shape[2:]
+    dq, dk = torch.zeros(p.q.shape).double(), torch.zeros(p.k.shape).double()
+    dist = (torch.arange(n)[:, None] - torch.arange(n)).double()
+    for h in range(p.q.shape[1]):
+        q, k, v, do = (x.double() for x in (p.q[0, h], p.k[0, 0], p.v[0, 0], p.do[0, h]))
+        x = p.softcap * torch.tanh(q @ k.T * p.scale / p.softcap)
+        x = x - dist.abs() * (0.0 if p.slopes is None else p.slopes[h].item())
+        w = torch.softmax(x.masked_fill(dist < 0, -math.inf), 1)
+        dp = do @ v.T
+        e = (d + 2) * 2.0 ** -24 * (q.abs() @ k.abs().T) * p.scale / p.softcap
+        loose = w * (0.77 * e).clamp(max=1.0) * (dp - (w * dp).sum(1, keepdim=True)).abs()
+        dq[0, h] = loose @ k.abs() * p.scale
+        dk[0, 0] += loose.T @ q.abs() * p.scale
+    return {"dq": dq, "dk": dk}
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("slopes", [None, [0.02, 0.0]])
+@pytest.mark.parametrize("gain", [0.005, 0.3])  # within 0.4 caps, and past them
+@pytest.mark.parametrize("softcap, scale", [(1e-20, 1e-20), (4e-20, 1e-21), (1e-37, 1e-36),
+                                            (1e-15, 1e-15), (1e-8, 0.125), (1e-12, 1e-13)])
+def test_caps_whose_square_is_next_to_nothing(softcap, scale, gain, slopes, d):
+    """Scores of next to nothing weigh all keys alike; the cap's derivative still tells which
+    scores get a gradient."""
+    p = Problem(1, 2, 1, 150, d, causal=True, softcap=softcap, scale=scale, slopes=slopes, gain=gain,
+                seed=d)
+    val, tol = whole(p.q, p.k, p.v, p.see(), scale, softcap, p.slopes, do=p.do)
+    for name, x in derivative_slack(p).items():
+        tol[name] += x
+    got = p.run()
+    for name in val:
+        assert off_by(got[name], val[name], tol[name]) <= 1, name
