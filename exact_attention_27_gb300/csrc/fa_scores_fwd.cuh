@@ -7,13 +7,15 @@
 // that the union of the rows' spans touches, counted from its first.
 //
 // A capped score cannot pass softcap, so with no distance term the reference that the
-// online softmax subtracts is fixed, at half the cap's exponent, as long as all weights then
-// stay within fp32's (and bf16's) exponents: no running maximum and no rescaling of O.  For
-// softcap log2(e) <= kFixedCap the weights lie in [2^-(1.5 kFixedCap), 2^(kFixedCap / 2)].  A row's
-// 128 keys of a tile then go to four warps, 32 each (16 heads of 8192, cap, d = 64 / 96 / 128: 201
-// / 219 / 228 us with four, 218 / 229 / 234 with two, 231 / 243 / 249 with one; two tiles a CTA
-// 205 / 227 / 284).  With a moving reference, warps that share a row have to exchange maxima each
-// tile, and wait for one another: slower with two or four than with one.
+// online softmax subtracts is fixed, at 0, as long as weights and their sums then stay within
+// fp32's (and bf16's) exponents: no running maximum and no rescaling of O.  For softcap log2(e) <=
+// kFixedCap the weights lie in [2^-kFixedCap, 2^kFixedCap], in the middle of the exponents: a row
+// at either end of the cap has its v whole down to 2^-46 and up to 2^47 over its keys (with half
+// the cap as the reference, v of 2^-18 was cut at the lower end).  A row's 128 keys of a tile then
+// go to four warps, 32 each (16 heads of 8192, cap, d = 64 / 96 / 128: 201 / 219 / 228 us with
+// four, 218 / 229 / 234 with two, 231 / 243 / 249 with one; two tiles a CTA 205 / 227 / 284).  With
+// a moving reference, warps that share a row have to exchange maxima each tile, and wait for one
+// another: slower with two or four than with one.
 //
 // Bound by the softmax's instructions: 55 % of the issue slots with a cap; 33 % without, where one
 // warp a scheduler waits for its own results (d = 128, uncapped: 205 us, 1.34 PFLOP/s).
@@ -85,7 +87,7 @@ struct ScoreFwdParams {
 // The scores of a row's key tile (BN keys from kbase on) at TMEM address `s_addr` to P over
 // them, with the running reference m and sum l (log2 domain); keys outside `span` get 0 where
 // `mask`.  Returns the factor that O and the old l are due (1 unless `moved`).  FIXED: m is
-// the reference, cap2 / 2, and stays.  The whole warp calls this.
+// the reference, 0, and stays.  The whole warp calls this.
 template <int BN, bool CAP, bool BIAS, bool FIXED>
 __device__ __forceinline__ float score_row(const ScoreParams& p, uint32_t s_addr, bool mask,
                                            const KeySpan& span, int kbase, int pos, float slope2,
@@ -229,7 +231,7 @@ __device__ __forceinline__ void store_row(const ScoreFwdParams& p, int bh, int q
         empty ? -INFINITY : (m + log2f(l)) * kScoreLn2;
 }
 
-// FIXED: the softmax reference is p.s.f.cap2 / 2.
+// FIXED: the softmax reference is 0.
 template <int D, bool CAP, bool BIAS, bool FIXED>
 __global__ void __launch_bounds__((ScoreFwdCfg<D, FIXED>::THREADS), 1)
     fa_scores_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__((ScoreFwdCfg<D, FIXED>::THREADS), 1)
     const int qi = qt * C::BM + row;
     const float slope2 = BIAS && p.s.slopes ? p.s.slopes[hq] * kScoreLog2e : 0.0f;
     const int pos = p.s.q_offset + qi;
-    float m_used = FIXED ? 0.5f * p.s.f.cap2 : -INFINITY;  // reference, log2 domain
+    float m_used = FIXED ? 0.0f : -INFINITY;  // reference, log2 domain
     float l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n_kv; ++j) {

@@ -9,8 +9,8 @@
 namespace fa {
 namespace {
 
-// Caps up to here (log2 domain; 55 in scores) have a fixed reference: weights down to
-// 2^-120 and up to 2^40.
+// Caps up to here (log2 domain; 55 in scores) have a fixed reference, 0: weights from 2^-80 to
+// 2^80.
 constexpr float kFixedCap = 80.0f;
 
 // One query tile a CTA or two: as for the unshaped forward, whose steps cost about the same

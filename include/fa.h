@@ -291,7 +291,9 @@ typedef struct {
 
 /*
  * Forward pass with shaped scores: fa_forward_ex with `spec` and `spans` (either may be NULL).
- * The tanh is off by 2e-7 at most (times softcap in the score).  Returns as fa_forward.
+ * The tanh is off by 2e-7 at most (times softcap in the score).  With a softcap up to 55 and no
+ * slopes, sums are held as exp(x) v: a row all of whose scores lie at an end of the cap keeps v
+ * whole from 2^-46 to 2^47 / N_kv.  Returns as fa_forward.
  */
 fa_status fa_forward_scores(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                             int H_q, int H_kv, int N_q, int N_kv, int d, float scale, int causal,

@@ -1,4 +1,4 @@
-"""Caps far above and far below the scores, against 64-bit values."""
+"""Caps far above and far below the scores, and scores at a cap's ends, against 64-bit values."""
 
 import math
 
@@ -86,3 +86,35 @@ def test_caps_whose_square_is_next_to_nothing(softcap, scale, gain, slopes, d):
     got = p.run()
     for name in val:
         assert off_by(got[name], val[name], tol[name]) <= 1, name
+
+
+# ------------------------------------------------------------------ scores at the ends of a cap
+
+def at_the_end(d, sign, softcap, window, octaves, gain=6.0, N=300):
+    """Every score is tanh(sign gain) of the cap; v goes through 2^octaves."""
+    p = Problem(1, 2, 1, N, d, causal=True, window=window, softcap=softcap, scale=1.0, seed=d)
+    p.q, p.k = torch.zeros_like(p.q), torch.zeros_like(p.k)
+    p.q[..., 0], p.k[..., 0] = sign * gain, softcap
+    away = torch.tensor([2.0 ** octaves[j % len(octaves)] for j in range(N)])
+    p.v = (p.v.float() * away[:, None]).to(torch.bfloat16)
+    return p
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("softcap", [30.0, 50.0, 55.0, 56.0])
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+def test_a_row_of_one_key_at_the_ends_of_the_cap_is_its_v(d, softcap, sign):
+    """To the bit, whatever v's size: v below 2^-40 and beyond 2^40 too."""
+    p = at_the_end(d, sign, softcap, 1, range(-40, 41))
+    got = p.run()
+    assert torch.equal(got["o"].cpu(), p.v.expand(1, 2, 300, d))
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("softcap", [50.0, 55.0])
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("octave", [-40, -24, -18, -7, 30])
+def test_rows_at_the_ends_of_the_cap(octave, d, softcap, sign):
+    p = at_the_end(d, sign, softcap, 0, [octave])
+    p.do = (p.do.float() * 2.0 ** -octave).to(torch.bfloat16)
+    p.check()
