@@ -155,6 +155,12 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int s) {
   return g;
 }
 
+// First key that the window leaves the token at `pos`, which may lie any distance before its
+// sequence (pos - window can pass 32 bits there).
+__device__ __forceinline__ int paged_from(const PagedParams& p, int pos) {
+  return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+}
+
 // Items of ROWS rows and key tiles of TK keys.  An item counts for its key
 // tiles and OVER more, about what starting and ending one costs, at FULL units each,
 // or HALF where its rows fill at most half of ROWS.  SHAPED: the scores are shaped, and an
@@ -182,7 +188,7 @@ struct PagedWalk {
                                                   int rt) {
     if (!SHAPED || p.window == 0) return 0;
     const int tok = static_cast<int>(static_cast<uint32_t>(rt * ROWS) / static_cast<uint32_t>(p.G));
-    return max(g.base + tok - p.window + 1, 0);
+    return paged_from(p, g.base + tok);
   }
   // Its key tiles: one at least, so that rows without keys are written too.
   static __device__ __forceinline__ int tiles(const PagedParams& p, const PagedSeq& g, int rt) {

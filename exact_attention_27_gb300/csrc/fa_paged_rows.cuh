@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
         last[i] = p.causal ? w.g.klen - w.g.qlen + tok[i] : w.g.klen - 1;
         if constexpr (SHAPED) {
           const int at = w.g.base + tok[i];
-          first[i] = p.window > 0 ? at - p.window + 1 : 0;
+          first[i] = paged_from(p, at);
           slope2[i] = p.slopes ? p.slopes[head[i]] * kPagedLog2e : 0.0f;
           pos[i] = static_cast<float>(at);
         }
@@ -272,9 +272,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3>::THREADS, RowsCfg<D, E4M3>::O
       const int all_see = p.causal ? w.g.klen - w.g.qlen + w.rt * C::ROWS / p.G : w.g.klen - 1;
       // ... and keys from here on, as far as windows go.
       const int from_all =
-          SHAPED && p.window > 0
-              ? w.g.base + (min(r0 + C::ROWS, rows) - 1) / p.G - p.window + 1
-              : 0;
+          SHAPED ? paged_from(p, w.g.base + (min(r0 + C::ROWS, rows) - 1) / p.G) : 0;
       // Q fragments, from global memory (rows past the sequence: zeros).  For
       // e4m3, K is read 8 bytes a lane, which fixes the order of the columns.
       uint32_t qf[D / 16][4];

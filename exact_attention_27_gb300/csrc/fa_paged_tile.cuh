@@ -66,9 +66,9 @@ __device__ __forceinline__ PagedRow paged_row(const PagedParams& p, const PagedS
     x.pos = s.w.g.base + tok;
     if (p.slopes) x.slope2 = p.slopes[x.head] * kPagedLog2e;
     if (p.window > 0) {
-      x.first = x.pos - p.window + 1;
+      x.first = paged_from(p, x.pos);
       const int last_row = min(s.w.rt * Walk::ROWS + Walk::ROWS, s.w.g.qlen * p.G) - 1;
-      x.all_from = s.w.g.base + last_row / p.G - p.window + 1;
+      x.all_from = paged_from(p, s.w.g.base + last_row / p.G);
     }
   }
   return x;
