@@ -152,7 +152,12 @@ class HeadNorm:
         given = [(n, w) for n, w in (("q_weight", q_weight), ("k_weight", k_weight))
                  if w is not None]
         self.d = self.dtype = None
-        self.device = None if device is None else torch.device(device).index or 0
+        self.device = None
+        if device is not None:
+            device = torch.device(device)
+            if device.type != "cuda":
+                raise ValueError(f"device {device}: a CUDA device is needed")
+            self.device = _device() if device.index is None else device.index
         for name, w in given:
             if w.dtype not in (torch.float32, torch.bfloat16) or not w.is_cuda or w.dim() != 1 or \
                     not w.is_contiguous() or w.data_ptr() & 15:
