@@ -25,8 +25,9 @@ class Scores:
     def __init__(self, softcap=0.0, slopes=None, window=0):
         torch = _load_torch()
         softcap, window = float(softcap), int(window)
-        if not math.isfinite(softcap) or softcap < 0:
-            raise ValueError(f"softcap {softcap}: finite and >= 0 is needed")
+        held = ctypes.c_float(softcap).value  # (0 means no cap, so that none may round to it)
+        if not math.isfinite(held) or softcap < 0 or (held == 0) != (softcap == 0):
+            raise ValueError(f"softcap {softcap}: finite and >= 0 in fp32 is needed")
         if not 0 <= window < 2**31:
             raise ValueError(f"window {window}: 0 to 2**31 - 1 is needed")
         self.slopes, self.softcap, self.window, self.device = slopes, softcap, window, None

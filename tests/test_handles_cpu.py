@@ -19,3 +19,10 @@ def test_a_norm_on_cuda_is_on_the_current_device(monkeypatch):
 def test_a_norm_is_on_a_gpu():
     with pytest.raises(ValueError):
         fa.HeadNorm(device="cpu")
+
+
+@pytest.mark.parametrize("softcap", [1e-50, 1e39, -1e-50])
+def test_a_cap_that_fp32_does_not_hold_is_refused(softcap):
+    """1e-50 would be no cap at all."""
+    with pytest.raises(ValueError):
+        fa.Scores(softcap)
