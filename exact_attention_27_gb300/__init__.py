@@ -24,7 +24,7 @@ Training with rotary positions, and serving from a paged cache (paged.py):
 import ctypes
 import math
 
-from ._lib import FaError, library, status_string  # noqa: F401
+from ._lib import FaError, int32, library, status_string  # noqa: F401
 
 __all__ = [
     "FaError", "fa_forward", "fa_forward_ex", "fa_forward_fp8", "fa_set_forward_tile_rows", "fa_forward_tile_rows_for",
@@ -125,6 +125,7 @@ def fa_forward(q, k, v, o, lse, scale, causal, stream=None):
 
 def fa_forward_ex(q, k, v, o, lse, scale, causal, q_offset=0, stream=None):
     """fa_forward_ex of include/fa.h: q [B,H_q,N_q,d] against k/v [B,H_kv,N_kv,d]."""
+    q_offset = int32("q_offset", q_offset)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must be [B, H, N, d]")
     B, Hq, Nq, d = q.shape
@@ -138,7 +139,7 @@ def fa_forward_ex(q, k, v, o, lse, scale, causal, q_offset=0, stream=None):
     _f32_cuda("lse", lse, (B, Hq, Nq))
     _check(library().fa_forward_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                    lse.data_ptr(), B, Hq, Hkv, Nq, Nk, d, ctypes.c_float(scale),
-                                   int(bool(causal)), int(q_offset), _stream(stream)),
+                                   int(bool(causal)), q_offset, _stream(stream)),
            "fa_forward_ex")
 
 

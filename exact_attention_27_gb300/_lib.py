@@ -84,6 +84,14 @@ def status_string(status):
     return _STATUS.get(int(status), "unknown status")
 
 
+def int32(name, x):
+    """x as an int that a C int holds (ctypes would cut off its upper bits)."""
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} {x} does not fit 32 bits")
+    return x
+
+
 def _declare(lib):
     p, i, f, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
     lib.fa_forward.restype = i

@@ -12,7 +12,7 @@ import ctypes
 import math
 
 from . import _lib, paged
-from ._lib import FaError, library
+from ._lib import FaError, int32, library
 from .paged import _byref, _load_torch, _same_device, _stream
 
 
@@ -148,10 +148,11 @@ def fa_forward_scores(q, k, v, o, lse, scale, causal, q_offset=0, scores=None, s
                       stream=None):
     """fa_forward_scores of include/fa.h: q [B, H_q, N_q, d] against k and v [B, H_kv, N_kv, d];
     writes o and lse."""
+    q_offset = int32("q_offset", q_offset)
     device, *sizes = _checked(q, k, [("v", v, k), ("o", o, q)], lse, scores, spans)
     status = library().fa_forward_scores(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), *sizes,
-        ctypes.c_float(scale), int(bool(causal)), int(q_offset),
+        ctypes.c_float(scale), int(bool(causal)), q_offset,
         scores._ref if scores is not None else None, spans._ref if spans is not None else None,
         _stream(stream, device))
     if status:
@@ -167,7 +168,8 @@ def scores_workspace(q, k, causal, q_offset=0):
         raise ValueError("q and k must be [B, H, N, d]")
     B, Hq, Nq, d = q.shape
     n = library().fa_backward_scores_workspace_bytes(B, Hq, k.shape[1], Nq, k.shape[2], d,
-                                                     int(bool(causal)), int(q_offset))
+                                                     int(bool(causal)),
+                                                     int32("q_offset", q_offset))
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
@@ -175,6 +177,7 @@ def fa_backward_scores(q, k, v, o, lse, do, dq, dk, dv, scale, causal, workspace
                        scores=None, spans=None, stream=None):
     """fa_backward_scores of include/fa.h with the arguments of the forward that gave o and lse;
     writes dq, dk and dv."""
+    q_offset = int32("q_offset", q_offset)
     device, *sizes = _checked(q, k, [("v", v, k), ("o", o, q), ("do", do, q), ("dq", dq, q),
                                      ("dk", dk, k), ("dv", dv, k)], lse, scores, spans)
     if workspace.get_device() != device or not workspace.is_contiguous():
@@ -182,7 +185,7 @@ def fa_backward_scores(q, k, v, o, lse, do, dq, dk, dv, scale, causal, workspace
     status = library().fa_backward_scores(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *sizes, ctypes.c_float(scale),
-        int(bool(causal)), int(q_offset), scores._ref if scores is not None else None,
+        int(bool(causal)), q_offset, scores._ref if scores is not None else None,
         spans._ref if spans is not None else None, workspace.data_ptr(), workspace.nbytes,
         _stream(stream, device))
     if status:
