@@ -12,14 +12,17 @@
 //
 // Everything after Q K^T is in the log2 domain (factors of log2(e) are folded in on
 // the host).  The tanh: for |y| <= 0.4, y = x / softcap, as y P(y^2) with P of degree 3,
-// fitted here for the least largest relative error, 9.8e-8 (2.0e-7 with fp32's roundings).
+// fitted here for the least largest relative error, 9.8e-8; with the roundings of its argument, of
+// cap2 and of the coefficients (4.6 x 2^-24 together) and of the last two steps under 5.2e-7.
 // Its coefficients take in scale / softcap and softcap log2(e) (score_factors), which leaves five
 // operations on the FMA pipe in place of the one that scales a score, where one ex2 and one rcp
 // more for each score would take the special-function unit longer than the weights' own
 // exponentials.  A warp with a score beyond goes by tanh y = 1 - 2 / (e^{2y} + 1), which holds
-// everywhere, to 2e-7 of the cap.  (16 heads of 8192, d = 64, causal: dQ takes 381 us if all go
-// that way.)  Caps of many thousands, whose folded coefficients would leave fp32's range, choose
-// between the two score by score: there 2e-7 of the cap is more than a score.
+// everywhere, to 5.5e-7 of the cap (rcp 2^-23 and the sum's 2^-24 of a quotient up to 2, the
+// exponent's 2^-22 and its argument's 2.1e-7 by what tanh makes of them, half of 1 - tanh^2 and y
+// (1 - tanh^2); 2^-24 at the end and of cap2).  (16 heads of 8192, d = 64, causal: dQ takes 381 us
+// if all go that way.)  Caps of many thousands, whose folded coefficients would leave fp32's range,
+// choose between the two score by score: there 5.5e-7 of the cap is more than a score.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -291,9 +291,13 @@ typedef struct {
 
 /*
  * Forward pass with shaped scores: fa_forward_ex with `spec` and `spans` (either may be NULL).
- * The tanh is off by 2e-7 at most (times softcap in the score).  With a softcap up to 55 and no
- * slopes, sums are held as exp(x) v: a row all of whose scores lie at an end of the cap keeps v
- * whole from 2^-46 to 2^47 / N_kv.  Returns as fa_forward.
+ * Beside the error of q.k, a capped score is off by 6e-7 softcap at most, and by 6e-7 of itself
+ * where all scores lie within 0.4 softcap.  There are two ways to the tanh, and a row's scores go
+ * by the largest beside them, those of other rows and of masked keys included: within that bound
+ * a row's bits depend on its neighbours.  With a softcap up to 55 and no slopes, sums are held as
+ * exp(x) v: a row all of whose scores lie at an end of the cap keeps v whole from 2^-46 to
+ * 2^47 / N_kv.  Distances are fp32: slopes add an error of 2^-22 slope (distance + 128).  Returns
+ * as fa_forward.
  */
 fa_status fa_forward_scores(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                             int H_q, int H_kv, int N_q, int N_kv, int d, float scale, int causal,

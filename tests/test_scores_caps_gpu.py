@@ -118,3 +118,41 @@ def test_rows_at_the_ends_of_the_cap(octave, d, softcap, sign):
     p = at_the_end(d, sign, softcap, 0, [octave])
     p.do = (p.do.float() * 2.0 ** -octave).to(torch.bfloat16)
     p.check()
+
+
+# ------------------------------------------------------------------ how far off a capped score is
+
+OFF = 6e-7  # of softcap, and of the score where all lie within 0.4 softcap (include/fa.h)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+@pytest.mark.parametrize("softcap, scale", [(0.3, 1 / 8), (17.3, 1 / 16), (30.0, 1 / 8),
+                                            (50.0, 1 / 8), (55.0, 1.0), (300.0, 1 / 16),
+                                            (7e3, 1 / 8), (1e5, 1 / 8), (1e9, 1 / 16)])
+def test_capped_scores_are_off_by_as_much_as_stated(softcap, scale, d):
+    """Rows of one key, whose lse is the score: q.k is one product, exact in fp32.  With a slope of
+    0 the reference is the score itself, so lse adds the roundings of ln 2 and of the product with
+    it alone: 2^-23 of the score."""
+    import exact_attention_27_gb300 as fa
+    N = 4096
+    cap, scale = (torch.tensor(x, dtype=torch.float32).item() for x in (softcap, scale))
+    worst = [0.0, 0.0]
+    for far in (0.39, 12.0):  # all within 0.4 caps, and any
+        g = torch.Generator().manual_seed(int(far))
+        q = torch.zeros(1, 1, N, d, dtype=torch.bfloat16)
+        k = torch.zeros(1, 1, N, d, dtype=torch.bfloat16)
+        q[..., 0] = (torch.rand(N, generator=g) * 2 - 1) * far / 1.02
+        k[..., 0] = cap / scale * (1 + 0.01 * torch.rand(N, generator=g))
+        v = torch.zeros_like(k)
+        o, lse = fa.attention_forward(q.cuda(), k.cuda(), v.cuda(), causal=True, scale=scale,
+                                      scores=fa.Scores(softcap, torch.zeros(1).cuda(), window=1))
+        y = q[..., 0].double() * k[..., 0].double() * scale / cap
+        x = cap * torch.tanh(y)
+        err = (lse.cpu().double() - x).abs() - 2.0 ** -23 * x.abs()
+        if far < 0.4:
+            assert y.abs().max() < 0.4
+            worst[0] = (err / x.abs().clamp_min(1e-30)).max().item()
+        else:
+            worst[1] = (err / cap).max().item()
+    print(f"softcap {softcap} scale {scale} d {d}: {worst[0]:.2e} {worst[1]:.2e}")
+    assert max(worst) <= OFF, worst
