@@ -395,7 +395,7 @@ struct PagedSegments {
   Walk w;
   long long unit, end;  // where the item's part of the range begins; the range's end
   int t0, t1, tiles, keys, used;
-  int first;  // first key that the item's rows see (a window's; 0 otherwise)
+  int first;  // SHAPED: first key that the item's rows see (a window's; 0 otherwise)
   __device__ __forceinline__ int tile0() const { return Walk::SHAPED ? first / Walk::TK : 0; }
   __device__ __forceinline__ int weight(const PagedParams& p) const {
     return Walk::weight(p, w.g, w.rt);
@@ -403,7 +403,8 @@ struct PagedSegments {
   __device__ __forceinline__ void load(const PagedParams& p, int at) {
     tiles = Walk::tiles(p, w.g, w.rt);
     keys = Walk::keys(p, w.g, w.rt);
-    first = Walk::first_key(p, w.g, w.rt);
+    // (set to 0 in the unshaped kernels, it costs them 1 %)
+    if constexpr (Walk::SHAPED) first = Walk::first_key(p, w.g, w.rt);
     const int wt = weight(p);
     used = static_cast<int>(
         min(static_cast<long long>((tiles + Walk::OVER) * wt - at), end - unit));
