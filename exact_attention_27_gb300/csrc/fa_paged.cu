@@ -176,9 +176,10 @@ int sm_count() {
 namespace {
 
 fa_status forward_paged(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* q,
-                           long long q_token, long long q_head, void* o, long long o_token,
-                           long long o_head, float* lse, int T, int H_q, float scale, int causal, const fa_score_spec* spec,
-                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+                        long long q_token, long long q_head, void* o, long long o_token,
+                        long long o_head, float* lse, int T, int H_q, float scale, int causal,
+                        const fa_score_spec* spec, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream) {
   const fa_status st = validate_cache(cache, batch, T);
   if (st != FA_OK) return st;
   const int d = cache->d, H = cache->H_kv;

@@ -54,9 +54,9 @@ __global__ void __launch_bounds__(256) fa_scores_sum_kernel(const float4* part, 
 
 // CTAs that share a key tile in the dK/dV kernel: 1, 2, 4 or 8, for which the longest of them
 // and the average SM finish first, in steps of 128 queries by one key tile (about 1.5 us): a
-// CTA's start and end cost some three, and the shares' sums what their bytes take.  Masks that
-// spans bring are not known here: the steps are those of the causal mask, or all.  The whole
-// backward with 1 / 2 / 4 / 8 (us; q and key heads, positions): 16/4, 8192, d = 128, causal: 644
+// CTA's start and end cost some three, and the shares' sums what their bytes take.  Windows and
+// the masks that spans bring are not known here: the steps are those of the causal mask, or all,
+// and no split has been timed under the others.  The whole backward with 1 / 2 / 4 / 8 (us; q and key heads, positions): 16/4, 8192, d = 128, causal: 644
 // / 637 / 683 / 777; 16/4, 4096, d = 64: 227 / 151 / 158 / 182; 8/1, 4096, d = 128, full: 446 / 265 /
 // 181 / 192; 32/32, 2048, d = 128: 131 / 208 / 305 / 477.  The choice loses 6 % to the best of
 // the four on two of ten shapes, and nothing on the others.

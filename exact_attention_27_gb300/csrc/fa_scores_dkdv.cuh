@@ -24,7 +24,7 @@
 //
 // Bound by shared memory and the tensor core: a step's four products read 384 KiB of
 // operands where d = 128, at 128 bytes a cycle, and the rows write P and dS there.  16 heads of
-// 8192, causal: d = 128 363 us (1.51 PFLOP/s), cap 470; d = 64 321, cap 414.
+// 8192, causal: d = 128 363 us (1.51 PFLOP/s), cap 453; d = 64 321, cap 398.
 //
 // Warps: 0-15 query rows (warp w: rows 32 (w % 4).., keys 32 (w / 4)..), 16 TMA, 17 MMA issuer and
 // tensor-memory owner.  Tensor memory: S [0,128), dP [128,256), dV [256, 256+DP), dK after it.

@@ -26,8 +26,8 @@
 //
 // Warps: 0 .. WARPS - 1 query rows (warp w: rows 32 (w % 4).., key columns KH (w / 4)..), then
 // TMA, and MMA issuer and tensor-memory owner.  Bound by issue and the FMA pipe with a cap
-// (60 % and 35 % at 16 heads of 8192, d = 64: 332 us, uncapped 189), by the tensor core otherwise
-// (70 % at d = 128: 264 us, 1.04 PFLOP/s; capped 346).
+// (60 % and 35 % at 16 heads of 8192, d = 64: 320 us, uncapped 189), by the tensor core otherwise
+// (70 % at d = 128: 264 us, 1.04 PFLOP/s; capped 345).
 
 #include <algorithm>
 

@@ -13,10 +13,11 @@ namespace {
 // 2^80.
 constexpr float kFixedCap = 80.0f;
 
-// One query tile a CTA or two: as for the unshaped forward, whose steps cost about the same
-// (forward_rows_for: it estimates when either grid ends).  Masks that spans bring are not
-// known here.  (16 heads of 8192, causal, one / two: d = 64 187 / 152 us, with slopes 241 / 207;
-// d = 96 197 / 170, 259 / 219; d = 128 200 / 225, 276 / 287.)
+// One query tile a CTA or two: as the unshaped forward chooses (forward_rows_for: it estimates
+// when either grid ends, at that kernel's costs).  16 heads of 8192, causal, one / two: d = 64 187 /
+// 152 us, with slopes 241 / 207; d = 96 197 / 170, 259 / 219; d = 128 200 / 225, 276 / 287.  Only
+// that grid was timed.  At d = 128, where one tile is the faster there, and is chosen, larger grids
+// still get two; and neither windows nor the masks that spans bring are known here.
 bool two_tiles(const ScoreParams& s, int d) {
   const int sms = sm_count();
   AttnShape a{s.B, s.Hq, s.Hkv, s.Nq, d, s.scale, s.causal};

@@ -294,10 +294,11 @@ typedef struct {
  * Beside the error of q.k, a capped score is off by 6e-7 softcap at most, and by 6e-7 of itself
  * where all scores lie within 0.4 softcap.  There are two ways to the tanh, and a row's scores go
  * by the largest beside them, those of other rows and of masked keys included: within that bound
- * a row's bits depend on its neighbours.  With a softcap up to 55 and no slopes, sums are held as
+ * a row's bits depend on its neighbours.  Distances are fp32: slopes add an error of 2^-22 slope
+ * (distance + 128).  Weights are rounded to bf16 before they meet V, but not in their sum (2^-8 of
+ * each; a row of one key is its v).  With a softcap up to 55 and no slopes, sums are held as
  * exp(x) v: a row all of whose scores lie at an end of the cap keeps v whole from 2^-46 to
- * 2^47 / N_kv.  Distances are fp32: slopes add an error of 2^-22 slope (distance + 128).  Returns
- * as fa_forward.
+ * 2^47 / N_kv.  Returns as fa_forward.
  */
 fa_status fa_forward_scores(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                             int H_q, int H_kv, int N_q, int N_kv, int d, float scale, int causal,
@@ -309,6 +310,7 @@ fa_status fa_forward_scores(const void* q, const void* k, const void* v, void* o
  *   P = exp(x - L);  dV = P^T dO;  dS = P o (1 - tanh^2) o (dO V^T - D);
  *   dQ = dS K scale;  dK = dS^T Q scale
  * (no 1 - tanh^2 without softcap), dK and dV of a shared head summed over its query heads.
+ * P and dS are rounded to bf16 before they meet dO, K and Q; sums are fp32.
  * One kernel for dK and dV and one for dQ, without atomics: results repeat to the bit.  dq, dk
  * and dv must not alias any input.
  *   workspace  device memory of at least fa_backward_scores_workspace_bytes for the same sizes,
